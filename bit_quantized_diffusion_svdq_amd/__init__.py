@@ -14,12 +14,17 @@ from ._lib import (SvdqError, awq_gemv_w4a16, check_device, library_path, load_l
                    svdq_smooth_weight, svdq_lowrank_workspace_size, svdq_lowrank, svdq_quantize_residual,
                    svdq_quantize_residual_mxfp4, awq_quantize_weight,
                    svdq_pack_lowrank, svdq_gemm_w4a4_quant_next, svdq_gemm_w4a4_quant_next_workspace_size,
-                   w4a4_linear_quant_next, svdq_gemm_mxfp4_quant_next, mxfp4_linear_quant_next)
-from .offline import quantize_awq, quantize_layer
+                   w4a4_linear_quant_next, svdq_gemm_mxfp4_quant_next, mxfp4_linear_quant_next,
+                   svdq_quantize_act_fp8, svdq_quantize_weight_fp8, svdq_gemm_fp8, svdq_gemm_fp8_grouped,
+                   svdq_rope_axes)
+from .fp8 import Fp8GroupedLinear, Fp8Linear, fp8_grouped_linear, fp8_linear, quantize_act_fp8
+from .offline import quantize_awq, quantize_fp8, quantize_layer
 from .fused import column_offsets, column_slice, projection_weights, split_columns
 from .graph import CapturedSequence
-from .block import SvdqLinear, SvdqMLP, awq_linear
-from .package import load_awq_layer, load_layer, read_metadata, save_awq_layer, save_layer
+from .rope import RopePlan, rope_axes
+from .block import FusedQKV, SvdqLinear, SvdqMLP, awq_linear
+from .package import (load_awq_layer, load_fp8_layer, load_layer, read_metadata, save_awq_layer, save_fp8_layer,
+                      save_layer)
 
 __all__ = ["SvdqError", "awq_gemv_w4a16", "check_device", "library_path", "load_library",
            "quantize_act", "svdq_check_device", "svdq_gemm_w4a4", "svdq_gemm_w4a4_partials",

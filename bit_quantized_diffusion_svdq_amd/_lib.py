@@ -56,6 +56,11 @@ _SIGS = {
                                    _P, _P, _I32, _P, _P, _P, _P, _I64, _P],
     "svdq_gemm_w4a4_quant_next_noalloc": [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _I32, _P, _I32,
                                           _P, _P, _I32, _P, _P, _P, _P],
+    "svdq_quantize_act_fp8": [_P, _I64, _I64, _I64, _P, _P, _P],
+    "svdq_quantize_weight_fp8": [_P, _I64, _I64, _I64, _P, _P, _P],
+    "svdq_gemm_fp8": [_P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _I64, _P],
+    "svdq_gemm_fp8_grouped": [_P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _P, _I32, _I64, _P],
+    "svdq_rope_axes": [_P, _P, _I64, _I32, _I32, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P],
 }
 
 
@@ -72,6 +77,13 @@ class LayerSizes(ctypes.Structure):
     """svdq_layer_sizes: byte sizes of a layer's arrays (see include/svdq.h)."""
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("qw", "sw", "l1t", "l2t", "inv_lambda", "bias", "qx_row", "sx_row", "xl1_row")]
+
+
+class RopeHeads(ctypes.Structure):
+    """svdq_rope_heads: the query or the key heads of one svdq_rope_axes call."""
+    _fields_ = [("x", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("norm", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64)]
 
 
 def load_library():
@@ -284,6 +296,35 @@ def svdq_gemm_w4a4_quant_next_noalloc(qx, sx, M, K, qw, sw, N, xl1, l2t, rank, b
         _ptr(qx), _ptr(sx), M, K, _ptr(qw), _ptr(sw), N, _ptr(xl1), _ptr(l2t), rank, _ptr(bias), act,
         _ptr(inv_next), _ptr(l1t_next), rank_next, _ptr(qx_next), _ptr(sx_next), _ptr(xl1_next),
         _stream(stream)), "svdq_gemm_w4a4_quant_next_noalloc")
+
+
+def svdq_quantize_act_fp8(x, M, K, ldx, qx, sx, stream=None):
+    _check(load_library().svdq_quantize_act_fp8(_ptr(x), M, K, ldx, _ptr(qx), _ptr(sx), _stream(stream)),
+           "svdq_quantize_act_fp8")
+
+
+def svdq_quantize_weight_fp8(w, K, N, ldw, qw, sw, stream=None):
+    _check(load_library().svdq_quantize_weight_fp8(_ptr(w), K, N, ldw, _ptr(qw), _ptr(sw), _stream(stream)),
+           "svdq_quantize_weight_fp8")
+
+
+def svdq_gemm_fp8(qx, sx, M, K, qw, sw, N, bias, act, y, y_dtype, ldy, stream=None):
+    _check(load_library().svdq_gemm_fp8(_ptr(qx), _ptr(sx), M, K, _ptr(qw), _ptr(sw), N, _ptr(bias), act, _ptr(y),
+                                        y_dtype, ldy, _stream(stream)), "svdq_gemm_fp8")
+
+
+def svdq_gemm_fp8_grouped(qx, sx, M, K, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, stream=None):
+    _check(load_library().svdq_gemm_fp8_grouped(_ptr(qx), _ptr(sx), M, K, _ptr(qw), _ptr(sw), N, _ptr(offsets), groups,
+                                                _ptr(bias), act, _ptr(y), y_dtype, ldy, _stream(stream)),
+           "svdq_gemm_fp8_grouped")
+
+
+def svdq_rope_axes(q, k, T, D, dtype, pos, pos_dtype, axes, turns, axis, pairs, pairing, inverse, eps, stream=None):
+    """q, k: RopeHeads (k None: queries only)."""
+    _check(load_library().svdq_rope_axes(None if q is None else ctypes.addressof(q),
+                                         None if k is None else ctypes.addressof(k), T, D, dtype, _ptr(pos), pos_dtype,
+                                         axes, _ptr(turns), _ptr(axis), pairs, pairing, inverse, eps, _stream(stream)),
+           "svdq_rope_axes")
 
 
 # ---------------------------------------------------------------- tensor helpers

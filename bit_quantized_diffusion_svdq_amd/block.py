@@ -21,7 +21,9 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
+from .fp8 import Fp8GroupedLinear
 from .graph import CapturedSequence
+from .rope import RopePlan, rope_axes
 
 
 @dataclass
@@ -138,3 +140,39 @@ class SvdqMLP:
             self._load(x)
         self.graph.replay()
         return self.y
+
+
+class FusedQKV:
+    """An attention block's input side: the fused [Q | K | V] projection (an
+    ``SvdqLinear``, ``Fp8Linear`` or ``Fp8GroupedLinear``; fused.py gives the
+    column order), then the head norms and the rotary positions, in place in
+    the projection's bf16 output. ``heads`` query heads and ``kv_heads`` key
+    and value heads of plan.head_dim channels. Calls give (q, k, v), views
+    [M, heads, head_dim] of one buffer: a projection and one more launch."""
+
+    def __init__(self, layer, plan: RopePlan, heads: int, kv_heads: int | None = None, q_norm=None, k_norm=None,
+                 eps: float = 1e-6):
+        kv_heads = heads if kv_heads is None else kv_heads
+        _lib._require(heads >= 1 and kv_heads >= 1, f"heads must be positive, got {heads} and {kv_heads}")
+        D = plan.head_dim
+        _lib._require(layer.N == (heads + 2 * kv_heads) * D,
+                      f"the layer has {layer.N} outputs, {heads} query and 2 x {kv_heads} key and value heads of {D} "
+                      f"need {(heads + 2 * kv_heads) * D}")
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            _lib._require(w is None or (tuple(w.shape) == (D,) and w.dtype == torch.bfloat16),
+                          f"{name} must be a bf16 vector of {D} values")
+        self.layer, self.plan, self.heads, self.kv_heads = layer, plan, heads, kv_heads
+        self.q_norm, self.k_norm, self.eps = q_norm, k_norm, eps
+
+    def __call__(self, x: torch.Tensor, pos: torch.Tensor, offsets=None, y=None, stream=None):
+        """x bf16 [M, K], pos [M, axes]; offsets for a grouped layer (rows
+        sorted by stream); y: the buffer for the projection, bf16 [M, N]."""
+        grouped = isinstance(self.layer, Fp8GroupedLinear)
+        _lib._require(grouped == (offsets is not None), "offsets belong to a grouped layer, and it needs them")
+        y = self.layer(x, offsets, y=y, stream=stream) if grouped else self.layer(x, y=y, stream=stream)
+        _lib._require(y.dtype == torch.bfloat16, f"y must be bf16, got {y.dtype}")
+        M, D = y.shape[0], self.plan.head_dim
+        h = y.unflatten(1, (self.heads + 2 * self.kv_heads, D))
+        q, k, v = h.split((self.heads, self.kv_heads, self.kv_heads), dim=1)
+        rope_axes(q, k, pos, self.plan, self.q_norm, self.k_norm, self.eps, q_out=q, k_out=k, stream=stream)
+        return q, k, v

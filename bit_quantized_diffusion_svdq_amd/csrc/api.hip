@@ -10,6 +10,7 @@
 #include <string>
 
 #include "../../include/svdq.h"
+#include "rope.h"
 
 hipError_t launch_act_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ldx,
                             const float* inv_lambda, const uint16_t* l1t, int rank,
@@ -53,6 +54,13 @@ hipError_t launch_awq_quantize(const uint16_t* w, int64_t K, int64_t N, int64_t 
 hipError_t launch_pack_lowrank(const uint16_t* l1, const uint16_t* l2, int64_t K, int64_t N, int r, uint16_t* l1t,
                                uint16_t* l2t, hipStream_t stream);
 int64_t gemm_next_partial_bytes(int64_t M, int64_t N, int rank_next);
+hipError_t launch_quant_act_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, uint8_t* qx, float* sx, int cus,
+                                hipStream_t stream);
+hipError_t launch_quant_weight_fp8(const uint16_t* w, int64_t K, int64_t N, int64_t ldw, uint8_t* qw, float* sw,
+                                   hipStream_t stream);
+hipError_t launch_gemm_fp8(const uint8_t* qx, const float* sx, int64_t M, int64_t K, const uint8_t* qw, const float* sw,
+                           int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
+                           int64_t ldy, int cus, hipStream_t stream);
 hipError_t launch_gemm_w4a4_next(const uint8_t* qx, const uint16_t* sx, const uint8_t* qw,
                                  const uint16_t* sw, const float* xl1, const uint16_t* l2t, int rank,
                                  const uint16_t* bias, int act, int64_t M, int64_t N, int64_t K,
@@ -734,3 +742,179 @@ svdq_status svdq_gemm_w4a4_quant_next_noalloc(const uint8_t* qx, const void* sx_
     return svdq_gemm_w4a4_quant_next(qx, sx_f16, M, K, qw, sw_f16, N, xl1, l2t, rank, bias, act, inv_lambda_next,
                                      l1t_next, rank_next, qx_next, sx_next_f16, xl1_next, ws, need, stream);
 }
+
+/* ------------------------------------------------------------------------ */
+/* 8-bit layers                                                              */
+
+namespace {
+
+svdq_status check_k_fp8(int64_t K) {
+    if (K <= 0 || K % 16) return fail(SVDQ_ERR_SHAPE, "K = %lld must be a positive multiple of 16", (long long)K);
+    if (K >= (int64_t)1 << 22) return fail(SVDQ_ERR_SHAPE, "K = %lld must be below 2^22", (long long)K);
+    return SVDQ_OK;
+}
+
+svdq_status gemm_fp8_impl(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
+                          int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act, void* y,
+                          int32_t y_dtype, int64_t ldy, void* stream, const char* what) {
+    svdq_status s;
+    if (M < 0 || M >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "M = %lld must be in [0, 2^31)", (long long)M);
+    if ((s = check_k_fp8(K)) != SVDQ_OK) return s;
+    if (N <= 0 || N >= (int64_t)1 << 30) return fail(SVDQ_ERR_SHAPE, "N = %lld must be in [1, 2^30)", (long long)N);
+    if (groups < 0 || groups > 65536) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
+    if (ldy < N) return fail(SVDQ_ERR_SHAPE, "ldy = %lld < N = %lld", (long long)ldy, (long long)N);
+    if (ldy >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "ldy = %lld must be below 2^31", (long long)ldy);
+    if ((s = check_act(act)) != SVDQ_OK) return s;
+    if (y_dtype != SVDQ_DT_BF16 && y_dtype != SVDQ_DT_F32)
+        return fail(SVDQ_ERR_UNSUPPORTED, "output dtype %d is not supported", y_dtype);
+    // the smallest tile is 16 x 16 with 512 lanes: 2^32 lanes a launch
+    if ((M / 16 + 1 + groups) * (N / 16 + 1) >= ((int64_t)1 << 23) &&
+        (M / 64 + 1 + groups) * (N / 64 + 1) >= ((int64_t)1 << 23))
+        return fail(SVDQ_ERR_SHAPE, "M = %lld x N = %lld needs more tiles than one launch holds", (long long)M, (long long)N);
+    if (M == 0) { g_last_error.clear(); return SVDQ_OK; }
+    if (!qx || !sx || !qw || !sw || !y || (groups && !offsets))
+        return fail(SVDQ_ERR_NULL, "qx, sx, qw, sw and y%s are required", groups ? ", offsets" : "");
+    if (!aligned(qx, 16) || !aligned(qw, 16) || !aligned(sx, 4) || !aligned(sw, 4) || (bias && !aligned(bias, 2)) ||
+        !aligned(y, y_dtype == SVDQ_DT_F32 ? 4 : 2) || (offsets && !aligned(offsets, 4)))
+        return fail(SVDQ_ERR_ALIGN, "qx, qw need 16-byte alignment, sx, sw, offsets 4, bias 2, y its element's");
+    int cus = 0;
+    if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
+    return launched(launch_gemm_fp8((const uint8_t*)qx, sx, M, K, (const uint8_t*)qw, sw, N, offsets, groups,
+                                    (const uint16_t*)bias, act, y, y_dtype == SVDQ_DT_F32, ldy, cus,
+                                    (hipStream_t)stream),
+                    what);
+}
+
+svdq_status check_rope_heads(const svdq_rope_heads* h, const char* name, int min_heads, int64_t T, int64_t D) {
+    if (h->heads < min_heads || h->heads > 65536)
+        return fail(SVDQ_ERR_SHAPE, "%s: %d heads must be in [%d, 65536]", name, h->heads, min_heads);
+    const int64_t st[4] = {h->token_stride, h->head_stride, h->y_token_stride, h->y_head_stride};
+    for (int64_t v : st) {
+        if (v < 0 || v >= ((int64_t)1 << 40)) return fail(SVDQ_ERR_SHAPE, "%s: stride %lld is out of range", name, (long long)v);
+        if (v % 8) return fail(SVDQ_ERR_ALIGN, "%s: stride %lld must be a multiple of 8", name, (long long)v);
+    }
+    if (T == 0 || h->heads == 0) return SVDQ_OK;
+    // outputs must not overlap: tokens inside heads or heads inside tokens
+    const int64_t ts = h->y_token_stride, hs = h->y_head_stride, last_h = h->heads - 1, last_t = T - 1;
+    const bool token_major = (last_h == 0 || hs >= D) && (last_t == 0 || ts >= last_h * hs + D);
+    const bool head_major = (last_t == 0 || ts >= D) && (last_h == 0 || hs >= last_t * ts + D);
+    if (!token_major && !head_major)
+        return fail(SVDQ_ERR_SHAPE, "%s: output strides %lld (token), %lld (head) overlap", name, (long long)ts, (long long)hs);
+    if (!h->x || !h->y) return fail(SVDQ_ERR_NULL, "%s: x and y are required", name);
+    if (!aligned(h->x, 16) || !aligned(h->y, 16) || (h->norm && !aligned(h->norm, 16)))
+        return fail(SVDQ_ERR_ALIGN, "%s: x, y and norm need 16-byte alignment", name);
+    return SVDQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+svdq_status svdq_quantize_act_fp8(const void* x, int64_t M, int64_t K, int64_t ldx, void* qx, float* sx,
+                                  void* stream) {
+    svdq_status s;
+    if (M < 0) return fail(SVDQ_ERR_SHAPE, "M = %lld is negative", (long long)M);
+    if ((s = check_k_fp8(K)) != SVDQ_OK) return s;
+    if (ldx < K) return fail(SVDQ_ERR_SHAPE, "ldx = %lld < K = %lld", (long long)ldx, (long long)K);
+    if (ldx % 8) return fail(SVDQ_ERR_ALIGN, "ldx = %lld must be a multiple of 8", (long long)ldx);
+    // one row and four blocks a wave at the least, 2^32 lanes a launch
+    if ((M / 4 + 1) * ((K + 511) / 512) >= ((int64_t)1 << 25))
+        return fail(SVDQ_ERR_SHAPE, "M = %lld x K = %lld needs more waves than one launch holds", (long long)M, (long long)K);
+    if (M == 0) { g_last_error.clear(); return SVDQ_OK; }
+    if (!x || !qx || !sx) return fail(SVDQ_ERR_NULL, "x, qx and sx are required");
+    if (!aligned(x, 16) || !aligned(qx, 16) || !aligned(sx, 4))
+        return fail(SVDQ_ERR_ALIGN, "x, qx need 16-byte alignment, sx 4");
+    int cus = 0;
+    if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
+    return launched(launch_quant_act_fp8((const uint16_t*)x, M, K, ldx, (uint8_t*)qx, sx, cus, (hipStream_t)stream),
+                    "svdq_quantize_act_fp8 launch");
+}
+
+svdq_status svdq_quantize_weight_fp8(const void* w, int64_t K, int64_t N, int64_t ldw, void* qw, float* sw,
+                                     void* stream) {
+    svdq_status s;
+    if ((s = check_k_fp8(K)) != SVDQ_OK) return s;
+    if (N <= 0 || N > (int64_t)65535 * 128) return fail(SVDQ_ERR_SHAPE, "N = %lld must be in [1, 65535 * 128]", (long long)N);
+    if (ldw < N) return fail(SVDQ_ERR_SHAPE, "ldw = %lld < N = %lld", (long long)ldw, (long long)N);
+    if (ldw % 8) return fail(SVDQ_ERR_ALIGN, "ldw = %lld must be a multiple of 8", (long long)ldw);
+    if (!w || !qw || !sw) return fail(SVDQ_ERR_NULL, "w, qw and sw are required");
+    if (!aligned(w, 16) || !aligned(qw, 16) || !aligned(sw, 4))
+        return fail(SVDQ_ERR_ALIGN, "w, qw need 16-byte alignment, sw 4");
+    if ((s = check_current_device()) != SVDQ_OK) return s;
+    return launched(launch_quant_weight_fp8((const uint16_t*)w, K, N, ldw, (uint8_t*)qw, sw, (hipStream_t)stream),
+                    "svdq_quantize_weight_fp8 launch");
+}
+
+svdq_status svdq_gemm_fp8(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
+                          int64_t N, const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
+                          void* stream) {
+    return gemm_fp8_impl(qx, sx, M, K, qw, sw, N, nullptr, 0, bias, act, y, y_dtype, ldy, stream,
+                         "svdq_gemm_fp8 launch");
+}
+
+svdq_status svdq_gemm_fp8_grouped(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw,
+                                  const float* sw, int64_t N, const int32_t* offsets, int32_t groups,
+                                  const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
+                                  void* stream) {
+    if (groups < 1) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
+    return gemm_fp8_impl(qx, sx, M, K, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, stream,
+                         "svdq_gemm_fp8_grouped launch");
+}
+
+svdq_status svdq_rope_axes(const svdq_rope_heads* q, const svdq_rope_heads* k, int64_t T, int32_t D, int32_t dtype,
+                           const void* pos, int32_t pos_dtype, int32_t axes, const double* turns,
+                           const int32_t* axis, int32_t pairs, int32_t pairing, int32_t inverse, float eps,
+                           void* stream) {
+    svdq_status s;
+    if (!q) return fail(SVDQ_ERR_NULL, "q is required");
+    if (T < 0 || T >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "T = %lld must be in [0, 2^31)", (long long)T);
+    if (D < 8 || D > 512 || D % 8) return fail(SVDQ_ERR_SHAPE, "D = %d must be a multiple of 8 in [8, 512]", D);
+    if (pairs < 0 || pairs % 4 || 2 * (int64_t)pairs > D)
+        return fail(SVDQ_ERR_SHAPE, "pairs = %d must be a multiple of 4 with 2 * pairs <= D = %d", pairs, D);
+    if (axes < 1 || axes > 8) return fail(SVDQ_ERR_SHAPE, "axes = %d must be in [1, 8]", axes);
+    if (dtype != SVDQ_DT_BF16 && dtype != SVDQ_DT_F32) return fail(SVDQ_ERR_UNSUPPORTED, "dtype %d is not supported", dtype);
+    if (pos_dtype != SVDQ_POS_I32 && pos_dtype != SVDQ_POS_F32)
+        return fail(SVDQ_ERR_UNSUPPORTED, "position dtype %d is not supported", pos_dtype);
+    if (pairing != SVDQ_PAIRS_INTERLEAVED && pairing != SVDQ_PAIRS_HALF)
+        return fail(SVDQ_ERR_UNSUPPORTED, "pairing %d is not supported", pairing);
+    if (inverse != 0 && inverse != 1) return fail(SVDQ_ERR_UNSUPPORTED, "inverse must be 0 or 1");
+    if (!(eps >= 0.0f)) return fail(SVDQ_ERR_UNSUPPORTED, "eps must be >= 0");
+    if ((s = check_rope_heads(q, "q", 1, T, D)) != SVDQ_OK) return s;
+    if (k && (s = check_rope_heads(k, "k", 0, T, D)) != SVDQ_OK) return s;
+    const int64_t heads = (int64_t)q->heads + (k ? k->heads : 0);
+    if (T * ((heads * D + 511) / 512 + 1) >= ((int64_t)1 << 26))
+        return fail(SVDQ_ERR_SHAPE, "T = %lld with %lld heads needs more waves than one launch holds", (long long)T, (long long)heads);
+    if (T == 0) { g_last_error.clear(); return SVDQ_OK; }
+    if (pairs > 0 && (!pos || !turns || !axis)) return fail(SVDQ_ERR_NULL, "pos, turns and axis are required");
+    if (pairs > 0 && (!aligned(pos, 4) || !aligned(turns, 8) || !aligned(axis, 4)))
+        return fail(SVDQ_ERR_ALIGN, "pos, axis need 4-byte alignment, turns 8");
+    int cus = 0;
+    if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
+    RopeArgs a = {};
+    const svdq_rope_heads* side[2] = {q, k};
+    for (int i = 0; i < 2; ++i) {
+        if (!side[i]) continue;
+        a.x[i] = side[i]->x;
+        a.y[i] = side[i]->y;
+        a.norm[i] = side[i]->norm;
+        a.ts[i] = side[i]->token_stride;
+        a.hs[i] = side[i]->head_stride;
+        a.yts[i] = side[i]->y_token_stride;
+        a.yhs[i] = side[i]->y_head_stride;
+        a.heads[i] = side[i]->heads;
+    }
+    a.pos = pos;
+    a.turns = turns;
+    a.axis = axis;
+    a.T = T;
+    a.D = D;
+    a.pairs = pairs;
+    a.axes = axes;
+    a.pos_f32 = pos_dtype == SVDQ_POS_F32;
+    a.inverse = inverse;
+    a.eps = eps;
+    return launched(launch_rope_axes(a, dtype == SVDQ_DT_F32, pairing == SVDQ_PAIRS_HALF, cus, (hipStream_t)stream),
+                    "svdq_rope_axes launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,190 @@
+"""8-bit layers: E4M3 weights and activations with an fp32 scale per block of
+128 (weights 128 x 128, activations 128 channels of a row), dense and grouped.
+
+For the projections that 4 bits hurt: the donmalab.com page (section on the
+two schemes) keeps precision-sensitive projections out of the 4-bit path, and
+the remio.ai page (section on the loading path) names a scheme per module.
+``Fp8Linear`` stands beside ``SvdqLinear``; ``Fp8GroupedLinear`` holds several
+weights of one shape, and the rows of a batch, sorted by group, each meet
+their group's (the experts of a mixture, or the text and image streams of a
+joint block in one launch).
+
+Marshalling only: the arithmetic is the library's. Tensors may live on any
+GPU; a call runs on that GPU's current stream unless ``stream`` is given, and
+allocates its outputs with torch.
+"""
+from __future__ import annotations
+
+import contextlib
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+from ._lib import _check_rows, _check_same_device, _require
+
+BLOCK = 128
+E4M3 = torch.float8_e4m3fn
+
+
+def blocks(n: int) -> int:
+    """Blocks of 128 that cover n channels."""
+    return (n + BLOCK - 1) // BLOCK
+
+
+def _on(t: torch.Tensor):
+    """The tensor's GPU made current, if it is not."""
+    if t.device.index in (None, torch.cuda.current_device()):
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def quantize_act_fp8(x: torch.Tensor, stream=None):
+    """x: bf16 [M, K] on the GPU (K a multiple of 16; rows may be strided, the
+    row stride a multiple of 8) -> (qx E4M3 [M, K], sx fp32 [ceil(K/128), M]):
+    per row and 128 channels s = max(amax / 448, 2^-120), code = e4m3(x / s)
+    (include/svdq.h gives every rounding)."""
+    _check_rows(x, "x", torch.bfloat16)
+    M, K = x.shape
+    _require(K >= 16 and K % 16 == 0, f"x must have K a positive multiple of 16, got {K}")
+    _check_same_device(x)
+    ldx = x.stride(0) if M > 1 else K
+    if ldx < K or ldx % 8:                      # a broadcast or unaligned row stride
+        x, ldx = x.contiguous(), K
+    with _on(x):
+        qx = torch.empty((M, K), dtype=E4M3, device=x.device)
+        sx = torch.empty((blocks(K), M), dtype=torch.float32, device=x.device)
+        _lib.svdq_quantize_act_fp8(x, M, K, ldx, qx, sx, stream)
+    return qx, sx
+
+
+def _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, groups):
+    """Argument checks of the dense (groups 0) and the grouped product; -> M, K, N, y's dtype."""
+    _check_rows(qx, "qx", E4M3)
+    _require(qx.is_contiguous(), "qx must be contiguous [M, K]")
+    M, K = qx.shape
+    _require(K >= 16 and K % 16 == 0, f"qx must have K a positive multiple of 16, got {K}")
+    lead = (groups,) if groups else ()
+    _require(qw.dim() == 2 + len(lead) and qw.dtype == E4M3 and qw.is_contiguous() and qw.shape[-1] == K,
+             f"qw must be contiguous E4M3 {[*lead, 'N', K]}, got {tuple(qw.shape)} {qw.dtype}")
+    N = qw.shape[-2]
+    _require(N >= 1, "qw must have at least one output row")
+    _require(tuple(sx.shape) == (blocks(K), M) and sx.dtype == torch.float32
+             and (sx.is_contiguous() or sx.numel() <= 1),
+             f"sx must be contiguous fp32 [{blocks(K)}, {M}], got {tuple(sx.shape)} {sx.dtype}")
+    want = (*lead, blocks(N), blocks(K))
+    _require(tuple(sw.shape) == want and sw.dtype == torch.float32 and sw.is_contiguous(),
+             f"sw must be contiguous fp32 {list(want)}, got {tuple(sw.shape)} {sw.dtype}")
+    if bias is not None:
+        _require(tuple(bias.shape) == (*lead, N) and bias.dtype == torch.bfloat16 and bias.is_contiguous(),
+                 f"bias must be contiguous bf16 {[*lead, N]}, got {tuple(bias.shape)} {bias.dtype}")
+    _require(act in _lib.ACT, f"act must be one of {sorted(_lib.ACT)}, got {act!r}")
+    if y is not None:
+        out_dtype = y.dtype
+        _require(y.dim() == 2 and tuple(y.shape) == (M, N) and (y.stride(1) == 1 or N == 1)
+                 and (y.stride(0) >= N or M <= 1),
+                 f"y must be [{M}, {N}] with contiguous columns and rows that do not overlap")
+    _require(out_dtype in (torch.bfloat16, torch.float32), f"y must be bf16 or fp32, got {out_dtype}")
+    _check_same_device(qx, sx=sx, qw=qw, sw=sw, bias=bias, y=y)
+    return M, K, N, out_dtype
+
+
+def _row_stride(y, N):
+    return y.stride(0) if y.shape[0] > 1 else N
+
+
+def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfloat16, y=None, stream=None):
+    """act(sum_b sx sw P_b + bias) for already quantised activations: qx E4M3
+    [M, K], sx fp32 [ceil(K/128), M] (quantize_act_fp8), qw E4M3 [N, K], sw
+    fp32 [ceil(N/128), ceil(K/128)], bias bf16 [N] or None -> y [M, N] (bf16
+    or fp32; rows of a given y may be strided)."""
+    M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, 0)
+    with _on(qx):
+        if y is None:
+            y = torch.empty((M, N), dtype=out_dtype, device=qx.device)
+        _lib.svdq_gemm_fp8(qx, sx, M, K, qw, sw, N, bias, _lib.ACT[act], y, int(out_dtype == torch.float32),
+                           _row_stride(y, N), stream)
+    return y
+
+
+def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfloat16, y=None,
+                       stream=None):
+    """fp8_linear with a weight per group: rows offsets[g] .. offsets[g + 1] - 1
+    of qx meet qw[g] [N, K], sw[g], bias[g]. offsets: int32 [groups + 1] on
+    the GPU, rising, within [0, M] (read there: no synchronisation). Rows of
+    no group (before offsets[0], from offsets[-1] on) are left as they are in
+    a given y and are unspecified in a new one."""
+    _require(offsets.dim() == 1 and offsets.numel() >= 2 and offsets.dtype == torch.int32 and offsets.is_contiguous(),
+             f"offsets must be a contiguous int32 vector of groups + 1 values, got {tuple(offsets.shape)} {offsets.dtype}")
+    groups = offsets.numel() - 1
+    M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, groups)
+    _check_same_device(qx, offsets=offsets)
+    with _on(qx):
+        if y is None:
+            y = torch.empty((M, N), dtype=out_dtype, device=qx.device)
+        _lib.svdq_gemm_fp8_grouped(qx, sx, M, K, qw, sw, N, offsets, groups, bias, _lib.ACT[act], y,
+                                   int(out_dtype == torch.float32), _row_stride(y, N), stream)
+    return y
+
+
+@dataclass
+class Fp8Linear:
+    """One 8-bit layer's device arrays."""
+    qw: torch.Tensor                # E4M3 [N, K]
+    sw: torch.Tensor                # fp32 [ceil(N/128), ceil(K/128)]
+    bias: torch.Tensor | None = None  # bf16 [N]
+
+    @property
+    def K(self) -> int:
+        return self.qw.shape[-1]
+
+    @property
+    def N(self) -> int:
+        return self.qw.shape[-2]
+
+    @classmethod
+    def from_quantized(cls, d: dict) -> "Fp8Linear":
+        """From the dict quantize_fp8() returns."""
+        return cls(d["qw"], d["sw"], d.get("bias"))
+
+    def __call__(self, x: torch.Tensor, act: str = "none", out_dtype=torch.bfloat16, y=None,
+                 stream=None) -> torch.Tensor:
+        """Y [M, N] for bf16 activations x [M, K]: the activation pass, then
+        the product, on one stream."""
+        _require(x.dim() == 2 and x.shape[1] == self.K, f"x must be [M, {self.K}], got {tuple(x.shape)}")
+        qx, sx = quantize_act_fp8(x, stream)
+        return fp8_linear(qx, sx, self.qw, self.sw, self.bias, act, out_dtype, y, stream)
+
+
+@dataclass
+class Fp8GroupedLinear:
+    """Weights of one shape for several groups of rows."""
+    qw: torch.Tensor                # E4M3 [groups, N, K]
+    sw: torch.Tensor                # fp32 [groups, ceil(N/128), ceil(K/128)]
+    bias: torch.Tensor | None = None  # bf16 [groups, N]
+
+    @property
+    def groups(self) -> int:
+        return self.qw.shape[0]
+
+    @property
+    def K(self) -> int:
+        return self.qw.shape[-1]
+
+    @property
+    def N(self) -> int:
+        return self.qw.shape[-2]
+
+    @classmethod
+    def from_quantized(cls, d: dict) -> "Fp8GroupedLinear":
+        """From the dict quantize_fp8() returns for a weight [groups, K, N]."""
+        return cls(d["qw"], d["sw"], d.get("bias"))
+
+    def __call__(self, x: torch.Tensor, offsets: torch.Tensor, act: str = "none", out_dtype=torch.bfloat16, y=None,
+                 stream=None) -> torch.Tensor:
+        """Y [M, N] for bf16 activations x [M, K] sorted by group
+        (fp8_grouped_linear's offsets)."""
+        _require(x.dim() == 2 and x.shape[1] == self.K, f"x must be [M, {self.K}], got {tuple(x.shape)}")
+        _require(offsets.numel() == self.groups + 1, f"offsets must hold {self.groups + 1} values")
+        qx, sx = quantize_act_fp8(x, stream)
+        return fp8_grouped_linear(qx, sx, offsets, self.qw, self.sw, self.bias, act, out_dtype, y, stream)

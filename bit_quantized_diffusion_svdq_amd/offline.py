@@ -123,3 +123,37 @@ def quantize_awq(w: torch.Tensor, inv_s=None, stream=None) -> dict:
     zero_t = torch.empty(N * K // 64, dtype=torch.float16, device=dev)
     _lib.awq_quantize_weight(w, K, N, w.stride(0), inv_s, qwt, scale_t, zero_t, stream)
     return dict(qwt=qwt, scale_t=scale_t, zero_t=zero_t, inv_s=inv_s, K=K, N=N)
+
+
+def quantize_fp8(w: torch.Tensor, bias=None, stream=None) -> dict:
+    """The 8-bit weight quantisation on the GPU: w bf16 [K, N], or [groups, K,
+    N] for a grouped layer (K a multiple of 16, columns contiguous, the row
+    stride a multiple of 8); bias bf16 [N] or [groups, N]. Returns qw E4M3
+    [N, K], sw fp32 [ceil(N/128), ceil(K/128)] (both with a leading group
+    axis for a grouped layer), bias, K, N: an Fp8Linear or Fp8GroupedLinear's
+    arrays."""
+    from .fp8 import E4M3, _on, blocks
+
+    _lib._require(w.dim() in (2, 3), f"w must be [K, N] or [groups, K, N], got shape {tuple(w.shape)}")
+    ws = [w] if w.dim() == 2 else list(w)
+    _lib._require(len(ws) >= 1, "w must hold at least one group")
+    K, N = w.shape[-2:]
+    _lib._require(K >= 16 and K % 16 == 0 and N >= 1, f"w must have K a positive multiple of 16 and N >= 1, got {(K, N)}")
+    lead = tuple(w.shape[:-2])
+    if bias is not None:
+        _lib._require(tuple(bias.shape) == (*lead, N) and bias.dtype == torch.bfloat16,
+                      f"bias must be bf16 {[*lead, N]}, got {tuple(bias.shape)} {bias.dtype}")
+    for wg in ws:
+        _lib._check_rows(wg, "w", torch.bfloat16)
+    _lib._check_same_device(w, bias=bias)
+    with _on(w):
+        qw = torch.empty((*lead, N, K), dtype=E4M3, device=w.device)
+        sw = torch.empty((*lead, blocks(N), blocks(K)), dtype=torch.float32, device=w.device)
+        for g, wg in enumerate(ws):
+            ldw = wg.stride(0)
+            if ldw < N or ldw % 8 or wg.data_ptr() % 16:         # a stride or an address the kernel cannot read
+                pad = torch.zeros((K, (N + 7) // 8 * 8), dtype=torch.bfloat16, device=w.device)
+                pad[:, :N].copy_(wg)
+                wg, ldw = pad, pad.stride(0)
+            _lib.svdq_quantize_weight_fp8(wg, K, N, ldw, qw[g] if lead else qw, sw[g] if lead else sw, stream)
+    return dict(qw=qw, sw=sw, bias=bias, K=K, N=N)

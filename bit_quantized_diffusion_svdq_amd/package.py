@@ -30,6 +30,7 @@ import torch
 
 from . import _lib
 from .block import SvdqLinear
+from .fp8 import Fp8GroupedLinear, Fp8Linear, blocks
 
 FORMAT_NAME = "svdq-layer"
 FORMAT_VERSION = 1
@@ -254,3 +255,80 @@ def load_awq_layer(path: str, device="cuda") -> dict:
     out.setdefault("bias", None)
     out.update(K=K, N=N)
     return out
+
+
+# ---------------------------------------------------------------- 8-bit layers
+
+FP8_FORMAT_NAME = "fp8-block-layer"
+_FP8_SPECS = {
+    "qw": (torch.float8_e4m3fn, "E4M3 codes [groups][N][K] (no group axis in a dense layer)"),
+    "sw": (torch.float32, "scales fp32 [groups][ceil(N/128)][ceil(K/128)]"),
+    "bias": (torch.bfloat16, "bias bf16 [groups][N]"),
+}
+
+
+def _fp8_shapes(K: int, N: int, groups: int) -> dict:
+    if K < 16 or K % 16 or N < 1 or groups < 0:
+        raise ValueError(f"8-bit layer needs K a positive multiple of 16 and N >= 1, got K {K}, N {N}, groups {groups}")
+    lead = (groups,) if groups else ()
+    return {"qw": (*lead, N, K), "sw": (*lead, blocks(N), blocks(K)), "bias": (*lead, N)}
+
+
+def _check_fp8_array(where: str, name: str, t: torch.Tensor, shapes: dict):
+    dtype, _ = _FP8_SPECS[name]
+    if t.dtype != dtype or tuple(t.shape) != shapes[name]:
+        raise ValueError(f"{where}{name}: expected {dtype} {shapes[name]}, got {t.dtype} {tuple(t.shape)}")
+
+
+def save_fp8_layer(path: str, layer, **provenance) -> dict:
+    """Write an ``Fp8Linear`` or ``Fp8GroupedLinear`` with its metadata
+    record. Returns the record."""
+    from safetensors.torch import save_file
+
+    groups = layer.groups if isinstance(layer, Fp8GroupedLinear) else 0
+    shapes = _fp8_shapes(layer.K, layer.N, groups)
+    tensors = {}
+    for name in _FP8_SPECS:
+        t = getattr(layer, name)
+        if t is None and name == "bias":
+            continue
+        _check_fp8_array("", name, t, shapes)
+        tensors[name] = t.detach().to("cpu").contiguous()
+    meta = {
+        "format": FP8_FORMAT_NAME, "format_version": str(FORMAT_VERSION),
+        "library_version": str(_library_version()), "K": str(layer.K), "N": str(layer.N), "group": "128",
+        "groups": str(groups), "layouts": json.dumps({n: _FP8_SPECS[n][1] for n in tensors}),
+        "provenance": json.dumps(provenance, sort_keys=True),
+    }
+    save_file(tensors, path, metadata=meta)
+    return meta
+
+
+def load_fp8_layer(path: str, device="cuda"):
+    """Read a packaged 8-bit layer, check it, and return it (an ``Fp8Linear``,
+    or an ``Fp8GroupedLinear`` if it has groups) on ``device``."""
+    from safetensors.torch import load_file
+
+    meta = read_metadata(path)
+    if meta.get("format") != FP8_FORMAT_NAME:
+        raise ValueError(f"{path}: format {meta.get('format')!r} is not {FP8_FORMAT_NAME!r}")
+    if _int_field(meta, "format_version") != FORMAT_VERSION:
+        raise ValueError(f"{path}: format version {meta['format_version']} is not {FORMAT_VERSION}")
+    if _int_field(meta, "group") != 128:
+        raise ValueError(f"{path}: group {meta['group']} is not 128")
+    K, N, groups = (_int_field(meta, k) for k in ("K", "N", "groups"))
+    try:
+        shapes = _fp8_shapes(K, N, groups)
+    except ValueError as e:
+        raise ValueError(f"{path}: malformed layer record ({e})") from None
+    tensors = load_file(path, device="cpu")
+    for name in ("qw", "sw"):
+        if name not in tensors:
+            raise ValueError(f"{path}: array {name!r} is missing")
+    for name, t in tensors.items():
+        if name not in _FP8_SPECS:
+            raise ValueError(f"{path}: unexpected array {name!r}")
+        _check_fp8_array(f"{path}: ", name, t, shapes)
+    dev = torch.device(device)
+    t = {k: v.to(dev) for k, v in tensors.items()}
+    return (Fp8GroupedLinear if groups else Fp8Linear)(t["qw"], t["sw"], t.get("bias"))

@@ -501,6 +501,113 @@ svdq_status awq_quantize_weight(const void* w_bf16, int64_t K, int64_t N, int64_
 svdq_status svdq_pack_lowrank(const void* l1, const void* l2, int64_t K, int64_t N, int32_t rank, void* l1t,
                               void* l2t, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit layers: E4M3 (OCP FP8: 1 sign, 4 exponent, 3 mantissa bits, largest
+ * value 448) weights and activations with one fp32 scale per block of 128
+ * input channels, for the projections that 4 bits hurt (the donmalab.com
+ * page, section on the two schemes, keeps precision-sensitive projections
+ * out of the 4-bit path). A layer is
+ *
+ *     Y[m, n] = act( sum_b sx[b, m] sw[n / 128, b] P_b[m, n] + bias[n] )
+ *     P_b[m, n] = sum_{k in block b} qx[m, k] qw[n, k]
+ *
+ * Layouts: qx [M][K] and qw [N][K] E4M3 bytes, dense rows, K a positive
+ * multiple of 16 (a last block may be short); sx fp32 [ceil(K/128)][M]
+ * (block-major: the rows of one block are contiguous); sw fp32
+ * [ceil(N/128)][ceil(K/128)], one scale per 128 x 128 block of the weight.
+ *
+ * svdq_quantize_act_fp8: x bf16 [M][ldx] (K <= ldx, ldx % 8 == 0, 16-byte
+ * aligned) -> qx (16-byte aligned), sx. Per (row, block): amax = max |x| over
+ * the finite values; s = max(fp32(amax / 448), 2^-120); code =
+ * e4m3(clamp(fp32(x * fp32(1 / s)), -448, 448)), to nearest, ties to even.
+ * Bit-exact with that definition. An infinity saturates at +-448 s, a NaN
+ * keeps a NaN code; neither touches the scale.
+ *
+ * svdq_quantize_weight_fp8: w bf16 [K][ldw] (row k = input channel, N <= ldw,
+ * ldw % 8 == 0, 16-byte aligned) -> qw [N][K] (16-byte aligned), sw, by the
+ * same rule per 128 x 128 block. N any size. Offline work.
+ */
+svdq_status svdq_quantize_act_fp8(const void* x, int64_t M, int64_t K, int64_t ldx, void* qx, float* sx,
+                                  void* stream);
+svdq_status svdq_quantize_weight_fp8(const void* w, int64_t K, int64_t N, int64_t ldw, void* qw, float* sw,
+                                     void* stream);
+
+/* svdq_gemm_fp8 -- the product above. N any positive size; bias bf16 [N] or
+ *   NULL; act SVDQ_ACT_NONE or SVDQ_ACT_GELU_TANH (in fp32); y [M][ldy] of
+ *   y_dtype, ldy >= N (rows whose ldy is a multiple of 8 and whose base is
+ *   16-byte aligned are written 16 bytes at a time, others by the element).
+ *   Block products are summed in fp32, one fp32 FMA per block joins them to
+ *   the result, and the output is rounded once. sx * sw has to stay finite
+ *   in fp32. qx, qw 16-byte aligned, sx, sw 4, bias 2, y by its element.
+ *   K < 2^22, ldy < 2^31; the tile grid has to fit a launch
+ *   (about M * N < 2^38).
+ *
+ * svdq_gemm_fp8_grouped -- rows sorted by group: rows offsets[g] ..
+ *   offsets[g + 1] - 1 of qx meet weight g (the experts of a
+ *   mixture, or the text and image streams of a joint block). offsets is a
+ *   DEVICE array int32 [groups + 1], rising, within [0, M] (read by the
+ *   kernel; values outside are clamped, so they cannot lead outside the
+ *   arrays); groups may be empty. qw [groups][N][K], sw
+ *   [groups][ceil(N/128)][ceil(K/128)], bias [groups][N] or NULL; sx as
+ *   above for all M rows. Rows of y before offsets[0] and from
+ *   offsets[groups] on are not written. groups in [1, 65536], M < 2^31.
+ */
+svdq_status svdq_gemm_fp8(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
+                          int64_t N, const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
+                          void* stream);
+svdq_status svdq_gemm_fp8_grouped(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw,
+                                  const float* sw, int64_t N, const int32_t* offsets, int32_t groups,
+                                  const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
+                                  void* stream);
+
+/* ------------------------------------------------------------------------
+ * svdq_rope_axes -- rotary positions with several axes (time, height, width
+ * of images and video) on the query and key heads of an attention block,
+ * optionally after an RMS norm of each head: what stands between a fused
+ * [Q | K | V] projection and attention. Pair i of a head turns by
+ * pos[t][axis[i]] * 2 pi turns[i]:
+ *
+ *   v = x                                    or  x * w / sqrt(mean(x^2) + eps)
+ *   (v_a, v_b) -> (v_a cos - v_b sin, v_a sin + v_b cos)
+ *
+ * with the angle negated if inverse is 1 (the rotation undone; without a
+ * norm also the gradient of the forward rotation).
+ *
+ *  q, k       the heads (k may be NULL: queries only). x [T][heads][D] with
+ *             strides in elements (multiples of 8; element (t, h, d) at
+ *             t * token_stride + h * head_stride + d), norm [D] of the same
+ *             dtype or NULL, y the output with strides of its own; y may be x
+ *             with the same strides (in place), other overlaps are not
+ *             allowed. x, y and norm 16-byte aligned.
+ *  dtype      SVDQ_DT_BF16 or SVDQ_DT_F32
+ *  D          head width, a multiple of 8 in [8, 512]
+ *  pos        [T][axes] int32 (pos_dtype SVDQ_POS_I32) or fp32 (SVDQ_POS_F32)
+ *  turns      fp64 [pairs]: turns per unit of position (frequency / 2 pi)
+ *  axis       int32 [pairs], each in [0, axes) (clamped)
+ *  pairs      a multiple of 4, 2 * pairs <= D; values past 2 * pairs of a head
+ *             take the norm but do not turn
+ *  pairing    SVDQ_PAIRS_INTERLEAVED: pair i is (2i, 2i + 1);
+ *             SVDQ_PAIRS_HALF: (i, i + pairs)
+ *
+ * Angles are formed in fp64 and reduced to a part of a turn before their
+ * fp32 sine and cosine; the rest is fp32 with one rounding of the output.
+ * heads of q >= 1, of k >= 0, axes in [1, 8]. T == 0 is valid.
+ */
+typedef enum { SVDQ_POS_I32 = 0, SVDQ_POS_F32 = 1 } svdq_pos_dtype;
+typedef enum { SVDQ_PAIRS_INTERLEAVED = 0, SVDQ_PAIRS_HALF = 1 } svdq_pairing;
+typedef struct {
+    const void* x;
+    int64_t token_stride, head_stride;
+    int32_t heads;
+    const void* norm;
+    void* y;
+    int64_t y_token_stride, y_head_stride;
+} svdq_rope_heads;
+svdq_status svdq_rope_axes(const svdq_rope_heads* q, const svdq_rope_heads* k, int64_t T, int32_t D, int32_t dtype,
+                           const void* pos, int32_t pos_dtype, int32_t axes, const double* turns,
+                           const int32_t* axis, int32_t pairs, int32_t pairing, int32_t inverse, float eps,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif
