@@ -58,6 +58,7 @@ hipError_t launch_quant_act_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t
                                 hipStream_t stream);
 hipError_t launch_quant_weight_fp8(const uint16_t* w, int64_t K, int64_t N, int64_t ldw, uint8_t* qw, float* sw,
                                    hipStream_t stream);
+bool gemm_fp8_fits(int64_t M, int64_t N, int E);
 hipError_t launch_gemm_fp8(const uint8_t* qx, const float* sx, int64_t M, int64_t K, const uint8_t* qw, const float* sw,
                            int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
                            int64_t ldy, int cus, hipStream_t stream);
@@ -767,9 +768,7 @@ svdq_status gemm_fp8_impl(const void* qx, const float* sx, int64_t M, int64_t K,
     if ((s = check_act(act)) != SVDQ_OK) return s;
     if (y_dtype != SVDQ_DT_BF16 && y_dtype != SVDQ_DT_F32)
         return fail(SVDQ_ERR_UNSUPPORTED, "output dtype %d is not supported", y_dtype);
-    // the smallest tile is 16 x 16 with 512 lanes: 2^32 lanes a launch
-    if ((M / 16 + 1 + groups) * (N / 16 + 1) >= ((int64_t)1 << 23) &&
-        (M / 64 + 1 + groups) * (N / 64 + 1) >= ((int64_t)1 << 23))
+    if (!gemm_fp8_fits(M, N, groups))
         return fail(SVDQ_ERR_SHAPE, "M = %lld x N = %lld needs more tiles than one launch holds", (long long)M, (long long)N);
     if (M == 0) { g_last_error.clear(); return SVDQ_OK; }
     if (!qx || !sx || !qw || !sw || !y || (groups && !offsets))

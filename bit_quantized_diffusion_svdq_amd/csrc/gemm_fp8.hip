@@ -94,6 +94,14 @@ DEV void tile_coords(int b, int tiles_m, int tiles_n, int& tm, int& tn) {
     tn = (t - g * per) / rows;
 }
 
+// acc += p * s in the two-address form, which issues faster than the
+// three-address one the compiler picks here. (The compiler does not see an
+// MFMA result's read in it: callers put other MFMAs in between.)
+DEV void fmac(v4f& acc, const v4f& p, float s) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) asm volatile("v_fmac_f32_e32 %0, %1, %2" : "+v"(acc[e]) : "v"(p[e]), "v"(s));
+}
+
 struct Args {
     const uint8_t* qx;
     const float* sx;
@@ -184,17 +192,17 @@ DEV void store4(const Args& a, int64_t row, int col, const float* v) {
 
 // BM x BN outputs per workgroup, WGM x WGN waves of (16 TM) x (16 TN) each;
 // PREC 0: E4M3 matrix instructions, 1: exact products on the bf16 ones
-template <int TM_, int TN_, int WGM_, int WGN_, int WPE_, int PREC_>
+template <int TM_, int TN_, int WGM_, int WGN_, int WPE_, int PREC_, int MID_ = (TM_ > 2 ? TM_ / 2 : 0)>
 struct Cfg {
-    static constexpr int TM = TM_, TN = TN_, WGM = WGM_, WGN = WGN_, WPE = WPE_, PREC = PREC_;
+    static constexpr int TM = TM_, TN = TN_, WGM = WGM_, WGN = WGN_, WPE = WPE_, PREC = PREC_, MID = MID_;
     static constexpr int BM = 16 * TM * WGM, BN = 16 * TN * WGN;
     static constexpr int NW = WGM * WGN, NT = 64 * NW;
     static constexpr int XL = BM / 8, WL = BN / 8;                // 8-row loads per block of K
     static constexpr int XP = (XL + NW - 1) / NW, WP = (WL + NW - 1) / NW, SP = (BM + 63) / 64;
     static_assert(128 % (TN * 16) == 0, "a wave's outputs share one weight scale");
     static_assert(SP <= NW, "one load of 64 row scales per wave");
-    static constexpr int SLOT = (BM + BN) * 128 + SP * 256;
-    static_assert(2 * SLOT * WPE * 4 / NW <= 160 * 1024, "LDS budget");
+    static constexpr int XSLOT = BM * 128 + SP * 256, WSLOT = BN * 128;
+    static_assert(2 * (XSLOT + WSLOT) * WPE * 4 / NW <= 160 * 1024, "LDS budget");
 };
 
 DEV void dma16(rsrc_t r, char* lds, int voff, int soff) {
@@ -207,11 +215,13 @@ DEV void dma4(rsrc_t r, char* lds, int voff, int soff) {
 template <class C, bool GROUPED>
 __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
     constexpr int BM = C::BM, BN = C::BN, TM = C::TM, TN = C::TN, NW = C::NW;
-    // two slots, each a block of K: X's rows, W's rows, X's scales
-    __shared__ __attribute__((aligned(16))) char slot0[C::SLOT];
-    __shared__ __attribute__((aligned(16))) char slot1[C::SLOT];
-    char *const xs0 = slot0, *const ws0 = slot0 + BM * 128, *const ss0 = slot0 + (BM + BN) * 128;
-    char *const xs1 = slot1, *const ws1 = slot1 + BM * 128, *const ss1 = slot1 + (BM + BN) * 128;
+    // two slots of X's rows and row scales and two of W's rows, each a block of
+    // K; separate objects, so that the compiler waits only for loads into the
+    // one it reads
+    __shared__ __attribute__((aligned(16))) char xs0[C::XSLOT];
+    __shared__ __attribute__((aligned(16))) char xs1[C::XSLOT];
+    __shared__ __attribute__((aligned(16))) char ws0[C::WSLOT];
+    __shared__ __attribute__((aligned(16))) char ws1[C::WSLOT];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / C::WGN, wn = wave % C::WGN;
@@ -248,19 +258,23 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
     const int c_even = 16 * ((lane & 7) ^ (lr8 >> 1));             // byte of the chunk, even p
     const int cme = (wave & 1) ? c_even ^ 64 : c_even;             // NW is even: a wave's p have one parity
     const int vx = (wave * 8 + lr8) * K + cme;                     // step NW rows of 8: + 8 NW K
-    auto load_block = [&](char* xs, char* ws, char* ss, int kb) __attribute__((always_inline)) {
-        const int v = kb * 128 + cme < K ? vx : kBeyond;
-#pragma unroll
-        for (int p = 0; p < C::XP; ++p)
-            if (C::XL % NW == 0 || wave + p * NW < C::XL)
-                dma16(rx, xs + (wave + p * NW) * 1024, v, kb * 128 + p * (8 * NW) * K);
-#pragma unroll
-        for (int p = 0; p < C::WP; ++p)
-            if (C::WL % NW == 0 || wave + p * NW < C::WL)
-                dma16(rw, ws + (wave + p * NW) * 1024, v, kb * 128 + p * (8 * NW) * K);
-        // (waves past the rows repeat them: no branch)
-        const rsrc_t rs = make_rsrc(a.sx + (int64_t)kb * a.M + rr.m0, kb < KB ? (int64_t)rr.rows * 4 : 0);
-        dma4(rs, ss + (wave % C::SP) * 256, (wave % C::SP) * 256 + lane * 4, 0);
+    // Loads of a block: XN of X's rows (the last: the row scales) and WP of
+    // W's. A wave without a load in the last round repeats its first (the same
+    // bytes to the same place), and waves past the row scales repeat those: no
+    // branches.
+    constexpr int XN = C::XP + 1;
+    auto load_x = [&](char* xs, int kb, int d) __attribute__((always_inline)) {
+        if (d < C::XP) {
+            const int p = C::XL % NW == 0 || wave + d * NW < C::XL ? d : 0;
+            dma16(rx, xs + (wave + p * NW) * 1024, kb * 128 + cme < K ? vx : kBeyond, kb * 128 + p * (8 * NW) * K);
+        } else {
+            const rsrc_t rs = make_rsrc(a.sx + (int64_t)kb * a.M + rr.m0, kb < KB ? (int64_t)rr.rows * 4 : 0);
+            dma4(rs, xs + BM * 128 + (wave % C::SP) * 256, (wave % C::SP) * 256 + lane * 4, 0);
+        }
+    };
+    auto load_w = [&](char* ws, int kb, int d) __attribute__((always_inline)) {
+        const int p = C::WL % NW == 0 || wave + d * NW < C::WL ? d : 0;
+        dma16(rw, ws + (wave + p * NW) * 1024, kb * 128 + cme < K ? vx : kBeyond, kb * 128 + p * (8 * NW) * K);
     };
 
     // the weight's scales of the wave's outputs, 64 blocks of K at a time, one per lane
@@ -269,85 +283,133 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
     float sw64 = 0.0f;
     auto load_sw = [&](int kb) __attribute__((always_inline)) {
         sw64 = kb + lane < KB ? swp[kb + lane] : 0.0f;
+        order_point(sw64);           // waited for here, not among the loads in flight later
     };
 
+    // the sums start at the bias (its loads hide behind the first block's)
     v4f acc[TM][TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-
-    // the lane's chunks q4 and q4 + 4 of its row in 16-row block 0 of the wave
-    const int xo0 = (wm * TM * 16 + l16) * 128 + 16 * (q4 ^ ((l16 >> 1) & 7));
-    const int wo0 = (wn * TN * 16 + l16) * 128 + 16 * (q4 ^ ((l16 >> 1) & 7));
-    auto block = [&](const char* xs, const char* ws, const char* ss, int kb) __attribute__((always_inline)) {
-        const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw64), kb & 63));
-        Frag<C::PREC> wf[TN], xf[2];
-        float sx[2];
-        auto read_x = [&](int i) __attribute__((always_inline)) {
-            xf[i & 1].set(*(const uint4*)(xs + i * 2048 + xo0), *(const uint4*)(xs + i * 2048 + (xo0 ^ 64)));
-            sx[i & 1] = *(const float*)(ss + (wm * TM + i) * 64 + l16 * 4);
-        };
-        read_x(0);
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-            wf[j].set(*(const uint4*)(ws + j * 2048 + wo0), *(const uint4*)(ws + j * 2048 + (wo0 ^ 64)));
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            if (i + 1 < TM) read_x(i + 1);
-            const float s = sx[i & 1] * sw;
-            v4f p[TN];
-#pragma unroll
-            for (int j = 0; j < TN; ++j) p[j] = Frag<C::PREC>::dot(wf[j], xf[i & 1]);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[j][e], s, acc[i][j][e]);
-                order_point(acc[i][j]);          // (keeps the sums from being put off past the barrier)
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
-    auto publish = [&]() __attribute__((always_inline)) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        lds_barrier();
-    };
-
-    // Pairs of blocks keep the loop free of branches (each slot is an object of
-    // its own, so the compiler waits only for loads into the slot it reads);
-    // blocks past the end of K load zeros.
-    load_block(xs0, ws0, ss0, 0);
-    load_sw(0);
-    publish();
-    for (int kb = 0; kb + 1 < KB; kb += 2) {
-        if ((kb & 63) == 0) load_sw(kb);
-        load_block(xs1, ws1, ss1, kb + 1);
-        block(xs0, ws0, ss0, kb);
-        publish();
-        load_block(xs0, ws0, ss0, kb + 2);
-        block(xs1, ws1, ss1, kb + 1);
-        publish();
-    }
-    if (KB & 1) {
-        if ((KB & 63) == 1) load_sw(KB - 1);
-        block(xs0, ws0, ss0, KB - 1);
-        lds_barrier();
-    }
-
-    // ---- outputs: bias and activation in registers, one rounding, then through
-    // LDS (free now) so that rows leave as 16-byte stores of whole lines. The
-    // 16-byte chunks of a staged row are XOR-swizzled against bank conflicts.
     const rsrc_t rb = make_rsrc(a.bias ? a.bias + (int64_t)rr.g * a.N : nullptr, a.bias ? (int64_t)a.N * 2 : 0);
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int col = n0 + wn * TN * 16 + j * 16 + q4 * 4 + e;
-            const float b = bf16_lo_to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rb, col * 2, 0, 0));
-#pragma unroll
-            for (int i = 0; i < TM; ++i) acc[i][j][e] += b;
+            acc[0][j][e] = bf16_lo_to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rb, col * 2, 0, 0));
         }
+#pragma unroll
+    for (int i = 1; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = acc[0][j];
+
+    // ---- operands: the lane's chunks q4 and q4 + 4 of its row in each 16-row block
+    const int xo0 = (wm * TM * 16 + l16) * 128 + 16 * (q4 ^ ((l16 >> 1) & 7));
+    const int wo0 = (wn * TN * 16 + l16) * 128 + 16 * (q4 ^ ((l16 >> 1) & 7));
+    const int so0 = BM * 128 + wm * TM * 64 + l16 * 4;
+    Frag<C::PREC> wf[TN], xf[2];
+    float sx[2];
+    auto read_x = [&](const char* xs, int i, int par) __attribute__((always_inline)) {
+        xf[par].set(*(const uint4*)(xs + i * 2048 + xo0), *(const uint4*)(xs + i * 2048 + (xo0 ^ 64)));
+        sx[par] = *(const float*)(xs + so0 + i * 64);
+    };
+    auto read_w = [&](const char* ws, int j) __attribute__((always_inline)) {
+        wf[j].set(*(const uint4*)(ws + j * 2048 + wo0), *(const uint4*)(ws + j * 2048 + (wo0 ^ 64)));
+    };
+
+    // Block kb, whose W operands and first X operand are in registers. Each
+    // MFMA is followed by the four FMAs that add the product of the same
+    // columns 16 rows earlier (the last block's last rows for the first),
+    // which is complete by then: alternating like this, the vector work runs
+    // in the matrix pipe's shadow (an MFMA and its four FMAs take 14.1 ns of a
+    // SIMD with two waves, the MFMA alone 14.3, while four MFMAs and then
+    // sixteen FMAs take 16.6 a piece).
+    //
+    // Two meetings of the waves. At row block MID everybody has W's operands
+    // of this block in registers, so W of block kb + 2 starts on its way into
+    // their slot. At the last row block nobody reads X's slot any more: block
+    // kb + 1 has landed (all but the WP loads of W just begun), its first
+    // operands are read as this block's are used up, and X of block kb + 2
+    // starts. Loads go out one at a time between the MFMAs: in a burst they
+    // hold the waves up at the vector memory unit.
+    constexpr int MID = C::MID, PX = (MID + 1) * TN, PW_ = (TM - 1 - MID) * TN;   // places for loads of X and W
+    static_assert(MID >= 0 && MID <= TM - 2, "the meetings follow each other");
+    constexpr int GAP = PW_ >= 2 * C::WP && PX >= 2 * XN ? 2 : 1;                 // a load at every GAP-th place,
+    constexpr int NX = (XN + PX - 1) / PX, NWL = (C::WP + PW_ - 1) / PW_;         // or several at each
+    auto meet = [&](bool all) __attribute__((always_inline)) {
+        if (all) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::WP) : "memory");
+        lds_barrier();
+    };
+    v4f p[2][TN];
+    float sp[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < TN; ++j) p[0][j] = p[1][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    auto block = [&](char* xs, char* ws, char* nxs, char* nws, int kb, int par0) __attribute__((always_inline)) {
+        const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw64), kb & 63));
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int par = (par0 + i) & 1, before = (i + TM - 1) % TM;
+            if (i == MID) lds_barrier();
+            if (i + 1 < TM) {
+                read_x(xs, i + 1, par ^ 1);
+            } else {
+                meet(false);
+                read_x(nxs, 0, par ^ 1);
+            }
+            sp[par] = sx[par] * sw;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                p[par][j] = Frag<C::PREC>::dot(wf[j], xf[par]);
+                __builtin_amdgcn_sched_barrier(0);
+                fmac(acc[before][j], p[par ^ 1][j], sp[par ^ 1]);
+                const int ax = (i + 1) % TM * TN + j, aw = (i - MID) * TN + j;   // places since the meetings
+#pragma unroll
+                for (int u = 0; u < NX; ++u) {
+                    const int d = ax / GAP * NX + u;
+                    if (ax % GAP == 0 && d < XN) {
+                        if (i + 1 == TM) load_x(xs, kb + 2, d);
+                        else load_x(nxs, kb + 1, d);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < NWL; ++u) {
+                    const int d = aw / GAP * NWL + u;
+                    if (aw >= 0 && aw % GAP == 0 && d < C::WP && i + 1 < TM) load_w(ws, kb + 2, d);
+                }
+                if (i + 1 == TM) read_w(nws, j);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+
+    // Blocks run in pairs, which keeps the loop free of branches; blocks past
+    // the end of K are zeros.
+#pragma unroll
+    for (int d = 0; d < XN; ++d) load_x(xs0, 0, d);
+#pragma unroll
+    for (int d = 0; d < C::WP; ++d) load_w(ws0, 0, d);
+#pragma unroll
+    for (int d = 0; d < C::WP; ++d) load_w(ws1, 1, d);
+    meet(false);
+    read_x(xs0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+#pragma unroll
+        for (int u = 0; u < NX; ++u)
+            if (j % GAP == 0 && j / GAP * NX + u < XN) load_x(xs1, 1, j / GAP * NX + u);
+        read_w(ws0, j);
+    }
+    for (int kb = 0; kb < KB; kb += 2) {
+        if ((kb & 63) == 0) load_sw(kb);
+        block(xs0, ws0, xs1, ws1, kb, 0);
+        block(xs1, ws1, xs0, ws0, kb + 1, TM & 1);
+    }
+    meet(true);                                          // (the last products are complete)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fmac(acc[TM - 1][j], p[(2 * TM - 1) & 1][j], sp[(2 * TM - 1) & 1]);
+
+    // ---- outputs: activation in registers, one rounding, then through
+    // LDS (free now) so that rows leave as 16-byte stores of whole lines. The
+    // 16-byte chunks of a staged row are XOR-swizzled against bank conflicts.
     if (a.act) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -358,9 +420,11 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
     }
     constexpr int ES = C::PREC ? 4 : 2;                            // bytes of an output
     constexpr int RB = TN * 16 * ES, CPR = RB / 16;                // bytes, 16-byte chunks of a staged row
-    constexpr int PER_SLOT = NW / 2;                               // waves staged in a slot
-    static_assert(PER_SLOT * 16 * TM * RB <= C::SLOT, "staging fits the slots");
-    char* stg = (wave < PER_SLOT ? slot0 : slot1) + (wave % PER_SLOT) * (16 * TM * RB);
+    constexpr int PW = 16 * TM * RB, XW = C::XSLOT / PW, WW = C::WSLOT / PW;   // a wave's bytes, waves per slot
+    static_assert(2 * (XW + WW) >= NW, "staging fits the slots");
+    char* stg = wave < XW ? xs0 + wave * PW
+              : wave < 2 * XW ? xs1 + (wave - XW) * PW
+              : wave < 2 * XW + WW ? ws0 + (wave - 2 * XW) * PW : ws1 + (wave - 2 * XW - WW) * PW;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -396,39 +460,51 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
 
 // ---------------------------------------------------------------- few rows
 
-// Up to 16 rows: 16 outputs per workgroup, the K blocks dealt to its NW waves,
-// the weights straight from memory into the MFMA operand (no reuse to stage
-// for), the waves' sums joined in LDS in wave order.
-template <int NW, int PREC, bool GROUPED>
-__global__ __launch_bounds__(64 * NW) void gemm_fp8_few_kernel(Args a) {
-    __shared__ __attribute__((aligned(16))) v4f red[NW][64];
+// Up to 16 MT rows: 16 NT outputs per workgroup, the K blocks dealt to its NW
+// waves U at a time, the weights straight from memory into the MFMA operand
+// (no reuse to stage for), the waves' sums joined in LDS in wave order.
+template <int MT_, int NT_, int NW_, int U_, int PREC_>
+struct FewCfg {
+    static constexpr int MT = MT_, NT = NT_, NW = NW_, U = U_, PREC = PREC_;
+};
+
+template <class C, bool GROUPED>
+__global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
+    constexpr int MT = C::MT, NT = C::NT, NW = C::NW, U = C::U;
+    __shared__ __attribute__((aligned(16))) v4f red[NW][MT * NT][64];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int tiles_n = (a.N + 15) / 16;
+    const int tiles_n = (a.N + 16 * NT - 1) / (16 * NT);
     const int t = blockIdx.x;
     Rows rr;
     if constexpr (GROUPED) {
         int total;
-        rr = group_rows(a, t / tiles_n, 16, &total);
+        rr = group_rows(a, t / tiles_n, 16 * MT, &total);
         if (t / tiles_n >= total) return;
     } else {
-        rr.m0 = (int64_t)(t / tiles_n) * 16;
-        rr.rows = (int)((a.M - rr.m0) < 16 ? (a.M - rr.m0) : 16);
+        rr.m0 = (int64_t)(t / tiles_n) * (16 * MT);
+        rr.rows = (int)((a.M - rr.m0) < 16 * MT ? (a.M - rr.m0) : 16 * MT);
         rr.g = 0;
     }
-    const int n0 = (t % tiles_n) * 16;
+    const int n0 = (t % tiles_n) * 16 * NT;
     const int K = a.K, KB = (K + 127) / 128, NB = (a.N + 127) / 128;
-    const int nrows = a.N - n0 < 16 ? a.N - n0 : 16;
+    const int nrows = a.N - n0 < 16 * NT ? a.N - n0 : 16 * NT;
     const rsrc_t rx = make_rsrc(a.qx + rr.m0 * K, (int64_t)rr.rows * K);
     const rsrc_t rw = make_rsrc(a.qw + ((int64_t)rr.g * a.N + n0) * K, (int64_t)nrows * K);
     const float* swp = a.sw + ((int64_t)rr.g * NB + n0 / 128) * KB;
-    const float* sxp = a.sx + rr.m0 + (l16 < rr.rows ? l16 : rr.rows - 1);
+    const float* sxp = a.sx + rr.m0;
+    int ms[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ms[i] = 16 * i + l16 < rr.rows ? 16 * i + l16 : rr.rows - 1;
     const int vo = l16 * K + 16 * q4;
-    v4f acc = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int U = 4;
+    v4f acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     for (int kb0 = wave; kb0 < KB; kb0 += NW * U) {
-        uint4 w[U][2], x[U][2];
-        float s[U];
+        uint4 w[U][NT][2], x[U][MT][2];
+        float s[U][MT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int kb = kb0 + u * NW;
@@ -436,38 +512,56 @@ __global__ __launch_bounds__(64 * NW) void gemm_fp8_few_kernel(Args a) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int v = 64 * h < left ? vo + 64 * h : kBeyond;
-                w[u][h] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rw, v, kb * 128, 0));
-                x[u][h] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, v, kb * 128, 0));
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    w[u][j][h] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rw, v, kb * 128 + j * 16 * K, 0));
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    x[u][i][h] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, v, kb * 128 + i * 16 * K, 0));
             }
             const int kc = kb < KB ? kb : KB - 1;
-            s[u] = sxp[(int64_t)kc * a.M] * swp[kc];
+            const float sw = swp[kc];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) s[u][i] = sxp[(int64_t)kc * a.M + ms[i]] * sw;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            Frag<PREC> wf, xf;
-            wf.set(w[u][0], w[u][1]);
-            xf.set(x[u][0], x[u][1]);
-            const v4f p = Frag<PREC>::dot(wf, xf);
+            Frag<C::PREC> wf[NT];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(p[e], s[u], acc[e]);
+            for (int j = 0; j < NT; ++j) wf[j].set(w[u][j][0], w[u][j][1]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                Frag<C::PREC> xf;
+                xf.set(x[u][i][0], x[u][i][1]);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const v4f p = Frag<C::PREC>::dot(wf[j], xf);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], s[u][i], acc[i][j][e]);
+                }
+            }
         }
     }
-    red[wave][lane] = acc;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) red[wave][i * NT + j][lane] = acc[i][j];
     __syncthreads();
-    if (wave == 0) {
+    for (int b = wave; b < MT * NT; b += NW) {           // a 16 x 16 tile per wave
+        v4f sum = red[0][b][lane];
 #pragma unroll
         for (int k = 1; k < NW; ++k) {
-            const v4f o = red[k][lane];
+            const v4f o = red[k][b][lane];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] += o[e];
+            for (int e = 0; e < 4; ++e) sum[e] += o[e];
         }
-        const int col = n0 + q4 * 4;
+        const int row = b / NT * 16 + l16, col = n0 + b % NT * 16 + q4 * 4;
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            v[e] = finish(acc[e], a.bias && col + e < a.N ? bf16_lo_to_f32(a.bias[(int64_t)rr.g * a.N + col + e]) : 0.0f,
+            v[e] = finish(sum[e], a.bias && col + e < a.N ? bf16_lo_to_f32(a.bias[(int64_t)rr.g * a.N + col + e]) : 0.0f,
                           a.act);
-        if (l16 < rr.rows) store4(a, rr.m0 + l16, col, v);
+        if (row < rr.rows) store4(a, rr.m0 + row, col, v);
     }
 }
 
@@ -478,33 +572,117 @@ void launch_tiles(const Args& a, hipStream_t stream) {
     hipLaunchKernelGGL((gemm_fp8_kernel<C, GROUPED>), dim3((unsigned)(tm * tn)), dim3(C::NT), 0, stream, a);
 }
 
-template <int PREC, bool GROUPED>
+template <class C, bool GROUPED>
 void launch_few(const Args& a, hipStream_t stream) {
-    const int64_t tm = GROUPED ? (a.M + (int64_t)a.E * 15) / 16 : (a.M + 15) / 16;
-    const int64_t tn = (a.N + 15) / 16;
-    hipLaunchKernelGGL((gemm_fp8_few_kernel<8, PREC, GROUPED>), dim3((unsigned)(tm * tn)), dim3(512), 0, stream, a);
+    const int64_t tm = GROUPED ? (a.M + (int64_t)a.E * (16 * C::MT - 1)) / (16 * C::MT) : (a.M + 16 * C::MT - 1) / (16 * C::MT);
+    const int64_t tn = (a.N + 16 * C::NT - 1) / (16 * C::NT);
+    hipLaunchKernelGGL((gemm_fp8_few_kernel<C, GROUPED>), dim3((unsigned)(tm * tn)), dim3(64 * C::NW), 0, stream, a);
+}
+
+// ---------------------------------------------------------------- which kernel
+//
+// One estimate per variant, in microseconds, from times measured on MI355X at
+// K = 4096 (32 blocks of 128; a launch of nothing takes 3):
+//  - tiles: `lone` per block of K with one workgroup on a CU, `full` with
+//    `per_cu` (its memory latency hidden by the others, the CU's pipes
+//    shared). Large tiles move fewer bytes and read LDS less per product:
+//    4096 x 4096 x 8192 takes 121 us with 256 x 256, 132 with 192 x 256, 143
+//    with 128 x 128, 184 with 64 x 128, 223 with 64 x 64. Which one wins is
+//    decided by how its tiles fill rounds of the CUs: 4608 x 12288 x 4096 takes
+//    211 us with 160 x 256 (1.8 rounds) and 272 with 256 x 256 (1.1), 4608 x
+//    4096 x 12288 208 with 224 x 256 (3.9 rounds), 233 with 160 x 256; 256 x
+//    4096 x 4096 takes 13 with 64 x 64 (256 tiles), 19 with 128 x 128 (64).
+//  - few rows: bound by the weights from memory (5.2 bytes a picosecond), the
+//    operands from L2 (8.4, short of 256 workgroups less) or the trips of a
+//    wave's loads (2.2 each). 1 x 4096 x 18432 takes 17 us (best tile 22),
+//    64 x 4096 x 4096 10.5 (13), 128 x 12288 x 4096 38 (46), but 64 x 4096 x 12288
+//    26 (20).
+struct Variant {
+    int rows, cols, few;             // outputs per workgroup; few: the few-rows kernel
+    int per_cu, trip;                // workgroups on a CU; K blocks per trip of a few-rows workgroup
+    double lone, full;
+};
+
+constexpr Variant kVariants[] = {
+    {256, 256, 0, 1, 0, 1.20, 1.81}, {224, 256, 0, 1, 0, 1.07, 1.63}, {192, 256, 0, 1, 0, 0.94, 1.38},
+    {160, 256, 0, 1, 0, 0.85, 1.21}, {256, 128, 0, 1, 0, 0.75, 0.98}, {128, 128, 0, 2, 0, 0.60, 1.07},
+    {64, 128, 0, 3, 0, 0.46, 1.05},  {64, 64, 0, 4, 0, 0.40, 0.86},   {16, 16, 1, 4, 32, 0, 0},
+    {16, 32, 1, 4, 16, 0, 0},        {32, 32, 1, 4, 16, 0, 0},        {32, 64, 1, 4, 16, 0, 0},
+};
+
+double estimate(const Variant& v, const Args& a, int cus) {
+    const double active = a.offs ? (double)(a.E < a.M ? a.E : a.M) : 1.0, kb = (a.K + 127) / 128;
+    const double tn = (double)((a.N + v.cols - 1) / v.cols);
+    // ragged groups: half a tile is lost at the end of each, on the average
+    double tm = a.offs ? (double)a.M / v.rows + 0.5 * active : (double)((a.M + v.rows - 1) / v.rows);
+    if (tm < active) tm = active;
+    const double tiles = tm * tn;
+    if (v.few) {
+        const double rows = a.M < v.rows * tm ? (double)a.M / tm : v.rows;
+        const double weights = active * a.N * (double)a.K / 5.2e6;
+        const double reads = tiles * (v.cols + rows) * (double)a.K / 8.4e6 * (tiles < cus ? cus / tiles : 1.0);
+        const double trips = 2.2 * __builtin_ceil(kb / v.trip) * __builtin_ceil(tiles / (4.0 * cus));
+        double t = weights > reads ? weights : reads;
+        return 3.0 + (t > trips ? t : trips);
+    }
+    const double slots = (double)cus * v.per_cu, rounds = __builtin_floor(tiles / slots);
+    const double rest = __builtin_ceil((tiles - rounds * slots) / cus);
+    const double share = v.full * rest / v.per_cu, out = 4.0 * v.rows * v.cols * v.per_cu / 65536.0;
+    return 3.0 + rounds * (kb * v.full + out) + (rest > 0 ? kb * (share > v.lone ? share : v.lone) + out * rest / v.per_cu : 0.0);
+}
+
+// lanes of a launch stay below 2^32
+bool fits(const Variant& v, const Args& a) {
+    const double tm = (double)a.M / v.rows + 1.0 + a.E, tn = (double)a.N / v.cols + 1.0;
+    return tm * tn * 512.0 < 4294967296.0;
 }
 
 template <int PREC, bool GROUPED>
-void launch_any(const Args& a, hipStream_t stream) {
-    if (GROUPED ? a.M <= (int64_t)16 * a.E : a.M <= 64) launch_few<PREC, GROUPED>(a, stream);
-    else launch_tiles<Cfg<4, 4, 2, 2, 2, PREC>, GROUPED>(a, stream);
+bool launch_variant(const Args& a, int cus, hipStream_t stream) {
+    int best = -1;
+    double least = 0.0;
+    for (int i = 0; i < (int)(sizeof kVariants / sizeof kVariants[0]); ++i) {
+        // fp32 outputs have the two tile sizes whose operands fit the registers when widened
+        if (PREC == 1 && i < 8 && i != 5 && i != 7) continue;
+        if (!fits(kVariants[i], a)) continue;
+        const double t = estimate(kVariants[i], a, cus);
+        if (best < 0 || t < least) best = i, least = t;
+    }
+    switch (best) {
+        case 0: if constexpr (PREC == 0) launch_tiles<Cfg<8, 4, 2, 4, 2, 0, 3>, GROUPED>(a, stream); break;
+        case 1: if constexpr (PREC == 0) launch_tiles<Cfg<7, 4, 2, 4, 2, 0, 3>, GROUPED>(a, stream); break;
+        case 2: if constexpr (PREC == 0) launch_tiles<Cfg<6, 4, 2, 4, 2, 0, 2>, GROUPED>(a, stream); break;
+        case 3: if constexpr (PREC == 0) launch_tiles<Cfg<5, 4, 2, 4, 2, 0, 2>, GROUPED>(a, stream); break;
+        case 4: if constexpr (PREC == 0) launch_tiles<Cfg<4, 4, 4, 2, 2, 0, 2>, GROUPED>(a, stream); break;
+        case 5: launch_tiles<Cfg<4, 4, 2, 2, 2, PREC, 2>, GROUPED>(a, stream); break;
+        case 6: if constexpr (PREC == 0) launch_tiles<Cfg<2, 4, 2, 2, 2, 0, 0>, GROUPED>(a, stream); break;
+        case 7: launch_tiles<Cfg<2, 2, 2, 2, 2, PREC, 0>, GROUPED>(a, stream); break;
+        case 8: launch_few<FewCfg<1, 1, 8, 4, PREC>, GROUPED>(a, stream); break;
+        case 9: launch_few<FewCfg<1, 2, 8, 2, PREC>, GROUPED>(a, stream); break;
+        case 10: launch_few<FewCfg<2, 2, 8, 2, PREC>, GROUPED>(a, stream); break;
+        case 11: launch_few<FewCfg<2, 4, 8, 2, PREC>, GROUPED>(a, stream); break;
+        default: return false;
+    }
+    return true;
 }
 
 }  // namespace
 
+// whether some variant's grid fits a launch
+bool gemm_fp8_fits(int64_t M, int64_t N, int E) {
+    Args a{};
+    a.M = M;
+    a.N = (int)N;
+    a.E = E;
+    return fits(kVariants[5], a);
+}
+
 hipError_t launch_gemm_fp8(const uint8_t* qx, const float* sx, int64_t M, int64_t K, const uint8_t* qw, const float* sw,
                            int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
                            int64_t ldy, int cus, hipStream_t stream) {
-    (void)cus;
     const int vec = ldy % (y_f32 ? 4 : 8) == 0 && (uintptr_t)y % 16 == 0;
     const Args a{qx, sx, qw, sw, bias, y, offs, M, ldy, (int)N, (int)K, E, act, y_f32, vec};
-    if (offs) {
-        if (y_f32) launch_any<1, true>(a, stream);
-        else launch_any<0, true>(a, stream);
-    } else {
-        if (y_f32) launch_any<1, false>(a, stream);
-        else launch_any<0, false>(a, stream);
-    }
-    return hipGetLastError();
+    const bool ok = offs ? (y_f32 ? launch_variant<1, true>(a, cus, stream) : launch_variant<0, true>(a, cus, stream))
+                         : (y_f32 ? launch_variant<1, false>(a, cus, stream) : launch_variant<0, false>(a, cus, stream));
+    return ok ? hipGetLastError() : hipErrorInvalidValue;
 }

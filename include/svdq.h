@@ -536,11 +536,15 @@ svdq_status svdq_quantize_weight_fp8(const void* w, int64_t K, int64_t N, int64_
  *   NULL; act SVDQ_ACT_NONE or SVDQ_ACT_GELU_TANH (in fp32); y [M][ldy] of
  *   y_dtype, ldy >= N (rows whose ldy is a multiple of 8 and whose base is
  *   16-byte aligned are written 16 bytes at a time, others by the element).
- *   Block products are summed in fp32, one fp32 FMA per block joins them to
- *   the result, and the output is rounded once. sx * sw has to stay finite
+ *   One fp32 FMA per block joins its product to the fp32 result, and the
+ *   output is rounded once. fp32 outputs: products and sums of a block keep
+ *   fp32. bf16 outputs: the E4M3 matrix instructions add 8 consecutive
+ *   channels' products at the exponent of the largest and drop what falls
+ *   more than 13 bits below it (at most 7 * 2^-13 of the largest of each 8;
+ *   about 3e-5 of the result for random operands), the rest is fp32. sx * sw has to stay finite
  *   in fp32. qx, qw 16-byte aligned, sx, sw 4, bias 2, y by its element.
- *   K < 2^22, ldy < 2^31; the tile grid has to fit a launch
- *   (about M * N < 2^38).
+ *   K < 2^22, ldy < 2^31; the grid of 128 x 128 tiles has to fit a launch
+ *   ((M / 128 + 1 + groups) (N / 128 + 1) < 2^23).
  *
  * svdq_gemm_fp8_grouped -- rows sorted by group: rows offsets[g] ..
  *   offsets[g + 1] - 1 of qx meet weight g (the experts of a
