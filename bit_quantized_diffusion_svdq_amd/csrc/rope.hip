@@ -14,34 +14,73 @@
 //
 // Bound by memory: every head is read and written once. A wave owns one
 // token and a run of its heads: it computes the token's cosines and sines
-// once (one pair per lane, shared through LDS) and reuses them for all its
+// once (one pair per lane, shared through LDS, while its first loads are on
+// their way) and reuses them, multiplied by the norm's weights, for all its
 // heads. A lane owns four pairs of a head (8 values, 16 bytes of bf16), so a
 // 128-wide head is 16 lanes and a load instruction covers four heads; the
-// norm's sum of squares is a butterfly over a head's lanes.
+// norm's sum of squares is a butterfly over a head's lanes without LDS. The
+// vector work counts beside the memory's: folding the weights into the
+// rotation, uniform sides and the hardware's reciprocal root took 4608 tokens
+// of 24 + 24 heads of 128 (normed) from 47.6 to 27.1 us, 4.2 TB/s; 32761 of
+// 16 + 4 without a norm run in 66.8 us, 5.0 TB/s (a plain copy: 5.5).
 #include "common.h"
 #include "rope.h"
 
 namespace {
 
+// a lane's eight values as they lie in memory
 template <int F32>
-DEV void load4(const void* p, int64_t at, float* v) {
+struct Raw {
+    uint4 v[F32 ? 2 : 1];
+};
+
+template <int F32, int HALF>
+DEV Raw<F32> load8(const void* p, int64_t at, int e0, int e1) {
+    Raw<F32> r;
     if constexpr (F32) {
-        const float4 u = *(const float4*)((const float*)p + at);
-        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+        r.v[0] = *(const uint4*)((const float*)p + at + e0);
+        r.v[1] = *(const uint4*)((const float*)p + at + e1);
+    } else if constexpr (HALF) {
+        const uint2 a = *(const uint2*)((const uint16_t*)p + at + e0), b = *(const uint2*)((const uint16_t*)p + at + e1);
+        r.v[0] = make_uint4(a.x, a.y, b.x, b.y);
     } else {
-        const uint2 u = *(const uint2*)((const uint16_t*)p + at);
-        v[0] = bf16_lo_to_f32(u.x); v[1] = bf16_hi_to_f32(u.x);
-        v[2] = bf16_lo_to_f32(u.y); v[3] = bf16_hi_to_f32(u.y);
+        r.v[0] = *(const uint4*)((const uint16_t*)p + at + e0);          // e1 = e0 + 4
+    }
+    return r;
+}
+
+template <int F32>
+DEV void unpack(const Raw<F32>& r, float* v) {
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (F32) {
+            const uint32_t w1[4] = {r.v[F32].x, r.v[F32].y, r.v[F32].z, r.v[F32].w};
+            v[i] = __uint_as_float(w[i]);
+            v[4 + i] = __uint_as_float(w1[i]);
+        } else {
+            v[2 * i] = bf16_lo_to_f32(w[i]);
+            v[2 * i + 1] = bf16_hi_to_f32(w[i]);
+        }
     }
 }
 
-template <int F32>
-DEV void store4(void* p, int64_t at, const float* v) {
-    if constexpr (F32) *(float4*)((float*)p + at) = make_float4(v[0], v[1], v[2], v[3]);
-    else *(uint2*)((uint16_t*)p + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+template <int F32, int HALF>
+DEV void store8(void* p, int64_t at, int e0, int e1, const float* v) {
+    if constexpr (F32) {
+        *(float4*)((float*)p + at + e0) = make_float4(v[0], v[1], v[2], v[3]);
+        *(float4*)((float*)p + at + e1) = make_float4(v[4], v[5], v[6], v[7]);
+    } else if constexpr (HALF) {
+        *(uint2*)((uint16_t*)p + at + e0) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        *(uint2*)((uint16_t*)p + at + e1) = make_uint2(pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    } else {
+        *(uint4*)((uint16_t*)p + at + e0) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
 }
 
 constexpr int kMaxPairs = 256;
+constexpr int U = 4;                     // loads of a wave in flight (16 bytes a lane each, bf16)
 
 // HALF 0: pairs are neighbours (2i, 2i + 1); 1: pair i is (i, i + pairs)
 template <int F32, int HALF>
@@ -49,20 +88,44 @@ __global__ __launch_bounds__(256) void rope_axes_kernel(RopeArgs a) {
     __shared__ float2 cs[4][kMaxPairs];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int per = 64 / a.lp;                                   // heads per load
-    const int H = a.heads[0] + a.heads[1];
-    const int loads = (H + per - 1) / per, chunks = (loads + a.chunk - 1) / a.chunk;
-    const int64_t item = (int64_t)blockIdx.x * 4 + wave;
-    const int64_t t = item / chunks;
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;            // the wave's token
     if (t >= a.T) return;
-    const int c = (int)(item - t * chunks);
+    const int per = 64 / a.lp;                                   // heads per load
+    // its share of the token's loads, of which the first lq are the queries'
+    const int lq = (a.heads[0] + per - 1) / per, loads = lq + (a.heads[1] + per - 1) / per;
+    const int first = blockIdx.y * a.chunk, last = first + a.chunk < loads ? first + a.chunk : loads;
+    const int u = lane & (a.lp - 1), slot = lane / a.lp;
+    const bool in = u * 8 < a.D, turned = u * 4 < a.pairs;
+    // the lane's values: e0 .. e0 + 3 and e1 .. e1 + 3 of the head
+    const int e0 = HALF && turned ? 4 * u : 8 * u, e1 = HALF && turned ? a.pairs + 4 * u : 8 * u + 4;
+    // a group: up to U loads of one side
+    auto side_of = [&](int l) __attribute__((always_inline)) { return l >= lq ? 1 : 0; };
+    auto end_of = [&](int l) __attribute__((always_inline)) {
+        const int stop = l < lq && lq < last ? lq : last;
+        return l + U < stop ? l + U : stop;
+    };
+    Raw<F32> raw[U];
+    auto fetch = [&](int l0) __attribute__((always_inline)) {
+        const int side = side_of(l0), end = end_of(l0);
+        const int64_t hs = a.hs[side], at0 = t * a.ts[side] + (int64_t)slot * hs;
+        const int h0 = (side ? l0 - lq : l0) * per;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int h = h0 + k * per;
+            raw[k] = Raw<F32>{};
+            if (l0 + k < end && in && h + slot < a.heads[side]) raw[k] = load8<F32, HALF>(a.x[side], at0 + h * hs, e0, e1);
+        }
+    };
+    if (first < last) fetch(first);                              // on its way while the angles are worked out
 
-    for (int p = lane; p < a.pairs; p += 64) {
+    const int pv = lane < a.axes ? ((const int*)a.pos)[t * a.axes + lane] : 0;   // the token's positions, one a lane
+    for (int p0 = 0; p0 < a.pairs; p0 += 64) {
+        const int p = p0 + lane < a.pairs ? p0 + lane : a.pairs - 1;
         int ax = a.axis[p];
+        const double turns = a.turns[p];
         ax = ax < 0 ? 0 : ax >= a.axes ? a.axes - 1 : ax;
-        const int64_t at = t * a.axes + ax;
-        const double pos = a.pos_f32 ? (double)((const float*)a.pos)[at] : (double)((const int*)a.pos)[at];
-        const double turn = pos * a.turns[p];
+        const int bits = __shfl(pv, ax);
+        const double turn = (a.pos_f32 ? (double)__int_as_float(bits) : (double)bits) * turns;
         const float part = (float)(turn - rint(turn));
         float s, co;
         sincospif(2.0f * part, &s, &co);
@@ -70,68 +133,62 @@ __global__ __launch_bounds__(256) void rope_axes_kernel(RopeArgs a) {
     }
     __builtin_amdgcn_wave_barrier();
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-
-    const int u = lane & (a.lp - 1), slot = lane / a.lp;
-    const bool in = u * 8 < a.D, turned = u * 4 < a.pairs;
-    // the lane's values: e0 .. e0 + 3 and e1 .. e1 + 3 of the head
-    const int e0 = HALF && turned ? 4 * u : 8 * u, e1 = HALF && turned ? a.pairs + 4 * u : 8 * u + 4;
-    float co[4], si[4];
+    const float inv_d = 1.0f / (float)a.D;
+    float m[4][4];
+    for (int l0 = first; l0 < last;) {
+        const int side = side_of(l0), end = end_of(l0);
+        if (l0 == first || l0 == lq) {
+            // Pair i of the lane, with the side's norm weights taken in:
+            //   x' = (x r) (w_x cos) - (y r) (w_y sin),  y' = (x r) (w_x sin) + (y r) (w_y cos)
+            float w[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 v = turned ? cs[wave][4 * u + i] : make_float2(1.0f, 0.0f);
-        co[i] = v.x;
-        si[i] = v.y;
-    }
-    const int first = c * a.chunk, last = first + a.chunk < loads ? first + a.chunk : loads;
-    constexpr int U = 4;
-    for (int l0 = first; l0 < last; l0 += U) {
-        float v[U][8];
-        int hd[U], side[U];
-        bool ok[U];
+            for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+            if (in && a.norm[side]) unpack<F32>(load8<F32, HALF>(a.norm[side], 0, e0, e1), w);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int h = (l0 + k) * per + slot;
-            ok[k] = in && l0 + k < last && h < H;
-            side[k] = h >= a.heads[0];
-            hd[k] = side[k] ? h - a.heads[0] : h;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
-            if (ok[k]) {
-                const int64_t at = t * a.ts[side[k]] + hd[k] * a.hs[side[k]];
-                load4<F32>(a.x[side[k]], at + e0, v[k]);
-                load4<F32>(a.x[side[k]], at + e1, v[k] + 4);
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = turned ? cs[wave][4 * u + i] : make_float2(1.0f, 0.0f);
+                const float wx = w[HALF ? i : 2 * i], wy = w[HALF ? 4 + i : 2 * i + 1];
+                m[i][0] = wx * v.x;
+                m[i][1] = wy * v.y;
+                m[i][2] = wx * v.y;
+                m[i][3] = wy * v.x;
             }
         }
+        Raw<F32> now[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) now[k] = raw[k];
+        if (end < last) fetch(end);
+        const int64_t hs = a.yhs[side], at0 = t * a.yts[side] + (int64_t)slot * hs;
+        const int h0 = (side ? l0 - lq : l0) * per;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            if (l0 + k >= last) break;                            // the same for all lanes
-            if (a.norm[0] || a.norm[1]) {
+            if (l0 + k >= end) break;                             // the same for all lanes
+            float v[8], o[8];
+            unpack<F32>(now[k], v);
+            if (a.norm[side]) {
                 float ss = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[k][e], v[k][e], ss);
-                for (int d = 1; d < a.lp; d <<= 1) ss += __shfl_xor(ss, d);
-                if (ok[k] && a.norm[side[k]]) {
-                    const float r = 1.0f / sqrtf(ss / (float)a.D + a.eps);
-                    float w[8];
-                    load4<F32>(a.norm[side[k]], e0, w);
-                    load4<F32>(a.norm[side[k]], e1, w + 4);
+                for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
+                if (a.lp > 1) ss += lane16_other<0>(ss);
+                if (a.lp > 2) ss += lane16_other<1>(ss);
+                if (a.lp > 4) ss += lane16_other<2>(ss);
+                if (a.lp > 8) ss += lane16_other<3>(ss);
+                if (a.lp > 16) ss += __shfl_xor(ss, 16);
+                if (a.lp > 32) ss += __shfl_xor(ss, 32);
+                const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_d, a.eps));   // within an ulp
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[k][e] = v[k][e] * r * w[e];
-                }
+                for (int e = 0; e < 8; ++e) v[e] *= r;
             }
-            float o[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int ex = HALF ? i : 2 * i, ey = HALF ? 4 + i : 2 * i + 1;
-                o[ex] = v[k][ex] * co[i] - v[k][ey] * si[i];
-                o[ey] = v[k][ex] * si[i] + v[k][ey] * co[i];
+                o[ex] = __builtin_fmaf(v[ex], m[i][0], -(v[ey] * m[i][1]));
+                o[ey] = __builtin_fmaf(v[ex], m[i][2], v[ey] * m[i][3]);
             }
-            if (ok[k]) {
-                const int64_t at = t * a.yts[side[k]] + hd[k] * a.yhs[side[k]];
-                store4<F32>(a.y[side[k]], at + e0, o);
-                store4<F32>(a.y[side[k]], at + e1, o + 4);
-            }
+            const int h = h0 + k * per;
+            if (in && h + slot < a.heads[side]) store8<F32, HALF>(a.y[side], at0 + h * hs, e0, e1, o);
         }
+        l0 = end;
     }
 }
 
@@ -140,11 +197,16 @@ __global__ __launch_bounds__(256) void rope_axes_kernel(RopeArgs a) {
 hipError_t launch_rope_axes(RopeArgs a, int f32, int half, int cus, hipStream_t stream) {
     a.lp = 1;
     while (a.lp * 8 < a.D) a.lp *= 2;
-    const int per = 64 / a.lp, loads = (a.heads[0] + a.heads[1] + per - 1) / per;
-    // all of a token's heads in one wave once that fills the chip (8 waves a SIMD), else one load each
-    a.chunk = a.T >= (int64_t)cus * 8 ? loads : 1;
-    const int64_t items = a.T * ((loads + a.chunk - 1) / a.chunk);
-    const dim3 grid((unsigned)((items + 3) / 4)), block(256);
+    const int per = 64 / a.lp, loads = (a.heads[0] + per - 1) / per + (a.heads[1] + per - 1) / per;
+    // A wave takes all of its token's heads where the tokens fill the chip (12
+    // waves a CU), else a share of them, U loads at the least, and works the
+    // angles out again (1024 tokens of 24 + 24 heads of 128 take 9.9 us in two
+    // or three waves a token and 11.7 in one, 32761 of 16 + 4 72.7 in two and
+    // 66.8 in one).
+    int64_t chunks = ((int64_t)cus * 12 + a.T - 1) / a.T;
+    if (chunks > (loads + U - 1) / U) chunks = (loads + U - 1) / U;
+    a.chunk = (int)((loads + chunks - 1) / chunks);
+    const dim3 grid((unsigned)((a.T + 3) / 4), (unsigned)((loads + a.chunk - 1) / a.chunk)), block(256);
     if (f32) {
         if (half) hipLaunchKernelGGL((rope_axes_kernel<1, 1>), grid, block, 0, stream, a);
         else hipLaunchKernelGGL((rope_axes_kernel<1, 0>), grid, block, 0, stream, a);

@@ -35,8 +35,12 @@ def blocks(n: int) -> int:
 def _on(t: torch.Tensor):
     """The tensor's GPU made current, if it is not."""
     if t.device.index in (None, torch.cuda.current_device()):
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.device(t.device)
+
+
+_HERE = contextlib.nullcontext()
+_F32, _BF16 = torch.float32, torch.bfloat16
 
 
 def quantize_act_fp8(x: torch.Tensor, stream=None):
@@ -44,39 +48,58 @@ def quantize_act_fp8(x: torch.Tensor, stream=None):
     row stride a multiple of 8) -> (qx E4M3 [M, K], sx fp32 [ceil(K/128), M]):
     per row and 128 channels s = max(amax / 448, 2^-120), code = e4m3(x / s)
     (include/svdq.h gives every rounding)."""
-    _check_rows(x, "x", torch.bfloat16)
+    if not (x.is_cuda and x.dtype is _BF16 and x.dim() == 2 and x.is_contiguous()):
+        _check_rows(x, "x", _BF16)              # the slow way: says what is wrong, if anything is
+        _require(x.shape[1] >= 16 and x.shape[1] % 16 == 0, f"x must have K a positive multiple of 16, got {x.shape[1]}")
+        _check_same_device(x)
     M, K = x.shape
-    _require(K >= 16 and K % 16 == 0, f"x must have K a positive multiple of 16, got {K}")
-    _check_same_device(x)
+    if K < 16 or K % 16:
+        raise ValueError(f"x must have K a positive multiple of 16, got {K}")
     ldx = x.stride(0) if M > 1 else K
     if ldx < K or ldx % 8:                      # a broadcast or unaligned row stride
         x, ldx = x.contiguous(), K
     with _on(x):
         qx = torch.empty((M, K), dtype=E4M3, device=x.device)
-        sx = torch.empty((blocks(K), M), dtype=torch.float32, device=x.device)
+        sx = torch.empty((blocks(K), M), dtype=_F32, device=x.device)
         _lib.svdq_quantize_act_fp8(x, M, K, ldx, qx, sx, stream)
     return qx, sx
 
 
 def _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, groups):
-    """Argument checks of the dense (groups 0) and the grouped product; -> M, K, N, y's dtype."""
+    """Argument checks of the dense (groups 0) and the grouped product. The
+    first condition is the usual call and costs the least; what it does not
+    pass is looked at one by one and refused with a reason."""
+    lead = (groups,) if groups else ()
+    dev = qx.device
+    if (y is None and qx.dtype is E4M3 and qw.dtype is E4M3 and sx.dtype is _F32 and sw.dtype is _F32
+            and dev.type == "cuda" and qw.device == dev and sx.device == dev and sw.device == dev
+            and qx.dim() == 2 and qw.dim() == 2 + len(lead) and qx.is_contiguous() and qw.is_contiguous()
+            and sx.is_contiguous() and sw.is_contiguous() and act in _lib.ACT
+            and (out_dtype is _BF16 or out_dtype is _F32)):
+        M, K = qx.shape
+        N = qw.shape[-2]
+        kb = blocks(K)
+        if (K >= 16 and K % 16 == 0 and N >= 1 and qw.shape == (*lead, N, K) and sx.shape == (kb, M)
+                and sw.shape == (*lead, blocks(N), kb)
+                and (bias is None or (bias.dtype is _BF16 and bias.shape == (*lead, N) and bias.is_contiguous()
+                                      and bias.device == dev))):
+            return M, K, N, out_dtype
     _check_rows(qx, "qx", E4M3)
     _require(qx.is_contiguous(), "qx must be contiguous [M, K]")
     M, K = qx.shape
     _require(K >= 16 and K % 16 == 0, f"qx must have K a positive multiple of 16, got {K}")
-    lead = (groups,) if groups else ()
-    _require(qw.dim() == 2 + len(lead) and qw.dtype == E4M3 and qw.is_contiguous() and qw.shape[-1] == K,
-             f"qw must be contiguous E4M3 {[*lead, 'N', K]}, got {tuple(qw.shape)} {qw.dtype}")
+    _require(qw.dim() == 2 + len(lead) and qw.dtype == E4M3 and qw.is_contiguous() and qw.shape[-1] == K
+             and qw.shape[:-2] == lead, f"qw must be contiguous E4M3 {[*lead, 'N', K]}, got {tuple(qw.shape)} {qw.dtype}")
     N = qw.shape[-2]
     _require(N >= 1, "qw must have at least one output row")
-    _require(tuple(sx.shape) == (blocks(K), M) and sx.dtype == torch.float32
+    _require(tuple(sx.shape) == (blocks(K), M) and sx.dtype == _F32
              and (sx.is_contiguous() or sx.numel() <= 1),
              f"sx must be contiguous fp32 [{blocks(K)}, {M}], got {tuple(sx.shape)} {sx.dtype}")
     want = (*lead, blocks(N), blocks(K))
-    _require(tuple(sw.shape) == want and sw.dtype == torch.float32 and sw.is_contiguous(),
+    _require(tuple(sw.shape) == want and sw.dtype == _F32 and sw.is_contiguous(),
              f"sw must be contiguous fp32 {list(want)}, got {tuple(sw.shape)} {sw.dtype}")
     if bias is not None:
-        _require(tuple(bias.shape) == (*lead, N) and bias.dtype == torch.bfloat16 and bias.is_contiguous(),
+        _require(tuple(bias.shape) == (*lead, N) and bias.dtype == _BF16 and bias.is_contiguous(),
                  f"bias must be contiguous bf16 {[*lead, N]}, got {tuple(bias.shape)} {bias.dtype}")
     _require(act in _lib.ACT, f"act must be one of {sorted(_lib.ACT)}, got {act!r}")
     if y is not None:
@@ -84,13 +107,16 @@ def _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, groups):
         _require(y.dim() == 2 and tuple(y.shape) == (M, N) and (y.stride(1) == 1 or N == 1)
                  and (y.stride(0) >= N or M <= 1),
                  f"y must be [{M}, {N}] with contiguous columns and rows that do not overlap")
-    _require(out_dtype in (torch.bfloat16, torch.float32), f"y must be bf16 or fp32, got {out_dtype}")
+    _require(out_dtype in (_BF16, _F32), f"y must be bf16 or fp32, got {out_dtype}")
     _check_same_device(qx, sx=sx, qw=qw, sw=sw, bias=bias, y=y)
     return M, K, N, out_dtype
 
 
-def _row_stride(y, N):
-    return y.stride(0) if y.shape[0] > 1 else N
+def _output(y, M, N, out_dtype, dev):
+    """(y, its row stride)"""
+    if y is None:
+        return torch.empty((M, N), dtype=out_dtype, device=dev), N
+    return y, y.stride(0) if M > 1 else N
 
 
 def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfloat16, y=None, stream=None):
@@ -100,10 +126,8 @@ def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfl
     or fp32; rows of a given y may be strided)."""
     M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, 0)
     with _on(qx):
-        if y is None:
-            y = torch.empty((M, N), dtype=out_dtype, device=qx.device)
-        _lib.svdq_gemm_fp8(qx, sx, M, K, qw, sw, N, bias, _lib.ACT[act], y, int(out_dtype == torch.float32),
-                           _row_stride(y, N), stream)
+        y, ldy = _output(y, M, N, out_dtype, qx.device)
+        _lib.svdq_gemm_fp8(qx, sx, M, K, qw, sw, N, bias, _lib.ACT[act], y, int(out_dtype is _F32), ldy, stream)
     return y
 
 
@@ -114,16 +138,17 @@ def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", ou
     the GPU, rising, within [0, M] (read there: no synchronisation). Rows of
     no group (before offsets[0], from offsets[-1] on) are left as they are in
     a given y and are unspecified in a new one."""
-    _require(offsets.dim() == 1 and offsets.numel() >= 2 and offsets.dtype == torch.int32 and offsets.is_contiguous(),
-             f"offsets must be a contiguous int32 vector of groups + 1 values, got {tuple(offsets.shape)} {offsets.dtype}")
+    if not (offsets.dtype is torch.int32 and offsets.dim() == 1 and offsets.numel() >= 2 and offsets.is_contiguous()):
+        raise ValueError(f"offsets must be a contiguous int32 vector of groups + 1 values, got {tuple(offsets.shape)} "
+                         f"{offsets.dtype}")
     groups = offsets.numel() - 1
     M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, groups)
-    _check_same_device(qx, offsets=offsets)
+    if offsets.device != qx.device:
+        raise ValueError(f"offsets is on {offsets.device}, expected {qx.device}")
     with _on(qx):
-        if y is None:
-            y = torch.empty((M, N), dtype=out_dtype, device=qx.device)
+        y, ldy = _output(y, M, N, out_dtype, qx.device)
         _lib.svdq_gemm_fp8_grouped(qx, sx, M, K, qw, sw, N, offsets, groups, bias, _lib.ACT[act], y,
-                                   int(out_dtype == torch.float32), _row_stride(y, N), stream)
+                                   int(out_dtype is _F32), ldy, stream)
     return y
 
 
@@ -151,7 +176,8 @@ class Fp8Linear:
                  stream=None) -> torch.Tensor:
         """Y [M, N] for bf16 activations x [M, K]: the activation pass, then
         the product, on one stream."""
-        _require(x.dim() == 2 and x.shape[1] == self.K, f"x must be [M, {self.K}], got {tuple(x.shape)}")
+        if x.dim() != 2 or x.shape[1] != self.K:
+            raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
         qx, sx = quantize_act_fp8(x, stream)
         return fp8_linear(qx, sx, self.qw, self.sw, self.bias, act, out_dtype, y, stream)
 
@@ -184,7 +210,9 @@ class Fp8GroupedLinear:
                  stream=None) -> torch.Tensor:
         """Y [M, N] for bf16 activations x [M, K] sorted by group
         (fp8_grouped_linear's offsets)."""
-        _require(x.dim() == 2 and x.shape[1] == self.K, f"x must be [M, {self.K}], got {tuple(x.shape)}")
-        _require(offsets.numel() == self.groups + 1, f"offsets must hold {self.groups + 1} values")
+        if x.dim() != 2 or x.shape[1] != self.K:
+            raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
+        if offsets.numel() != self.groups + 1:
+            raise ValueError(f"offsets must hold {self.groups + 1} values, got {offsets.numel()}")
         qx, sx = quantize_act_fp8(x, stream)
         return fp8_grouped_linear(qx, sx, offsets, self.qw, self.sw, self.bias, act, out_dtype, y, stream)

@@ -17,7 +17,7 @@ from typing import Sequence
 import torch
 
 from . import _lib
-from ._lib import RopeHeads, _check_same_device, _require
+from ._lib import RopeHeads, _require
 from .fp8 import _on
 
 PAIRING = {"interleaved": 0, "half": 1}
@@ -58,21 +58,26 @@ class RopePlan:
 
 
 def _heads(x, name, D):
-    _require(x.dim() == 3 and x.shape[2] == D, f"{name} must be [T, heads, {D}], got {tuple(x.shape)}")
-    _require(x.stride(2) == 1, f"{name} must have contiguous heads (stride(2) == 1)")
+    if x.dim() != 3 or x.shape[2] != D:
+        raise ValueError(f"{name} must be [T, heads, {D}], got {tuple(x.shape)}")
+    if x.stride(2) != 1:
+        raise ValueError(f"{name} must have contiguous heads (stride(2) == 1)")
 
 
-def _strides(x):
+def _strides(x, T, H, D):
     """Token and head stride; an axis of one element has none of its own."""
-    T, H, D = x.shape
-    hs = x.stride(1) if H > 1 else D
-    return (x.stride(0) if T > 1 else max(H * hs, D)), hs
+    ts, hs, _ = x.stride()
+    if H == 1:
+        hs = D
+    return (ts if T > 1 else H * hs), hs
 
 
-def _side(x, y, norm):
-    ts, hs = _strides(x)
-    yts, yhs = _strides(y)
-    return RopeHeads(x.data_ptr(), ts, hs, x.shape[1], None if norm is None else norm.data_ptr(), y.data_ptr(), yts, yhs)
+def _side(x, y, norm, T, H, D):
+    ts, hs = _strides(x, T, H, D)
+    yts, yhs = (H * D, D) if y is None else _strides(y, T, H, D)
+    if y is None:
+        y = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    return y, RopeHeads(x.data_ptr(), ts, hs, H, None if norm is None else norm.data_ptr(), y.data_ptr(), yts, yhs)
 
 
 def rope_axes(q, k, pos, plan: RopePlan, q_norm=None, k_norm=None, eps: float = 1e-6, inverse: bool = False,
@@ -83,33 +88,41 @@ def rope_axes(q, k, pos, plan: RopePlan, q_norm=None, k_norm=None, eps: float = 
     is given: (q', k'), or q' alone if k is None. q_out / k_out may be q / k
     themselves (in place) or buffers of any such layout. inverse undoes the
     rotation; without a norm it is also its gradient."""
-    D = plan.head_dim
+    D, dt, dev = plan.head_dim, q.dtype, q.device
     _heads(q, "q", D)
-    T = q.shape[0]
-    _require(q.dtype in (torch.bfloat16, torch.float32), f"q must be bf16 or fp32, got {q.dtype}")
-    _require(q.shape[1] >= 1, "q must have at least one head")
-    sides = [("q", q, q_norm, q_out)]
+    T, hq, _ = q.shape
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise ValueError(f"q must be bf16 or fp32, got {dt}")
+    if hq < 1:
+        raise ValueError("q must have at least one head")
+    hk = 0
     if k is not None:
         _heads(k, "k", D)
-        _require(k.shape[0] == T and k.dtype == q.dtype, f"k must have {T} tokens of {q.dtype}, got {tuple(k.shape)} {k.dtype}")
-        sides.append(("k", k, k_norm, k_out))
-    else:
-        _require(k_norm is None and k_out is None, "k_norm and k_out need k")
-    for name, x, norm, out in sides:
-        if norm is not None:
-            _require(tuple(norm.shape) == (D,) and norm.dtype == q.dtype and norm.is_contiguous(),
-                     f"{name}_norm must be a contiguous {q.dtype} vector of {D} values")
+        hk = k.shape[1]
+        if k.shape[0] != T or k.dtype is not dt:
+            raise ValueError(f"k must have {T} tokens of {dt}, got {tuple(k.shape)} {k.dtype}")
+    elif k_norm is not None or k_out is not None:
+        raise ValueError("k_norm and k_out need k")
+    for name, x, norm, out in (("q", q, q_norm, q_out), ("k", k, k_norm, k_out)):
+        if norm is not None and not (norm.dtype is dt and norm.shape == (D,) and norm.is_contiguous()):
+            raise ValueError(f"{name}_norm must be a contiguous {dt} vector of {D} values")
         if out is not None:
             _heads(out, f"{name}_out", D)
-            _require(out.shape == x.shape and out.dtype == q.dtype, f"{name}_out must be {tuple(x.shape)} {q.dtype}")
-    _require(tuple(pos.shape) == (T, plan.axes) and pos.dtype in (torch.int32, torch.float32) and pos.is_contiguous(),
-             f"pos must be contiguous int32 or fp32 [{T}, {plan.axes}], got {tuple(pos.shape)} {pos.dtype}")
-    _check_same_device(q, k=k, pos=pos, q_norm=q_norm, k_norm=k_norm, q_out=q_out, k_out=k_out, plan=plan.turns)
+            if out.shape != x.shape or out.dtype is not dt:
+                raise ValueError(f"{name}_out must be {tuple(x.shape)} {dt}")
+    f32_pos = pos.dtype is torch.float32
+    if not ((f32_pos or pos.dtype is torch.int32) and pos.shape == (T, plan.axes) and pos.is_contiguous()):
+        raise ValueError(f"pos must be contiguous int32 or fp32 [{T}, {plan.axes}], got {tuple(pos.shape)} {pos.dtype}")
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU device, got {dev}")
+    for t in (k, pos, q_norm, k_norm, q_out, k_out, plan.turns):
+        if t is not None and t.device != dev:
+            raise ValueError(f"a tensor or the plan is on {t.device}, expected {dev}")
     with _on(q):
-        outs = [torch.empty((T, x.shape[1], D), dtype=q.dtype, device=q.device) if out is None else out
-                for _, x, _, out in sides]
-        structs = [_side(x, o, norm) for (_, x, norm, _), o in zip(sides, outs)]
-        _lib.svdq_rope_axes(structs[0], structs[1] if k is not None else None, T, D, int(q.dtype == torch.float32),
-                            pos, int(pos.dtype == torch.float32), plan.axes, plan.turns, plan.axis, plan.pairs,
-                            PAIRING[plan.pairing], int(inverse), eps, stream)
-    return (outs[0], outs[1]) if k is not None else outs[0]
+        q_out, qs = _side(q, q_out, q_norm, T, hq, D)
+        ks = None
+        if k is not None:
+            k_out, ks = _side(k, k_out, k_norm, T, hk, D)
+        _lib.svdq_rope_axes(qs, ks, T, D, int(dt is torch.float32), pos, int(f32_pos), plan.axes, plan.turns, plan.axis,
+                            plan.pairs, PAIRING[plan.pairing], int(inverse), eps, stream)
+    return q_out if k is None else (q_out, k_out)

@@ -357,3 +357,16 @@ def test_joint_block_input_in_eight_bits():
         bound = 2 * rel_in * np.abs(np64(w)).max() * math.sqrt(D) + (2.0 ** -8 + 2.0 ** -15) * np.linalg.norm(want, axis=2)
         assert (err <= bound).all(), f"worst ratio {(err / bound).max():.3g}"
     check_product(v.reshape(T, -1), [r[:, (H + HK) * D:] for r in ref], K)
+
+
+def test_quantize_act_every_maximum():
+    """Every finite bf16 magnitude as a block's maximum: the scale's division
+    and its reciprocal are rounded correctly, and the codes follow."""
+    note("quantize_act_fp8 every maximum")
+    amax = torch.arange(0x7F80, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = torch.zeros((amax.numel(), 128), dtype=torch.bfloat16)
+    part = torch.tensor([1.0, -0.7, 0.33, -0.051, 0.0077, 1e-3, 1e-5], dtype=torch.float64)
+    x[:, 3:10] = (amax.double()[:, None] * part).to(torch.bfloat16)
+    q, s = svdq.quantize_act_fp8(x.cuda())
+    qo, so = ofp8.quantize_act(x.double().numpy())
+    assert np.array_equal(s.cpu().numpy(), so) and np.array_equal(np64(q), qo)
