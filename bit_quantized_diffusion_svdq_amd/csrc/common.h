@@ -137,14 +137,3 @@ DEV int mx_block_exponent(float amax) {
 
 // 2^-e for an E8M0 exponent e in [-127, 127], exact
 DEV float mx_inv_scale(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
-
-// The value of another lane of the same 16 (a VALU operand path, no LDS):
-// step 0 lane ^ 1, 1 lane ^ 2, 2 mirrored in its 8, 3 mirrored in its 16. A
-// reduction that takes steps 0 .. s leaves every lane of 2^(s + 1) the same
-// result (after step i all lanes of 2^(i + 1) agree, so mirroring is as good
-// as an xor).
-template <int STEP>
-DEV float lane16_other(float v) {
-    constexpr int ctrl = STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : STEP == 2 ? 0x141 : 0x140;
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, true));
-}

@@ -190,19 +190,22 @@ DEV void store4(const Args& a, int64_t row, int col, const float* v) {
 
 // ---------------------------------------------------------------- tiles
 
-// BM x BN outputs per workgroup, WGM x WGN waves of (16 TM) x (16 TN) each;
-// PREC 0: E4M3 matrix instructions, 1: exact products on the bf16 ones
-template <int TM_, int TN_, int WGM_, int WGN_, int WPE_, int PREC_, int MID_ = (TM_ > 2 ? TM_ / 2 : 0)>
+// BM x BN outputs per workgroup, WGM x WGN waves of (16 TM) x (16 TN) each, S
+// slots (blocks of K in LDS or on their way). PREC 0: E4M3 matrix
+// instructions, 1: exact products on the bf16 ones. WPE: waves per SIMD the
+// registers are kept for. MID: where W's slot is given back (see block()).
+template <int TM_, int TN_, int WGM_, int WGN_, int WPE_, int PREC_, int MID_, int S_>
 struct Cfg {
-    static constexpr int TM = TM_, TN = TN_, WGM = WGM_, WGN = WGN_, WPE = WPE_, PREC = PREC_, MID = MID_;
+    static constexpr int TM = TM_, TN = TN_, WGM = WGM_, WGN = WGN_, WPE = WPE_, PREC = PREC_, MID = MID_, S = S_;
     static constexpr int BM = 16 * TM * WGM, BN = 16 * TN * WGN;
     static constexpr int NW = WGM * WGN, NT = 64 * NW;
     static constexpr int XL = BM / 8, WL = BN / 8;                // 8-row loads per block of K
     static constexpr int XP = (XL + NW - 1) / NW, WP = (WL + NW - 1) / NW, SP = (BM + 63) / 64;
     static_assert(128 % (TN * 16) == 0, "a wave's outputs share one weight scale");
+    static_assert(NW % 2 == 0, "a wave's loads have one parity");
     static_assert(SP <= NW, "one load of 64 row scales per wave");
     static constexpr int XSLOT = BM * 128 + SP * 256, WSLOT = BN * 128;
-    static_assert(2 * (XSLOT + WSLOT) * WPE * 4 / NW <= 160 * 1024, "LDS budget");
+    static_assert(S >= 2 && S <= 4 && S * (XSLOT + WSLOT) * WPE * 4 / NW <= 160 * 1024, "LDS budget");
 };
 
 DEV void dma16(rsrc_t r, char* lds, int voff, int soff) {
@@ -215,16 +218,21 @@ DEV void dma4(rsrc_t r, char* lds, int voff, int soff) {
 template <class C, bool GROUPED>
 __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
     constexpr int BM = C::BM, BN = C::BN, TM = C::TM, TN = C::TN, NW = C::NW;
-    // two slots of X's rows and row scales and two of W's rows, each a block of
-    // K; separate objects, so that the compiler waits only for loads into the
-    // one it reads
-    __shared__ __attribute__((aligned(16))) char xs0[C::XSLOT];
-    __shared__ __attribute__((aligned(16))) char xs1[C::XSLOT];
-    __shared__ __attribute__((aligned(16))) char ws0[C::WSLOT];
-    __shared__ __attribute__((aligned(16))) char ws1[C::WSLOT];
+    // S slots of X's rows and row scales and S of W's rows, each a block of K;
+    // separate objects, so that the compiler waits only for loads into the one
+    // it reads
+    constexpr int S = C::S, XB = C::XSLOT, WB = C::WSLOT;
+    __shared__ __attribute__((aligned(16))) char xs0[XB], xs1[XB], xs2[S > 2 ? XB : 16], xs3[S > 3 ? XB : 16];
+    __shared__ __attribute__((aligned(16))) char ws0[WB], ws1[WB], ws2[S > 2 ? WB : 16], ws3[S > 3 ? WB : 16];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / C::WGN, wn = wave % C::WGN;
+    auto xslot = [&](int s) __attribute__((always_inline)) {
+        return s % S == 0 ? xs0 : s % S == 1 ? xs1 : s % S == 2 ? xs2 : xs3;
+    };
+    auto wslot = [&](int s) __attribute__((always_inline)) {
+        return s % S == 0 ? ws0 : s % S == 1 ? ws1 : s % S == 2 ? ws2 : ws3;
+    };
     const int tiles_n = (a.N + BN - 1) / BN;
     Rows rr;
     int tn;
@@ -281,7 +289,9 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
     const int nb = (n0 + wn * TN * 16) / 128;
     const float* swp = a.sw + ((int64_t)rr.g * NB + (nb < NB ? nb : NB - 1)) * KB;
     float sw64 = 0.0f;
+    int sw0 = 0;                                                   // the block of lane 0
     auto load_sw = [&](int kb) __attribute__((always_inline)) {
+        sw0 = kb;
         sw64 = kb + lane < KB ? swp[kb + lane] : 0.0f;
         order_point(sw64);           // waited for here, not among the loads in flight later
     };
@@ -324,27 +334,30 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
     // sixteen FMAs take 16.6 a piece).
     //
     // Two meetings of the waves. At row block MID everybody has W's operands
-    // of this block in registers, so W of block kb + 2 starts on its way into
+    // of this block in registers, so W of block kb + S starts on its way into
     // their slot. At the last row block nobody reads X's slot any more: block
-    // kb + 1 has landed (all but the WP loads of W just begun), its first
-    // operands are read as this block's are used up, and X of block kb + 2
+    // kb + 1 has landed (all but the loads begun after its own, AHEAD), its
+    // first operands are read as this block's are used up, and X of block kb + S
     // starts. Loads go out one at a time between the MFMAs: in a burst they
     // hold the waves up at the vector memory unit.
     constexpr int MID = C::MID, PX = (MID + 1) * TN, PW_ = (TM - 1 - MID) * TN;   // places for loads of X and W
     static_assert(MID >= 0 && MID <= TM - 2, "the meetings follow each other");
     constexpr int GAP = PW_ >= 2 * C::WP && PX >= 2 * XN ? 2 : 1;                 // a load at every GAP-th place,
     constexpr int NX = (XN + PX - 1) / PX, NWL = (C::WP + PW_ - 1) / PW_;         // or several at each
+    constexpr int AHEAD = C::WP + (S - 2) * (C::WP + XN);
     auto meet = [&](bool all) __attribute__((always_inline)) {
         if (all) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(C::WP) : "memory");
+        else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(AHEAD) : "memory");
         lds_barrier();
     };
     v4f p[2][TN];
     float sp[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < TN; ++j) p[0][j] = p[1][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    auto block = [&](char* xs, char* ws, char* nxs, char* nws, int kb, int par0) __attribute__((always_inline)) {
-        const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw64), kb & 63));
+    auto block = [&](int s, int kb, int par0) __attribute__((always_inline)) {
+        char *const xs = xslot(s), *const nxs = xslot(s + 1), *const pxs = xslot(s + S - 1);
+        char *const ws = wslot(s), *const nws = wslot(s + 1);
+        const float sw = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw64), kb - sw0));
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int par = (par0 + i) & 1, before = (i + TM - 1) % TM;
@@ -366,14 +379,14 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
                 for (int u = 0; u < NX; ++u) {
                     const int d = ax / GAP * NX + u;
                     if (ax % GAP == 0 && d < XN) {
-                        if (i + 1 == TM) load_x(xs, kb + 2, d);
-                        else load_x(nxs, kb + 1, d);
+                        if (i + 1 == TM) load_x(xs, kb + S, d);
+                        else load_x(pxs, kb + S - 1, d);
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < NWL; ++u) {
                     const int d = aw / GAP * NWL + u;
-                    if (aw >= 0 && aw % GAP == 0 && d < C::WP && i + 1 < TM) load_w(ws, kb + 2, d);
+                    if (aw >= 0 && aw % GAP == 0 && d < C::WP && i + 1 < TM) load_w(ws, kb + S, d);
                 }
                 if (i + 1 == TM) read_w(nws, j);
                 __builtin_amdgcn_sched_barrier(0);
@@ -381,31 +394,36 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
         }
     };
 
-    // Blocks run in pairs, which keeps the loop free of branches; blocks past
-    // the end of K are zeros.
+    // Blocks run S (or twice an odd S) at a time, which keeps the loop free of
+    // branches; blocks past the end of K are zeros.
 #pragma unroll
     for (int d = 0; d < XN; ++d) load_x(xs0, 0, d);
 #pragma unroll
-    for (int d = 0; d < C::WP; ++d) load_w(ws0, 0, d);
+    for (int s = 0; s < S; ++s) {
 #pragma unroll
-    for (int d = 0; d < C::WP; ++d) load_w(ws1, 1, d);
+        for (int d = 0; d < C::WP; ++d) load_w(wslot(s), s, d);
+#pragma unroll
+        for (int d = 0; d < XN; ++d)
+            if (s > 0 && s + 1 < S) load_x(xslot(s), s, d);
+    }
     meet(false);
     read_x(xs0, 0, 0);
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
 #pragma unroll
         for (int u = 0; u < NX; ++u)
-            if (j % GAP == 0 && j / GAP * NX + u < XN) load_x(xs1, 1, j / GAP * NX + u);
+            if (j % GAP == 0 && j / GAP * NX + u < XN) load_x(xslot(S - 1), S - 1, j / GAP * NX + u);
         read_w(ws0, j);
     }
-    for (int kb = 0; kb < KB; kb += 2) {
-        if ((kb & 63) == 0) load_sw(kb);
-        block(xs0, ws0, xs1, ws1, kb, 0);
-        block(xs1, ws1, xs0, ws0, kb + 1, TM & 1);
+    constexpr int TURN = TM % 2 && S % 2 ? 2 * S : S;              // (the registers' roles repeat after these)
+    for (int kb = 0; kb < KB; kb += TURN) {
+        if (kb == 0 || kb - sw0 + TURN > 64) load_sw(kb);
+#pragma unroll
+        for (int s = 0; s < TURN; ++s) block(s, kb + s, s * TM & 1);
     }
     meet(true);                                          // (the last products are complete)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) fmac(acc[TM - 1][j], p[(2 * TM - 1) & 1][j], sp[(2 * TM - 1) & 1]);
+    for (int j = 0; j < TN; ++j) fmac(acc[TM - 1][j], p[(TURN * TM - 1) & 1][j], sp[(TURN * TM - 1) & 1]);
 
     // ---- outputs: activation in registers, one rounding, then through
     // LDS (free now) so that rows leave as 16-byte stores of whole lines. The
@@ -584,19 +602,25 @@ void launch_few(const Args& a, hipStream_t stream) {
 // One estimate per variant, in microseconds, from times measured on MI355X at
 // K = 4096 (32 blocks of 128; a launch of nothing takes 3):
 //  - tiles: `lone` per block of K with one workgroup on a CU, `full` with
-//    `per_cu` (its memory latency hidden by the others, the CU's pipes
-//    shared). Large tiles move fewer bytes and read LDS less per product:
+//    `per_cu`. Large tiles move fewer bytes and read LDS less per product:
 //    4096 x 4096 x 8192 takes 121 us with 256 x 256, 132 with 192 x 256, 143
-//    with 128 x 128, 184 with 64 x 128, 223 with 64 x 64. Which one wins is
-//    decided by how its tiles fill rounds of the CUs: 4608 x 12288 x 4096 takes
-//    211 us with 160 x 256 (1.8 rounds) and 272 with 256 x 256 (1.1), 4608 x
-//    4096 x 12288 208 with 224 x 256 (3.9 rounds), 233 with 160 x 256; 256 x
-//    4096 x 4096 takes 13 with 64 x 64 (256 tiles), 19 with 128 x 128 (64).
-//  - few rows: bound by the weights from memory (5.2 bytes a picosecond), the
-//    operands from L2 (8.4, short of 256 workgroups less) or the trips of a
-//    wave's loads (2.2 each). 1 x 4096 x 18432 takes 17 us (best tile 22),
-//    64 x 4096 x 4096 10.5 (13), 128 x 12288 x 4096 38 (46), but 64 x 4096 x 12288
-//    26 (20).
+//    with 128 x 128 (two a CU), 184 with 64 x 128, 223 with 64 x 64. Which one
+//    wins is decided by how its tiles fill rounds of the CUs: 4608 x 12288 x 4096
+//    takes 211 us with 160 x 256 (1.8 rounds) and 272 with 256 x 256 (1.1),
+//    4608 x 4096 x 12288 208 with 224 x 256 (3.9 rounds) and 233 with 160 x
+//    256. Where the tiles do not fill the CUs once, memory latency counts, and
+//    the small ones keep three or four slots: 256 x 4096 x 4096 takes 11.6 with
+//    64 x 64 (256 tiles; 13.2 with two slots), 19.3 with 128 x 128 (64 tiles);
+//    256 x 12288 x 4096 34 (46 with two slots); 1024 x 4096 x 4096 22 with
+//    128 x 128 in eight waves and four slots, 23.5 in four waves and two, two
+//    workgroups a CU, which take 512 x 4096 x 12288 in 37 (44 the other way,
+//    33 with 256 x 128). Weights that are read once come at 4.3 MB a us.
+//  - few rows: bound by the weights from memory (6.5 MB a us), the operands
+//    from L2 (8.4, less with fewer workgroups than CUs) or the trips of a
+//    wave's loads (2.2 us each, and 4 for a workgroup's start and end where
+//    they come in turns). 1 x 4096 x 18432 takes 17 us (best tile 19), 64 x
+//    12288 x 4096 28 (35), but 64 x 4096 x 12288 26 (15); 48 rows of 32 groups x
+//    2048 x 4096 35 with 32 columns a workgroup, 53 with 16, 38 in tiles.
 struct Variant {
     int rows, cols, few;             // outputs per workgroup; few: the few-rows kernel
     int per_cu, trip;                // workgroups on a CU; K blocks per trip of a few-rows workgroup
@@ -606,8 +630,8 @@ struct Variant {
 constexpr Variant kVariants[] = {
     {256, 256, 0, 1, 0, 1.20, 1.81}, {224, 256, 0, 1, 0, 1.07, 1.63}, {192, 256, 0, 1, 0, 0.94, 1.38},
     {160, 256, 0, 1, 0, 0.85, 1.21}, {256, 128, 0, 1, 0, 0.75, 0.98}, {128, 128, 0, 2, 0, 0.60, 1.07},
-    {64, 128, 0, 3, 0, 0.46, 1.05},  {64, 64, 0, 4, 0, 0.40, 0.86},   {16, 16, 1, 4, 32, 0, 0},
-    {16, 32, 1, 4, 16, 0, 0},        {32, 32, 1, 4, 16, 0, 0},        {32, 64, 1, 4, 16, 0, 0},
+    {128, 128, 0, 1, 0, 0.50, 0.60}, {64, 128, 0, 2, 0, 0.42, 0.76},  {64, 64, 0, 2, 0, 0.30, 0.44},
+    {16, 16, 1, 4, 32, 0, 0},        {16, 32, 1, 4, 16, 0, 0},        {32, 32, 1, 4, 16, 0, 0},
 };
 
 double estimate(const Variant& v, const Args& a, int cus) {
@@ -619,16 +643,19 @@ double estimate(const Variant& v, const Args& a, int cus) {
     const double tiles = tm * tn;
     if (v.few) {
         const double rows = a.M < v.rows * tm ? (double)a.M / tm : v.rows;
-        const double weights = active * a.N * (double)a.K / 5.2e6;
+        const double weights = active * a.N * (double)a.K / 6.5e6;
         const double reads = tiles * (v.cols + rows) * (double)a.K / 8.4e6 * (tiles < cus ? cus / tiles : 1.0);
-        const double trips = 2.2 * __builtin_ceil(kb / v.trip) * __builtin_ceil(tiles / (4.0 * cus));
+        const double turns = tiles / ((double)v.per_cu * cus);
+        const double trips = (4.0 * (turns > 1.0) + 2.2 * __builtin_ceil(kb / v.trip)) * (turns > 1.0 ? turns : 1.0);
         double t = weights > reads ? weights : reads;
         return 3.0 + (t > trips ? t : trips);
     }
     const double slots = (double)cus * v.per_cu, rounds = __builtin_floor(tiles / slots);
     const double rest = __builtin_ceil((tiles - rounds * slots) / cus);
     const double share = v.full * rest / v.per_cu, out = 4.0 * v.rows * v.cols * v.per_cu / 65536.0;
-    return 3.0 + rounds * (kb * v.full + out) + (rest > 0 ? kb * (share > v.lone ? share : v.lone) + out * rest / v.per_cu : 0.0);
+    const double t = rounds * (kb * v.full + out) + (rest > 0 ? kb * (share > v.lone ? share : v.lone) + out * rest / v.per_cu : 0.0);
+    const double weights = active * a.N * (double)a.K / 4.3e6;
+    return 3.0 + (t > weights ? t : weights);
 }
 
 // lanes of a launch stay below 2^32
@@ -643,24 +670,24 @@ bool launch_variant(const Args& a, int cus, hipStream_t stream) {
     double least = 0.0;
     for (int i = 0; i < (int)(sizeof kVariants / sizeof kVariants[0]); ++i) {
         // fp32 outputs have the two tile sizes whose operands fit the registers when widened
-        if (PREC == 1 && i < 8 && i != 5 && i != 7) continue;
+        if (PREC == 1 && i < 9 && i != 5 && i != 8) continue;
         if (!fits(kVariants[i], a)) continue;
         const double t = estimate(kVariants[i], a, cus);
         if (best < 0 || t < least) best = i, least = t;
     }
     switch (best) {
-        case 0: if constexpr (PREC == 0) launch_tiles<Cfg<8, 4, 2, 4, 2, 0, 3>, GROUPED>(a, stream); break;
-        case 1: if constexpr (PREC == 0) launch_tiles<Cfg<7, 4, 2, 4, 2, 0, 3>, GROUPED>(a, stream); break;
-        case 2: if constexpr (PREC == 0) launch_tiles<Cfg<6, 4, 2, 4, 2, 0, 2>, GROUPED>(a, stream); break;
-        case 3: if constexpr (PREC == 0) launch_tiles<Cfg<5, 4, 2, 4, 2, 0, 2>, GROUPED>(a, stream); break;
-        case 4: if constexpr (PREC == 0) launch_tiles<Cfg<4, 4, 4, 2, 2, 0, 2>, GROUPED>(a, stream); break;
-        case 5: launch_tiles<Cfg<4, 4, 2, 2, 2, PREC, 2>, GROUPED>(a, stream); break;
-        case 6: if constexpr (PREC == 0) launch_tiles<Cfg<2, 4, 2, 2, 2, 0, 0>, GROUPED>(a, stream); break;
-        case 7: launch_tiles<Cfg<2, 2, 2, 2, 2, PREC, 0>, GROUPED>(a, stream); break;
-        case 8: launch_few<FewCfg<1, 1, 8, 4, PREC>, GROUPED>(a, stream); break;
-        case 9: launch_few<FewCfg<1, 2, 8, 2, PREC>, GROUPED>(a, stream); break;
-        case 10: launch_few<FewCfg<2, 2, 8, 2, PREC>, GROUPED>(a, stream); break;
-        case 11: launch_few<FewCfg<2, 4, 8, 2, PREC>, GROUPED>(a, stream); break;
+        case 0: if constexpr (PREC == 0) launch_tiles<Cfg<8, 4, 2, 4, 2, 0, 3, 2>, GROUPED>(a, stream); break;
+        case 1: if constexpr (PREC == 0) launch_tiles<Cfg<7, 4, 2, 4, 2, 0, 3, 2>, GROUPED>(a, stream); break;
+        case 2: if constexpr (PREC == 0) launch_tiles<Cfg<6, 4, 2, 4, 2, 0, 2, 2>, GROUPED>(a, stream); break;
+        case 3: if constexpr (PREC == 0) launch_tiles<Cfg<5, 4, 2, 4, 2, 0, 2, 2>, GROUPED>(a, stream); break;
+        case 4: if constexpr (PREC == 0) launch_tiles<Cfg<4, 4, 4, 2, 2, 0, 2, 2>, GROUPED>(a, stream); break;
+        case 5: launch_tiles<Cfg<4, 4, 2, 2, 2, PREC, 2, 2>, GROUPED>(a, stream); break;
+        case 6: if constexpr (PREC == 0) launch_tiles<Cfg<2, 4, 4, 2, 2, 0, 0, 4>, GROUPED>(a, stream); break;
+        case 7: if constexpr (PREC == 0) launch_tiles<Cfg<2, 4, 2, 2, 2, 0, 0, 3>, GROUPED>(a, stream); break;
+        case 8: launch_tiles<Cfg<2, 2, 2, 2, 2, PREC, 0, 4>, GROUPED>(a, stream); break;
+        case 9: launch_few<FewCfg<1, 1, 8, 4, PREC>, GROUPED>(a, stream); break;
+        case 10: launch_few<FewCfg<1, 2, 8, 2, PREC>, GROUPED>(a, stream); break;
+        case 11: launch_few<FewCfg<2, 2, 8, 2, PREC>, GROUPED>(a, stream); break;
         default: return false;
     }
     return true;

@@ -16,7 +16,7 @@
 // contiguous run per block instead of one 4-byte store per row. Maxima are
 // taken on the bf16 bits, two at a time, and across lanes without LDS; with
 // that 4608 x 12288 went from 37.4 to 34.6 us, 4.9 TB/s (a plain copy: 5.5).
-#include "common.h"
+#include "lanes.h"
 
 namespace {
 

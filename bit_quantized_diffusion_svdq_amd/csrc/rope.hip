@@ -23,7 +23,7 @@
 // rotation, uniform sides and the hardware's reciprocal root took 4608 tokens
 // of 24 + 24 heads of 128 (normed) from 47.6 to 27.1 us, 4.2 TB/s; 32761 of
 // 16 + 4 without a norm run in 66.8 us, 5.0 TB/s (a plain copy: 5.5).
-#include "common.h"
+#include "lanes.h"
 #include "rope.h"
 
 namespace {

@@ -34,9 +34,7 @@ def blocks(n: int) -> int:
 
 def _on(t: torch.Tensor):
     """The tensor's GPU made current, if it is not."""
-    if t.device.index in (None, torch.cuda.current_device()):
-        return _HERE
-    return torch.cuda.device(t.device)
+    return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
 _HERE = contextlib.nullcontext()
