@@ -21,7 +21,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from .fp8 import Fp8GroupedLinear
+from .fp8 import Fp8GroupedLinear, _on
 from .graph import CapturedSequence
 from .rope import RopePlan, rope_axes
 
@@ -169,10 +169,10 @@ class FusedQKV:
         sorted by stream); y: the buffer for the projection, bf16 [M, N]."""
         grouped = isinstance(self.layer, Fp8GroupedLinear)
         _lib._require(grouped == (offsets is not None), "offsets belong to a grouped layer, and it needs them")
-        y = self.layer(x, offsets, y=y, stream=stream) if grouped else self.layer(x, y=y, stream=stream)
-        _lib._require(y.dtype == torch.bfloat16, f"y must be bf16, got {y.dtype}")
-        M, D = y.shape[0], self.plan.head_dim
-        h = y.unflatten(1, (self.heads + 2 * self.kv_heads, D))
-        q, k, v = h.split((self.heads, self.kv_heads, self.kv_heads), dim=1)
-        rope_axes(q, k, pos, self.plan, self.q_norm, self.k_norm, self.eps, q_out=q, k_out=k, stream=stream)
+        with _on(x, stream):
+            y = self.layer(x, offsets, y=y) if grouped else self.layer(x, y=y)
+            _lib._require(y.dtype == torch.bfloat16, f"y must be bf16, got {y.dtype}")
+            h = y.unflatten(1, (self.heads + 2 * self.kv_heads, self.plan.head_dim))
+            q, k, v = h.split((self.heads, self.kv_heads, self.kv_heads), dim=1)
+            rope_axes(q, k, pos, self.plan, self.q_norm, self.k_norm, self.eps, q_out=q, k_out=k)
         return q, k, v

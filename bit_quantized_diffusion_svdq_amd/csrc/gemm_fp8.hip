@@ -425,52 +425,47 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) fmac(acc[TM - 1][j], p[(TURN * TM - 1) & 1][j], sp[(TURN * TM - 1) & 1]);
 
-    // ---- outputs: activation in registers, one rounding, then through
-    // LDS (free now) so that rows leave as 16-byte stores of whole lines. The
-    // 16-byte chunks of a staged row are XOR-swizzled against bank conflicts.
-    if (a.act) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = gelu_tanh_f32(acc[i][j][e]);
-    }
+    // ---- outputs, 16 rows at a time: activation in registers, one rounding, then
+    // through LDS (free now) so that rows leave as 16-byte stores of whole
+    // lines, the memory taking one run of rows while the next is worked on.
+    // The 16-byte chunks of a staged row are XOR-swizzled against bank
+    // conflicts; a wave reads back only what it wrote, in order.
     constexpr int ES = C::PREC ? 4 : 2;                            // bytes of an output
     constexpr int RB = TN * 16 * ES, CPR = RB / 16;                // bytes, 16-byte chunks of a staged row
-    constexpr int PW = 16 * TM * RB, XW = C::XSLOT / PW, WW = C::WSLOT / PW;   // a wave's bytes, waves per slot
-    static_assert(2 * (XW + WW) >= NW, "staging fits the slots");
-    char* stg = wave < XW ? xs0 + wave * PW
-              : wave < 2 * XW ? xs1 + (wave - XW) * PW
-              : wave < 2 * XW + WW ? ws0 + (wave - 2 * XW) * PW : ws1 + (wave - 2 * XW - WW) * PW;
+    constexpr int PER = 16 / ES, CHUNKS = 16 * CPR / 64;           // outputs of a chunk, chunks of a lane
+    static_assert(NW * 16 * RB <= C::XSLOT && 16 * CPR % 64 == 0, "the staged rows fit a slot");
+    char* stg = xs0 + wave * (16 * RB);
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            const int r = i * 16 + l16, at = (j * 16 + q4 * 4) * ES;
-            char* d = stg + r * RB + ((((at >> 4) ^ r) & (CPR - 1)) << 4) + (at & 15);
+            if (a.act) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = gelu_tanh_f32(acc[i][j][e]);
+            }
+            const int at = (j * 16 + q4 * 4) * ES;
+            char* d = stg + l16 * RB + ((((at >> 4) ^ l16) & (CPR - 1)) << 4) + (at & 15);
             if constexpr (C::PREC) *(float4*)d = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
             else *(uint2*)d = make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
         }
-    // the wave reads back only what it wrote
-    constexpr int PER = 16 / ES;
-    for (int q = lane; q < 16 * TM * CPR; q += 64) {
-        const int r = q / CPR, c = q % CPR;
-        const uint4 v = *(const uint4*)(stg + r * RB + (((c ^ r) & (CPR - 1)) << 4));
-        const int row = wm * TM * 16 + r, col = n0 + wn * TN * 16 + c * PER;
-        if (row < rr.rows && col < a.N) {
-            char* d = (char*)a.y + ((rr.m0 + row) * a.ldy + col) * ES;
-            if (a.vec && col + PER <= a.N) {
-                *(uint4*)d = v;
-            } else {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                const int cnt = a.N - col < PER ? a.N - col : PER;
 #pragma unroll
-                for (int e = 0; e < PER; ++e)
-                    if (e < cnt) {
-                        if constexpr (C::PREC) ((uint32_t*)d)[e] = w[e];
-                        else ((uint16_t*)d)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-                    }
+        for (int k = 0; k < CHUNKS; ++k) {
+            const int q = k * 64 + lane, r = q / CPR, c = q % CPR;
+            const uint4 v = *(const uint4*)(stg + r * RB + (((c ^ r) & (CPR - 1)) << 4));
+            const int row = (wm * TM + i) * 16 + r, col = n0 + wn * TN * 16 + c * PER;
+            if (row < rr.rows && col < a.N) {
+                char* d = (char*)a.y + ((rr.m0 + row) * a.ldy + col) * ES;
+                if (a.vec && col + PER <= a.N) {
+                    *(uint4*)d = v;
+                } else {
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < PER; ++e)
+                        if (col + e < a.N) {
+                            if constexpr (C::PREC) ((uint32_t*)d)[e] = w[e];
+                            else ((uint16_t*)d)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                        }
+                }
             }
         }
     }
@@ -607,7 +602,7 @@ void launch_few(const Args& a, hipStream_t stream) {
 //    with 128 x 128 (two a CU), 184 with 64 x 128, 223 with 64 x 64. Which one
 //    wins is decided by how its tiles fill rounds of the CUs: 4608 x 12288 x 4096
 //    takes 211 us with 160 x 256 (1.8 rounds) and 272 with 256 x 256 (1.1),
-//    4608 x 4096 x 12288 208 with 224 x 256 (3.9 rounds) and 233 with 160 x
+//    4608 x 4096 x 12288 204 with 224 x 256 (3.9 rounds) and 233 with 160 x
 //    256. Where the tiles do not fill the CUs once, memory latency counts, and
 //    the small ones keep three or four slots: 256 x 4096 x 4096 takes 11.6 with
 //    64 x 64 (256 tiles; 13.2 with two slots), 19.3 with 128 x 128 (64 tiles);
@@ -628,8 +623,8 @@ struct Variant {
 };
 
 constexpr Variant kVariants[] = {
-    {256, 256, 0, 1, 0, 1.20, 1.81}, {224, 256, 0, 1, 0, 1.07, 1.63}, {192, 256, 0, 1, 0, 0.94, 1.38},
-    {160, 256, 0, 1, 0, 0.85, 1.21}, {256, 128, 0, 1, 0, 0.75, 0.98}, {128, 128, 0, 2, 0, 0.60, 1.07},
+    {256, 256, 0, 1, 0, 1.20, 1.74}, {224, 256, 0, 1, 0, 1.07, 1.52}, {192, 256, 0, 1, 0, 0.94, 1.36},
+    {160, 256, 0, 1, 0, 0.85, 1.18}, {256, 128, 0, 1, 0, 0.75, 0.98}, {128, 128, 0, 2, 0, 0.60, 1.07},
     {128, 128, 0, 1, 0, 0.50, 0.60}, {64, 128, 0, 2, 0, 0.42, 0.76},  {64, 64, 0, 2, 0, 0.30, 0.44},
     {16, 16, 1, 4, 32, 0, 0},        {16, 32, 1, 4, 16, 0, 0},        {32, 32, 1, 4, 16, 0, 0},
 };

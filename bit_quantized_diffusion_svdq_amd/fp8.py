@@ -10,8 +10,8 @@ their group's (the experts of a mixture, or the text and image streams of a
 joint block in one launch).
 
 Marshalling only: the arithmetic is the library's. Tensors may live on any
-GPU; a call runs on that GPU's current stream unless ``stream`` is given, and
-allocates its outputs with torch.
+GPU; a call runs on that GPU's current stream, or on ``stream``, and
+allocates what it needs there.
 """
 from __future__ import annotations
 
@@ -32,9 +32,15 @@ def blocks(n: int) -> int:
     return (n + BLOCK - 1) // BLOCK
 
 
-def _on(t: torch.Tensor):
-    """The tensor's GPU made current, if it is not."""
-    return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+def _on(t: torch.Tensor, stream=None):
+    """The tensor's GPU made current, if it is not, and the given stream (a
+    torch stream or a raw handle), so that what a call allocates belongs to the
+    stream that uses it."""
+    if stream is None:
+        return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
+    return torch.cuda.stream(stream)
 
 
 _HERE = contextlib.nullcontext()
@@ -54,12 +60,12 @@ def quantize_act_fp8(x: torch.Tensor, stream=None):
     if K < 16 or K % 16:
         raise ValueError(f"x must have K a positive multiple of 16, got {K}")
     ldx = x.stride(0) if M > 1 else K
-    if ldx < K or ldx % 8:                      # a broadcast or unaligned row stride
-        x, ldx = x.contiguous(), K
-    with _on(x):
+    with _on(x, stream):
+        if ldx < K or ldx % 8:                  # a broadcast or unaligned row stride
+            x, ldx = x.contiguous(), K
         qx = torch.empty((M, K), dtype=E4M3, device=x.device)
         sx = torch.empty((blocks(K), M), dtype=_F32, device=x.device)
-        _lib.svdq_quantize_act_fp8(x, M, K, ldx, qx, sx, stream)
+        _lib.svdq_quantize_act_fp8(x, M, K, ldx, qx, sx)
     return qx, sx
 
 
@@ -123,9 +129,9 @@ def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfl
     fp32 [ceil(N/128), ceil(K/128)], bias bf16 [N] or None -> y [M, N] (bf16
     or fp32; rows of a given y may be strided)."""
     M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, 0)
-    with _on(qx):
+    with _on(qx, stream):
         y, ldy = _output(y, M, N, out_dtype, qx.device)
-        _lib.svdq_gemm_fp8(qx, sx, M, K, qw, sw, N, bias, _lib.ACT[act], y, int(out_dtype is _F32), ldy, stream)
+        _lib.svdq_gemm_fp8(qx, sx, M, K, qw, sw, N, bias, _lib.ACT[act], y, int(out_dtype is _F32), ldy)
     return y
 
 
@@ -143,10 +149,10 @@ def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", ou
     M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, groups)
     if offsets.device != qx.device:
         raise ValueError(f"offsets is on {offsets.device}, expected {qx.device}")
-    with _on(qx):
+    with _on(qx, stream):
         y, ldy = _output(y, M, N, out_dtype, qx.device)
         _lib.svdq_gemm_fp8_grouped(qx, sx, M, K, qw, sw, N, offsets, groups, bias, _lib.ACT[act], y,
-                                   int(out_dtype is _F32), ldy, stream)
+                                   int(out_dtype is _F32), ldy)
     return y
 
 
@@ -176,8 +182,9 @@ class Fp8Linear:
         the product, on one stream."""
         if x.dim() != 2 or x.shape[1] != self.K:
             raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
-        qx, sx = quantize_act_fp8(x, stream)
-        return fp8_linear(qx, sx, self.qw, self.sw, self.bias, act, out_dtype, y, stream)
+        with _on(x, stream):                     # (the codes are freed on the stream that reads them)
+            qx, sx = quantize_act_fp8(x)
+            return fp8_linear(qx, sx, self.qw, self.sw, self.bias, act, out_dtype, y)
 
 
 @dataclass
@@ -212,5 +219,6 @@ class Fp8GroupedLinear:
             raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
         if offsets.numel() != self.groups + 1:
             raise ValueError(f"offsets must hold {self.groups + 1} values, got {offsets.numel()}")
-        qx, sx = quantize_act_fp8(x, stream)
-        return fp8_grouped_linear(qx, sx, offsets, self.qw, self.sw, self.bias, act, out_dtype, y, stream)
+        with _on(x, stream):
+            qx, sx = quantize_act_fp8(x)
+            return fp8_grouped_linear(qx, sx, offsets, self.qw, self.sw, self.bias, act, out_dtype, y)

@@ -146,7 +146,7 @@ def quantize_fp8(w: torch.Tensor, bias=None, stream=None) -> dict:
     for wg in ws:
         _lib._check_rows(wg, "w", torch.bfloat16)
     _lib._check_same_device(w, bias=bias)
-    with _on(w):
+    with _on(w, stream):
         qw = torch.empty((*lead, N, K), dtype=E4M3, device=w.device)
         sw = torch.empty((*lead, blocks(N), blocks(K)), dtype=torch.float32, device=w.device)
         for g, wg in enumerate(ws):
@@ -155,5 +155,5 @@ def quantize_fp8(w: torch.Tensor, bias=None, stream=None) -> dict:
                 pad = torch.zeros((K, (N + 7) // 8 * 8), dtype=torch.bfloat16, device=w.device)
                 pad[:, :N].copy_(wg)
                 wg, ldw = pad, pad.stride(0)
-            _lib.svdq_quantize_weight_fp8(wg, K, N, ldw, qw[g] if lead else qw, sw[g] if lead else sw, stream)
+            _lib.svdq_quantize_weight_fp8(wg, K, N, ldw, qw[g] if lead else qw, sw[g] if lead else sw)
     return dict(qw=qw, sw=sw, bias=bias, K=K, N=N)

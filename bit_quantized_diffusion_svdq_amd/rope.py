@@ -118,11 +118,11 @@ def rope_axes(q, k, pos, plan: RopePlan, q_norm=None, k_norm=None, eps: float = 
     for t in (k, pos, q_norm, k_norm, q_out, k_out, plan.turns):
         if t is not None and t.device != dev:
             raise ValueError(f"a tensor or the plan is on {t.device}, expected {dev}")
-    with _on(q):
+    with _on(q, stream):
         q_out, qs = _side(q, q_out, q_norm, T, hq, D)
         ks = None
         if k is not None:
             k_out, ks = _side(k, k_out, k_norm, T, hk, D)
         _lib.svdq_rope_axes(qs, ks, T, D, int(dt is torch.float32), pos, int(f32_pos), plan.axes, plan.turns, plan.axis,
-                            plan.pairs, PAIRING[plan.pairing], int(inverse), eps, stream)
+                            plan.pairs, PAIRING[plan.pairing], int(inverse), eps)
     return q_out if k is None else (q_out, k_out)

@@ -314,6 +314,27 @@ def test_layers_on_streams_and_in_a_graph():
             t.zero_()
 
 
+def test_buffers_of_a_call_belong_to_its_stream():
+    """Calls on a side stream while the current one allocates and overwrites
+    memory of the same sizes: the codes between a layer's two kernels are the
+    side stream's, also for a raw handle."""
+    note("Fp8Linear on a busy side stream")
+    M, K, N = 300, 1024, 512
+    lay = svdq.Fp8Linear.from_quantized(svdq.quantize_fp8(weights(K, N, 1)))
+    x = acts(M, K, 2)
+    want = lay(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s in (side, side.cuda_stream):
+        got = []
+        for _ in range(20):
+            got.append(lay(x, stream=s))
+            for shape in ((M, K), (8, M * 4)):
+                torch.empty(shape, dtype=torch.uint8, device="cuda").fill_(0x7F)
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, want) for g in got)
+
+
 def test_package_round_trip(tmp_path):
     note("save_fp8_layer / load_fp8_layer")
     x = acts(9, 144, 1)
