@@ -1,4 +1,4 @@
-// svdq_gemm_fp8 / svdq_gemm_fp8_grouped: E4M3 x E4M3 products with one fp32
+// svdq_gemm_fp8 / svdq_gemm_fp8_grouped / svdq_linear_fp8: E4M3 x E4M3 products with one fp32
 // scale per block of 128 input channels,
 //
 //   Y[m, n] = act( sum_b sx[b, m] sw[n / 128, b] P_b[m, n] + bias[n] ),
@@ -14,7 +14,7 @@
 //  - Block scales are fp32 with a mantissa, so they cannot ride on the matrix
 //    pipe's E8M0 scales: the FMAs (4 of 64 lanes, 16 cycles of a SIMD) run
 //    beside the MFMAs (32 cycles).
-#include "common.h"
+#include "fp8.h"
 
 namespace {
 
@@ -113,6 +113,8 @@ struct Args {
     int64_t M, ldy;
     int N, K, E;
     int act, y_f32, vec;            // vec: rows of y take 16-byte stores
+    const uint16_t* x;              // the layer of few rows: bf16 activations (qx, sx NULL), else NULL
+    int64_t ldx;
 };
 
 // The rows a workgroup works on: m0 .. m0 + rows - 1 of group g (rows 0: none)
@@ -481,16 +483,29 @@ struct FewCfg {
     static constexpr int MT = MT_, NT = NT_, NW = NW_, U = U_, PREC = PREC_;
 };
 
-template <class C, bool GROUPED>
+// What its activations are: codes of one batch, codes of ragged groups, or bf16
+// values, which every workgroup turns into codes in LDS for itself while its
+// first weights are on their way (LAYER: one launch instead of two). That
+// costs rows x blocks of vector work per workgroup, so it is for few of them:
+// 1 x 4096 x 18432 takes 16.3 us (20.2 in two launches, 16.9 their product
+// alone), 1 x 18432 x 4096 18.2 (22.4), 16 x 1536 x 6144 7.3 (8.2); even at 256
+// rows x blocks, 8 x 4096 x 18432 24.6 (24.9), 8 x 4096 x 4096 9.4 (9.1); behind
+// at 384, 4 x 12288 x 4096 17.6 (16.1). The codes are the activation pass's.
+enum { DENSE, GROUPS, LAYER };
+
+template <class C, int KIND>
 __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
     constexpr int MT = C::MT, NT = C::NT, NW = C::NW, U = C::U;
+    static_assert(KIND != LAYER || MT == 1, "up to 16 rows");
+    constexpr int QB = 3;                                // blocks of activations in flight per 16 lanes
     __shared__ __attribute__((aligned(16))) v4f red[NW][MT * NT][64];
+    extern __shared__ __attribute__((aligned(16))) char codes[];   // LAYER: M rows of codes, then M rows of scales
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int tiles_n = (a.N + 16 * NT - 1) / (16 * NT);
     const int t = blockIdx.x;
     Rows rr;
-    if constexpr (GROUPED) {
+    if constexpr (KIND == GROUPS) {
         int total;
         rr = group_rows(a, t / tiles_n, 16 * MT, &total);
         if (t / tiles_n >= total) return;
@@ -502,10 +517,12 @@ __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
     const int n0 = (t % tiles_n) * 16 * NT;
     const int K = a.K, KB = (K + 127) / 128, NB = (a.N + 127) / 128;
     const int nrows = a.N - n0 < 16 * NT ? a.N - n0 : 16 * NT;
-    const rsrc_t rx = make_rsrc(a.qx + rr.m0 * K, (int64_t)rr.rows * K);
+    const rsrc_t rx = make_rsrc(a.qx + rr.m0 * K, KIND == LAYER ? 0 : (int64_t)rr.rows * K);
     const rsrc_t rw = make_rsrc(a.qw + ((int64_t)rr.g * a.N + n0) * K, (int64_t)nrows * K);
     const float* swp = a.sw + ((int64_t)rr.g * NB + n0 / 128) * KB;
     const float* sxp = a.sx + rr.m0;
+    const int pitch = KB * 128 + 16;                     // of a row of codes: 16 rows fall on different banks
+    float* scales = (float*)(codes + rr.rows * pitch);
     int ms[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) ms[i] = 16 * i + l16 < rr.rows ? 16 * i + l16 : rr.rows - 1;
@@ -515,9 +532,9 @@ __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kb0 = wave; kb0 < KB; kb0 += NW * U) {
-        uint4 w[U][NT][2], x[U][MT][2];
-        float s[U][MT];
+    uint4 w[U][NT][2];
+    float sw[U];
+    auto load_w = [&](int kb0) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int kb = kb0 + u * NW;
@@ -528,14 +545,52 @@ __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
                     w[u][j][h] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rw, v, kb * 128 + j * 16 * K, 0));
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    x[u][i][h] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, v, kb * 128 + i * 16 * K, 0));
             }
-            const int kc = kb < KB ? kb : KB - 1;
-            const float sw = swp[kc];
+            sw[u] = swp[kb < KB ? kb : KB - 1];
+        }
+    };
+    if constexpr (KIND == LAYER) {
+        load_w(wave);                                    // on their way while the activations are turned
+        const int pairs = rr.rows * KB;                  // (row, block): 16 lanes each
+        for (int p0 = tid >> 4; p0 < pairs; p0 += QB * NW * 4) {
+            uint4 v[QB];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) s[u][i] = sxp[(int64_t)kc * a.M + ms[i]] * sw;
+            for (int b = 0; b < QB; ++b) {
+                const int p = p0 + b * NW * 4, m = p / KB, k = (p - m * KB) * 128 + l16 * 8;
+                v[b] = make_uint4(0u, 0u, 0u, 0u);
+                if (p < pairs && k < K) v[b] = *(const uint4*)(a.x + m * a.ldx + k);
+            }
+#pragma unroll
+            for (int b = 0; b < QB; ++b) {
+                const int p = p0 + b * NW * 4, m = p / KB, k = (p - m * KB) * 128 + l16 * 8;
+                if (p < pairs) {
+                    float s;
+                    *(uint2*)(codes + m * pitch + k) = block_codes(v[b], s);
+                    if (l16 == 0) scales[p] = s;
+                }
+            }
+        }
+        __syncthreads();
+    }
+    for (int kb0 = wave; kb0 < KB; kb0 += NW * U) {
+        uint4 x[U][MT][2];
+        float s[U][MT];
+        if (KIND != LAYER || kb0 != wave) load_w(kb0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = kb0 + u * NW, kc = kb < KB ? kb : KB - 1;
+            const int left = K - kb * 128 - 16 * q4;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int v = 64 * h < left ? vo + 64 * h : kBeyond;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    if constexpr (KIND == LAYER) x[u][i][h] = *(const uint4*)(codes + ms[i] * pitch + kc * 128 + 64 * h + 16 * q4);
+                    else x[u][i][h] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, v, kb * 128 + i * 16 * K, 0));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) s[u][i] = (KIND == LAYER ? scales[ms[i] * KB + kc] : sxp[(int64_t)kc * a.M + ms[i]]) * sw[u];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -589,7 +644,24 @@ template <class C, bool GROUPED>
 void launch_few(const Args& a, hipStream_t stream) {
     const int64_t tm = GROUPED ? (a.M + (int64_t)a.E * (16 * C::MT - 1)) / (16 * C::MT) : (a.M + 16 * C::MT - 1) / (16 * C::MT);
     const int64_t tn = (a.N + 16 * C::NT - 1) / (16 * C::NT);
-    hipLaunchKernelGGL((gemm_fp8_few_kernel<C, GROUPED>), dim3((unsigned)(tm * tn)), dim3(64 * C::NW), 0, stream, a);
+    hipLaunchKernelGGL((gemm_fp8_few_kernel<C, GROUPED ? GROUPS : DENSE>), dim3((unsigned)(tm * tn)), dim3(64 * C::NW), 0, stream, a);
+}
+
+// 16 outputs a workgroup, or 32 where one trip of its waves' loads still covers
+// K and the narrow ones would come in turns: 1 x 1536 x 6144 takes 5.1 us with
+// 32 (5.6 with 16), but 1 x 4096 x 18432 21.4 (16.2) and 1 x 1024 x 1024, 64
+// narrow workgroups, 4.1 (3.7).
+template <int PREC>
+void launch_layer(const Args& a, int cus, hipStream_t stream) {
+    const int KB = (a.K + 127) / 128;
+    const size_t lds = (size_t)a.M * (KB * 128 + 16 + KB * 4);
+    if (KB <= 16 && (a.N + 15) / 16 > cus) {
+        typedef FewCfg<1, 2, 8, 2, PREC> C;
+        hipLaunchKernelGGL((gemm_fp8_few_kernel<C, LAYER>), dim3((unsigned)((a.N + 31) / 32)), dim3(64 * C::NW), lds, stream, a);
+    } else {
+        typedef FewCfg<1, 1, 8, 4, PREC> C;
+        hipLaunchKernelGGL((gemm_fp8_few_kernel<C, LAYER>), dim3((unsigned)((a.N + 15) / 16)), dim3(64 * C::NW), lds, stream, a);
+    }
 }
 
 // ---------------------------------------------------------------- which kernel
@@ -703,8 +775,18 @@ hipError_t launch_gemm_fp8(const uint8_t* qx, const float* sx, int64_t M, int64_
                            int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
                            int64_t ldy, int cus, hipStream_t stream) {
     const int vec = ldy % (y_f32 ? 4 : 8) == 0 && (uintptr_t)y % 16 == 0;
-    const Args a{qx, sx, qw, sw, bias, y, offs, M, ldy, (int)N, (int)K, E, act, y_f32, vec};
+    const Args a{qx, sx, qw, sw, bias, y, offs, M, ldy, (int)N, (int)K, E, act, y_f32, vec, nullptr, 0};
     const bool ok = offs ? (y_f32 ? launch_variant<1, true>(a, cus, stream) : launch_variant<0, true>(a, cus, stream))
                          : (y_f32 ? launch_variant<1, false>(a, cus, stream) : launch_variant<0, false>(a, cus, stream));
     return ok ? hipGetLastError() : hipErrorInvalidValue;
+}
+
+hipError_t launch_linear_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw, const float* sw,
+                             int64_t N, const uint16_t* bias, int act, void* y, int y_f32, int64_t ldy, int cus,
+                             hipStream_t stream) {
+    const int vec = ldy % (y_f32 ? 4 : 8) == 0 && (uintptr_t)y % 16 == 0;
+    const Args a{nullptr, nullptr, qw, sw, bias, y, nullptr, M, ldy, (int)N, (int)K, 0, act, y_f32, vec, x, ldx};
+    if (y_f32) launch_layer<1>(a, cus, stream);
+    else launch_layer<0>(a, cus, stream);
+    return hipGetLastError();
 }

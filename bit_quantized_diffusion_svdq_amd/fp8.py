@@ -35,7 +35,9 @@ def blocks(n: int) -> int:
 def _on(t: torch.Tensor, stream=None):
     """The tensor's GPU made current, if it is not, and the given stream (a
     torch stream or a raw handle), so that what a call allocates belongs to the
-    stream that uses it."""
+    stream that uses it. (Host tensors: the checks that follow refuse them.)"""
+    if not t.is_cuda:
+        return _HERE
     if stream is None:
         return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
     if isinstance(stream, int):
@@ -156,6 +158,43 @@ def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", ou
     return y
 
 
+# what svdq_linear_fp8 takes: rows, and rows x blocks of 128 channels
+_FEW_ROWS, _FEW_BLOCKS = 16, 256
+
+
+def _linear_few(x, qw, sw, bias, act, out_dtype, y):
+    """The layer of few rows in one launch, or None for a call that has more
+    or that is not the usual one (the two passes then say what is wrong)."""
+    M, K = x.shape
+    kb = blocks(K)
+    dev = x.device
+    if not (0 < M <= _FEW_ROWS and M * kb <= _FEW_BLOCKS and x.is_cuda and x.dtype is _BF16 and K >= 16 and K % 16 == 0
+            and x.stride(1) == 1 and qw.dtype is E4M3 and sw.dtype is _F32 and qw.device == dev and sw.device == dev
+            and qw.dim() == 2 and qw.is_contiguous() and sw.is_contiguous() and act in _lib.ACT):
+        return None
+    N = qw.shape[0]
+    ldx = x.stride(0) if M > 1 else K
+    if not (N >= 1 and sw.shape == (blocks(N), kb)
+            and (bias is None or (bias.dtype is _BF16 and bias.shape == (N,) and bias.is_contiguous()
+                                  and bias.device == dev))):
+        return None
+    if y is None:
+        if not (out_dtype is _BF16 or out_dtype is _F32):
+            return None
+        y, ldy = torch.empty((M, N), dtype=out_dtype, device=dev), N
+    else:
+        ldy = y.stride(0) if y.dim() == 2 and M > 1 else N
+        if not (y.shape == (M, N) and (y.dtype is _BF16 or y.dtype is _F32) and y.device == dev
+                and (y.stride(1) == 1 or N == 1) and ldy >= N):
+            return None
+        if y.untyped_storage().data_ptr() == x.untyped_storage().data_ptr():
+            x, ldx = x.clone(memory_format=torch.contiguous_format), K   # in place: y is written while x is read
+    if ldx < K or ldx % 8:                      # a broadcast or unaligned row stride
+        x, ldx = x.contiguous(), K
+    _lib.svdq_linear_fp8(x, M, K, ldx, qw, sw, N, bias, _lib.ACT[act], y, int(y.dtype is _F32), ldy)
+    return y
+
+
 @dataclass
 class Fp8Linear:
     """One 8-bit layer's device arrays."""
@@ -179,10 +218,14 @@ class Fp8Linear:
     def __call__(self, x: torch.Tensor, act: str = "none", out_dtype=torch.bfloat16, y=None,
                  stream=None) -> torch.Tensor:
         """Y [M, N] for bf16 activations x [M, K]: the activation pass, then
-        the product, on one stream."""
+        the product, on one stream; in one launch for few rows (M <= 16 and
+        M * ceil(K / 128) <= 256: single tokens, pooled conditioning)."""
         if x.dim() != 2 or x.shape[1] != self.K:
             raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
         with _on(x, stream):                     # (the codes are freed on the stream that reads them)
+            out = _linear_few(x, self.qw, self.sw, self.bias, act, out_dtype, y)
+            if out is not None:
+                return out
             qx, sx = quantize_act_fp8(x)
             return fp8_linear(qx, sx, self.qw, self.sw, self.bias, act, out_dtype, y)
 

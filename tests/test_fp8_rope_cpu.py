@@ -96,6 +96,31 @@ def test_well_formed_calls_reach_the_device_check(lib):
     valid(_gemm(lib, True, y=F + 2, bias=E))
 
 
+def _few(lib, **kw):
+    a = dict(x=A, M=16, K=2048, ldx=2048, qw=C, sw=D, N=77, bias=None, act=0, y=F, ydt=0, ldy=77)
+    a.update(kw)
+    return lib.svdq_linear_fp8(a["x"], a["M"], a["K"], a["ldx"], a["qw"], a["sw"], a["N"], a["bias"], a["act"], a["y"],
+                               a["ydt"], a["ldy"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), SHAPE), (dict(M=17, K=128), SHAPE), (dict(K=2064, ldx=2064), SHAPE), (dict(M=1, K=32784, ldx=32784), SHAPE),
+    (dict(K=40), SHAPE), (dict(K=0), SHAPE), (dict(K=1 << 22), SHAPE), (dict(N=0), SHAPE),
+    (dict(N=1 << 26, ldy=1 << 26), SHAPE), (dict(ldx=2032), SHAPE), (dict(ldx=2052), ALIGN), (dict(ldy=76), SHAPE),
+    (dict(ldy=1 << 31), SHAPE), (dict(act=2), UNSUP), (dict(ydt=2), UNSUP), (dict(x=None), NULL), (dict(qw=None), NULL),
+    (dict(sw=None), NULL), (dict(y=None), NULL), (dict(x=A + 8), ALIGN), (dict(qw=C + 4), ALIGN), (dict(sw=D + 2), ALIGN),
+    (dict(bias=E + 1), ALIGN), (dict(y=F + 1), ALIGN), (dict(y=F + 2, ydt=1), ALIGN), (dict(M=0, x=None), OK),
+])
+def test_layer_of_few_rows_rejects(lib, kw, status):
+    assert _few(lib, **kw) == status
+    assert status == OK or lib.svdq_last_error()
+
+
+def test_layer_of_few_rows_limits(lib):
+    valid(_few(lib))
+    valid(_few(lib, M=1, K=32768, ldx=1 << 40, bias=E, N=(1 << 26) - 1, ldy=1 << 26))
+
+
 def _heads(**kw):
     a = dict(x=A, ts=256, hs=64, heads=4, norm=None, y=B, yts=256, yhs=64)
     a.update(kw)
@@ -236,6 +261,22 @@ def test_fp8_grouped_linear_refuses(kw, text):
     a.update(kw)
     with pytest.raises(ValueError, match=text):
         svdq.fp8_grouped_linear(a.pop("qx"), a.pop("sx"), a.pop("offsets"), a.pop("qw"), a.pop("sw"), **a)
+
+
+@pytest.mark.parametrize("M", [1, 16, 400])
+@pytest.mark.parametrize("kw,text", [
+    (dict(x=torch.zeros((16, 128), dtype=bf)), "x must be"), (dict(x=torch.zeros((16, 144))), "x must be"),
+    (dict(x=torch.zeros(144, dtype=bf)), "x must be"), (dict(x=torch.zeros((144, 16), dtype=bf).t()), "contiguous"),
+    (dict(), "GPU device"),
+])
+def test_layer_refuses(M, kw, text):
+    """The same words for few rows (one launch) and many."""
+    a = _prod()
+    x = kw.get("x", torch.zeros((M, 144), dtype=bf))
+    if x.dim() == 2 and x.shape[0] == 16 and M > 16:
+        x = x.repeat(M // 16, 1) if x.is_contiguous() else torch.zeros((144, M), dtype=bf).t()
+    with pytest.raises(ValueError, match=text):
+        svdq.Fp8Linear(a["qw"], a["sw"])(x)
 
 
 def test_quantisers_refuse():

@@ -314,6 +314,98 @@ def test_layers_on_streams_and_in_a_graph():
             t.zero_()
 
 
+FEW = [(1, 16, 1), (1, 4096, 300), (2, 144, 7), (3, 10240, 24), (7, 272, 129), (16, 2048, 100), (5, 112, 8201),
+       (16, 2048, 4200), (9, 1040, 4104), (1, 24576, 40), (1, 32768, 33), (16, 2064, 20), (17, 128, 20)]
+
+
+@pytest.mark.parametrize("M,K,N", FEW)
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_layer_of_few_rows(M, K, N, out):
+    """A layer on bf16 rows, up to and past what one launch takes, against the
+    oracle's codes and products."""
+    note(f"Fp8Linear {M} x {K} x {N} {out}")
+    x, b = acts(M, K, M + N), biases(N, K)
+    lay = svdq.Fp8Linear.from_quantized(svdq.quantize_fp8(weights(K, N, K + N), b if M % 3 else None))
+    act = "gelu_tanh" if (M + N) % 2 else "none"
+    y = lay(x, act=act, out_dtype=out)
+    qx, sx = ofp8.quantize_act(np64(x))
+    ref = ofp8.linear(qx, sx, np64(lay.qw), lay.sw.cpu().numpy(), np64(b) if M % 3 else None)
+    assert y.dtype == out and tuple(y.shape) == (M, N)
+    check_product(y, ref, K, act)
+
+
+@pytest.mark.parametrize("M,K,N", [(6, 400, 136), (6, 400, 4200)])
+def test_layer_of_few_rows_values_that_are_not_finite(M, K, N):
+    """Infinities saturate and leave the scale alone, NaN spoils its own row
+    only, rows of zeros give the bias: as in the two passes."""
+    note(f"Fp8Linear non-finite {M} x {K} x {N}")
+    x, b = acts(M, K, 8), biases(N, 9)
+    lay = svdq.Fp8Linear.from_quantized(svdq.quantize_fp8(weights(K, N, 10), b))
+    clean = lay(x, out_dtype=torch.float32)
+    x[1] = 0.0
+    x[2, 5], x[2, 300] = float("inf"), float("-inf")
+    x[4, 399] = float("nan")
+    y = lay(x, out_dtype=torch.float32)
+    rest = [0, 3, 5]
+    assert torch.equal(y[rest], clean[rest]) and torch.equal(y[1], b.float()) and y[4].isnan().all()
+    qx, sx = ofp8.quantize_act(np64(x[2:3]))
+    check_product(y[2:3], ofp8.linear(qx, sx, np64(lay.qw), lay.sw.cpu().numpy(), np64(b)), K)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,ld,off", [(200, 200, 0), (200, 203, 1), (121, 128, 0), (4200, 4204, 4)])
+def test_layer_of_few_rows_views(dt, N, ld, off):
+    """Strided inputs, outputs into strided, odd and unaligned buffers whose
+    other values stay, and an output over its own input."""
+    note(f"Fp8Linear views {dt} {N} {ld} {off}")
+    M, K = 5, 400
+    lay = svdq.Fp8Linear.from_quantized(svdq.quantize_fp8(weights(K, N, N)))
+    x = acts(40, 1024, 3)[3:3 + M, 64:64 + K]
+    want = lay(x.contiguous(), out_dtype=dt)
+    assert torch.equal(lay(x, out_dtype=dt), want)
+    assert torch.equal(lay(x[:1].expand(M, K), out_dtype=dt), want[:1].expand(M, N))
+    buf = torch.full((M * ld + 64,), -3.0, dtype=dt, device="cuda")
+    y = buf[off:off + M * ld].view(M, ld)[:, :N]
+    assert lay(x, y=y) is y and torch.equal(y, want)
+    rest = torch.ones_like(buf, dtype=torch.bool)
+    rest[off:off + M * ld].view(M, ld)[:, :N] = False
+    assert (buf[rest] == -3.0).all()
+
+
+@pytest.mark.parametrize("M", [1, 8, 16])
+def test_layer_of_few_rows_over_its_input(M):
+    note(f"Fp8Linear in place {M}")
+    K = N = 1024
+    lay = svdq.Fp8Linear.from_quantized(svdq.quantize_fp8(weights(K, N, 1)))
+    x = acts(M, K, 2)
+    want = lay(x)
+    for _ in range(5):
+        z = x.clone()
+        assert lay(z, y=z) is z and torch.equal(z, want)
+
+
+def test_layer_of_few_rows_on_streams_and_in_a_graph():
+    note("Fp8Linear few rows: streams and graphs")
+    K, N, M = 1040, 520, 4
+    lay = svdq.Fp8Linear.from_quantized(svdq.quantize_fp8(weights(K, N, 1), biases(N, 2)))
+    x = acts(M, K, 5)
+    want = lay(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [lay(x, stream=side), lay(x, stream=side.cuda_stream)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    y = torch.empty_like(want)
+    graph = svdq.CapturedSequence(lambda: lay(x, y=y))
+    for i in range(4):
+        x.copy_(acts(M, K, 6 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, lay(x))
+        y.zero_()
+    assert tuple(lay(x[:0]).shape) == (0, N)
+
+
 def test_buffers_of_a_call_belong_to_its_stream():
     """Calls on a side stream while the current one allocates and overwrites
     memory of the same sizes: the codes between a layer's two kernels are the
