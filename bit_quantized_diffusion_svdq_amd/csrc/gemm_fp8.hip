@@ -681,47 +681,55 @@ void launch_layer(const Args& a, int cus, hipStream_t stream) {
 //    256 x 12288 x 4096 34 (46 with two slots); 1024 x 4096 x 4096 22 with
 //    128 x 128 in eight waves and four slots, 23.5 in four waves and two, two
 //    workgroups a CU, which take 512 x 4096 x 12288 in 37 (44 the other way,
-//    33 with 256 x 128). Weights that are read once come at 4.3 MB a us.
-//  - few rows: bound by the weights from memory (6.5 MB a us), the operands
-//    from L2 (8.4, less with fewer workgroups than CUs) or the trips of a
-//    wave's loads (2.2 us each, and 4 for a workgroup's start and end where
-//    they come in turns). 1 x 4096 x 18432 takes 17 us (best tile 19), 64 x
-//    12288 x 4096 28 (35), but 64 x 4096 x 12288 26 (15); 48 rows of 32 groups x
-//    2048 x 4096 35 with 32 columns a workgroup, 53 with 16, 38 in tiles.
+//    33 with 256 x 128). Where M is small the weights count: `start` and then
+//    `rate` MB a us (tiles of 64 rows hide most of it beside their loads).
+//  - few rows: `lone` for a trip of a workgroup's loads, four workgroups a CU;
+//    the operands at 29 KB a us and CU; the weights from memory. 1 x 4096 x 18432
+//    takes 17.4 us (20.4 with 32 columns, best tile 20.5), 16 of its rows 23
+//    (19.4 with 64 x 128), 16 x 1536 x 6144 6.6 with 16 columns and 5.1 with 32,
+//    64 x 4096 x 12288 26 (15 in tiles); 48 rows of 32 groups x 2048 x 4096 37
+//    with 32 columns, 43 in tiles.
+// Over 500 sizes of 1 to 64 rows the variant it picks is 1 % slower than the
+// best one on the average, over 170 grouped ones 5 %.
 struct Variant {
     int rows, cols, few;             // outputs per workgroup; few: the few-rows kernel
     int per_cu, trip;                // workgroups on a CU; K blocks per trip of a few-rows workgroup
     double lone, full;
+    double start, rate;              // of the weights
 };
 
 constexpr Variant kVariants[] = {
-    {256, 256, 0, 1, 0, 1.20, 1.74}, {224, 256, 0, 1, 0, 1.07, 1.52}, {192, 256, 0, 1, 0, 0.94, 1.36},
-    {160, 256, 0, 1, 0, 0.85, 1.18}, {256, 128, 0, 1, 0, 0.75, 0.98}, {128, 128, 0, 2, 0, 0.60, 1.07},
-    {128, 128, 0, 1, 0, 0.50, 0.60}, {64, 128, 0, 2, 0, 0.42, 0.76},  {64, 64, 0, 2, 0, 0.30, 0.44},
-    {16, 16, 1, 4, 32, 0, 0},        {16, 32, 1, 4, 16, 0, 0},        {32, 32, 1, 4, 16, 0, 0},
+    {256, 256, 0, 1, 0, 1.20, 1.74, 1.2, 4.3}, {224, 256, 0, 1, 0, 1.07, 1.52, 1.2, 4.3},
+    {192, 256, 0, 1, 0, 0.94, 1.36, 1.2, 4.3}, {160, 256, 0, 1, 0, 0.85, 1.18, 1.2, 4.3},
+    {256, 128, 0, 1, 0, 0.75, 0.98, 1.2, 4.3}, {128, 128, 0, 2, 0, 0.60, 1.07, 1.2, 4.3},
+    {128, 128, 0, 1, 0, 0.50, 0.60, 3.2, 5.1}, {64, 128, 0, 2, 0, 0.42, 0.76, 1.6, 8.5},
+    {64, 64, 0, 2, 0, 0.30, 0.44, 1.3, 9.4},   {16, 16, 1, 4, 32, 2.2, 0, 2.0, 6.6},
+    {16, 32, 1, 4, 16, 2.2, 0, 0.5, 5.3},      {32, 32, 1, 4, 16, 3.1, 0, 1.0, 5.4},
 };
 
 double estimate(const Variant& v, const Args& a, int cus) {
-    const double active = a.offs ? (double)(a.E < a.M ? a.E : a.M) : 1.0, kb = (a.K + 127) / 128;
+    const double M = (double)a.M, E = a.E, kb = (a.K + 127) / 128;
+    // groups that have rows, if rows fall at random
+    const double active = a.offs ? E * (1.0 - __builtin_exp(-M / E)) : 1.0;
     const double tn = (double)((a.N + v.cols - 1) / v.cols);
     // ragged groups: half a tile is lost at the end of each, on the average
-    double tm = a.offs ? (double)a.M / v.rows + 0.5 * active : (double)((a.M + v.rows - 1) / v.rows);
+    double tm = a.offs ? M / v.rows + 0.5 * active : (double)((a.M + v.rows - 1) / v.rows);
     if (tm < active) tm = active;
     const double tiles = tm * tn;
+    // many groups' weights stream at one rate in the small variants
+    const double weights = v.start + active * a.N * (double)a.K / (a.offs && v.rows < 128 ? 6.5e6 : v.rate * 1e6);
+    double t;
     if (v.few) {
-        const double rows = a.M < v.rows * tm ? (double)a.M / tm : v.rows;
-        const double weights = active * a.N * (double)a.K / 6.5e6;
-        const double reads = tiles * (v.cols + rows) * (double)a.K / 8.4e6 * (tiles < cus ? cus / tiles : 1.0);
-        const double turns = tiles / ((double)v.per_cu * cus);
-        const double trips = (4.0 * (turns > 1.0) + 2.2 * __builtin_ceil(kb / v.trip)) * (turns > 1.0 ? turns : 1.0);
-        double t = weights > reads ? weights : reads;
-        return 3.0 + (t > trips ? t : trips);
+        const double g = __builtin_ceil(tiles / cus), turns = g < v.per_cu ? 1.0 : g / v.per_cu;
+        const double rows = M < v.rows * tm ? M / tm : v.rows;
+        const double trips = turns * v.lone * __builtin_ceil(kb / v.trip), reads = g * (v.cols + rows) * a.K / 2.9e4;
+        t = trips > reads ? trips : reads;
+    } else {
+        const double slots = (double)cus * v.per_cu, rounds = __builtin_floor(tiles / slots);
+        const double rest = __builtin_ceil((tiles - rounds * slots) / cus);
+        const double share = v.full * rest / v.per_cu, out = 4.0 * v.rows * v.cols * v.per_cu / 65536.0;
+        t = rounds * (kb * v.full + out) + (rest > 0 ? kb * (share > v.lone ? share : v.lone) + out * rest / v.per_cu : 0.0);
     }
-    const double slots = (double)cus * v.per_cu, rounds = __builtin_floor(tiles / slots);
-    const double rest = __builtin_ceil((tiles - rounds * slots) / cus);
-    const double share = v.full * rest / v.per_cu, out = 4.0 * v.rows * v.cols * v.per_cu / 65536.0;
-    const double t = rounds * (kb * v.full + out) + (rest > 0 ? kb * (share > v.lone ? share : v.lone) + out * rest / v.per_cu : 0.0);
-    const double weights = active * a.N * (double)a.K / 4.3e6;
     return 3.0 + (t > weights ? t : weights);
 }
 
