@@ -118,7 +118,8 @@ __global__ __launch_bounds__(256) void rope_axes_kernel(RopeArgs a) {
     };
     if (first < last) fetch(first);                              // on its way while the angles are worked out
 
-    const int pv = lane < a.axes ? ((const int*)a.pos)[t * a.axes + lane] : 0;   // the token's positions, one a lane
+    // the token's positions, one a lane (no pairs: there may be none)
+    const int pv = a.pairs > 0 && lane < a.axes ? ((const int*)a.pos)[t * a.axes + lane] : 0;
     for (int p0 = 0; p0 < a.pairs; p0 += 64) {
         const int p = p0 + lane < a.pairs ? p0 + lane : a.pairs - 1;
         int ax = a.axis[p];

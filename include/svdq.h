@@ -605,7 +605,8 @@ svdq_status svdq_linear_fp8(const void* x, int64_t M, int64_t K, int64_t ldx, co
  *
  * Angles are formed in fp64 and reduced to a part of a turn before their
  * fp32 sine and cosine; the rest is fp32 with one rounding of the output.
- * heads of q >= 1, of k >= 0, axes in [1, 8]. T == 0 is valid.
+ * heads of q >= 1, of k >= 0, axes in [1, 8]. T == 0 is valid, and so is
+ * pairs == 0 (the norm alone; pos, turns and axis may then be NULL).
  */
 typedef enum { SVDQ_POS_I32 = 0, SVDQ_POS_F32 = 1 } svdq_pos_dtype;
 typedef enum { SVDQ_PAIRS_INTERLEAVED = 0, SVDQ_PAIRS_HALF = 1 } svdq_pairing;

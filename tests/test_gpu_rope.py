@@ -182,6 +182,23 @@ def test_streams_graphs_and_non_finite():
     assert bad[3, 1].all() and bad.sum() == D
 
 
+@pytest.mark.parametrize("T", [1, 9])
+def test_no_pairs_no_positions(T):
+    """The C entry without pairs takes no positions and no plan: the norm
+    alone, or a copy."""
+    note(f"svdq_rope_axes without positions {T}")
+    H, D = 3, 40
+    q = heads(T, H, D, 1)
+    w = (1 + 0.1 * heads(1, 1, D, 7)).flatten()
+    plan = svdq.RopePlan((0,), head_dim=D)
+    for norm in (None, w):
+        y = torch.zeros_like(q)
+        side = svdq._lib.RopeHeads(q.data_ptr(), H * D, D, H, None if norm is None else norm.data_ptr(), y.data_ptr(), H * D, D)
+        svdq.svdq_rope_axes(side, None, T, D, 0, None, 0, 1, None, None, 0, 0, 0, 1e-6)
+        assert torch.equal(y, svdq.rope_axes(q, None, positions(T, 1, 2), plan, q_norm=norm))
+        assert norm is not None or torch.equal(y, q)
+
+
 def test_qkv_block_over_a_four_bit_layer():
     """FusedQKV over a W4A4 layer is the layer's call and then the rotation."""
     note("FusedQKV over SvdqLinear")
