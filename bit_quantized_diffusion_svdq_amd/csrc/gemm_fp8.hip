@@ -20,7 +20,9 @@ namespace {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-// byte offset past any buffer: a load there returns 0
+// byte offset past any buffer: a load there returns 0. (The range check takes
+// the lane's and the wave's offset together, and their sum stays below 2^32:
+// checked on gfx950 for loads into registers and into LDS.)
 constexpr int kBeyond = 0x7ffffff0;
 
 // D = A(16x128) * B(128x16) from zero, both E4M3: lane l holds 32 bytes of

@@ -279,6 +279,13 @@ def test_layer_refuses(M, kw, text):
         svdq.Fp8Linear(a["qw"], a["sw"])(x)
 
 
+def test_names_are_public():
+    names = ("svdq_quantize_act_fp8", "svdq_quantize_weight_fp8", "svdq_gemm_fp8", "svdq_gemm_fp8_grouped",
+             "svdq_linear_fp8", "svdq_rope_axes", "Fp8Linear", "Fp8GroupedLinear", "fp8_linear", "fp8_grouped_linear",
+             "quantize_act_fp8", "quantize_fp8", "RopePlan", "rope_axes", "FusedQKV", "save_fp8_layer", "load_fp8_layer")
+    assert all(n in svdq.__all__ and hasattr(svdq, n) for n in names)
+
+
 def test_quantisers_refuse():
     for x in (torch.zeros((3, 32)), torch.zeros((3, 40), dtype=bf), torch.zeros((3, 0), dtype=bf),
               torch.zeros(32, dtype=bf), torch.zeros((32, 3), dtype=bf).t(), torch.zeros((3, 32), dtype=bf)):
