@@ -65,8 +65,8 @@ def quantize_act_fp8(x: torch.Tensor, stream=None):
     with _on(x, stream):
         if ldx < K or ldx % 8:                  # a broadcast or unaligned row stride
             x, ldx = x.contiguous(), K
-        qx = torch.empty((M, K), dtype=E4M3, device=x.device)
-        sx = torch.empty((blocks(K), M), dtype=_F32, device=x.device)
+        # (x.new_empty costs half a us less than torch.empty)
+        qx, sx = x.new_empty(M, K, dtype=E4M3), x.new_empty(blocks(K), M, dtype=_F32)
         _lib.svdq_quantize_act_fp8(x, M, K, ldx, qx, sx)
     return qx, sx
 
@@ -118,10 +118,10 @@ def _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, groups):
     return M, K, N, out_dtype
 
 
-def _output(y, M, N, out_dtype, dev):
+def _output(y, M, N, out_dtype, like):
     """(y, its row stride)"""
     if y is None:
-        return torch.empty((M, N), dtype=out_dtype, device=dev), N
+        return like.new_empty(M, N, dtype=out_dtype), N
     return y, y.stride(0) if M > 1 else N
 
 
@@ -132,7 +132,7 @@ def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfl
     or fp32; rows of a given y may be strided)."""
     M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, 0)
     with _on(qx, stream):
-        y, ldy = _output(y, M, N, out_dtype, qx.device)
+        y, ldy = _output(y, M, N, out_dtype, qx)
         _lib.svdq_gemm_fp8(qx, sx, M, K, qw, sw, N, bias, _lib.ACT[act], y, int(out_dtype is _F32), ldy)
     return y
 
@@ -152,7 +152,7 @@ def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", ou
     if offsets.device != qx.device:
         raise ValueError(f"offsets is on {offsets.device}, expected {qx.device}")
     with _on(qx, stream):
-        y, ldy = _output(y, M, N, out_dtype, qx.device)
+        y, ldy = _output(y, M, N, out_dtype, qx)
         _lib.svdq_gemm_fp8_grouped(qx, sx, M, K, qw, sw, N, offsets, groups, bias, _lib.ACT[act], y,
                                    int(out_dtype is _F32), ldy)
     return y
@@ -181,7 +181,7 @@ def _linear_few(x, qw, sw, bias, act, out_dtype, y):
     if y is None:
         if not (out_dtype is _BF16 or out_dtype is _F32):
             return None
-        y, ldy = torch.empty((M, N), dtype=out_dtype, device=dev), N
+        y, ldy = x.new_empty(M, N, dtype=out_dtype), N
     else:
         ldy = y.stride(0) if y.dim() == 2 and M > 1 else N
         if not (y.shape == (M, N) and (y.dtype is _BF16 or y.dtype is _F32) and y.device == dev

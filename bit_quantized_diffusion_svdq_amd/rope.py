@@ -76,7 +76,7 @@ def _side(x, y, norm, T, H, D):
     ts, hs = _strides(x, T, H, D)
     yts, yhs = (H * D, D) if y is None else _strides(y, T, H, D)
     if y is None:
-        y = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+        y = x.new_empty(T, H, D)
     return y, RopeHeads(x.data_ptr(), ts, hs, H, None if norm is None else norm.data_ptr(), y.data_ptr(), yts, yhs)
 
 
