@@ -184,7 +184,7 @@ DEV void store1(const Args& a, int64_t row, int col, float v) {
 DEV void store4(const Args& a, int64_t row, int col, const float* v) {
     if (a.vec && col + 4 <= a.N) {
         if (a.y_f32) *(float4*)((float*)a.y + row * a.ldy + col) = make_float4(v[0], v[1], v[2], v[3]);
-        else *(uint2*)((uint16_t*)a.y + row * a.ldy + col) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        else *(uint2*)((uint16_t*)a.y + row * a.ldy + col) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -450,7 +450,7 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
             const int at = (j * 16 + q4 * 4) * ES;
             char* d = stg + l16 * RB + ((((at >> 4) ^ l16) & (CPR - 1)) << 4) + (at & 15);
             if constexpr (C::PREC) *(float4*)d = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
-            else *(uint2*)d = make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
+            else *(uint2*)d = make_uint2(bf16x2(acc[i][j][0], acc[i][j][1]), bf16x2(acc[i][j][2], acc[i][j][3]));
         }
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {

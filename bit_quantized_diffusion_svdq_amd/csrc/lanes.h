@@ -1,4 +1,4 @@
-// Exchanges between the lanes of a wave without LDS.
+// Exchanges between the lanes of a wave without LDS, and pairs of bf16 values.
 #pragma once
 #include "common.h"
 
@@ -11,4 +11,12 @@ template <int STEP>
 DEV float lane16_other(float v) {
     constexpr int ctrl = STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : STEP == 2 ? 0x141 : 0x140;
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, true));
+}
+
+// Two values to two bf16, nearest even, in one conversion (pack_bf16x2 gives
+// the same bits in four instructions).
+DEV uint32_t bf16x2(float lo, float hi) {
+    typedef float v2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2{lo, hi}, b2));
 }

@@ -71,11 +71,11 @@ DEV void store8(void* p, int64_t at, int e0, int e1, const float* v) {
         *(float4*)((float*)p + at + e0) = make_float4(v[0], v[1], v[2], v[3]);
         *(float4*)((float*)p + at + e1) = make_float4(v[4], v[5], v[6], v[7]);
     } else if constexpr (HALF) {
-        *(uint2*)((uint16_t*)p + at + e0) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-        *(uint2*)((uint16_t*)p + at + e1) = make_uint2(pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        *(uint2*)((uint16_t*)p + at + e0) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+        *(uint2*)((uint16_t*)p + at + e1) = make_uint2(bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
     } else {
-        *(uint4*)((uint16_t*)p + at + e0) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        *(uint4*)((uint16_t*)p + at + e0) = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]),
+                                                       bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
     }
 }
 
