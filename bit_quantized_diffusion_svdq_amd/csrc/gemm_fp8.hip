@@ -692,8 +692,8 @@ void launch_layer(const Args& a, int cus, hipStream_t stream) {
 //    64 x 4096 x 12288 26 (15 in tiles); 48 rows of 32 groups x 2048 x 4096 37
 //    with 32 columns, 43 in tiles.
 // Over 500 sizes of 1 to 64 rows and 435 of 77 to 4608 the variant it picks is
-// half a per cent slower than the best one on the average, over 170 grouped
-// ones 4.5.
+// half a per cent slower than the best one on the average, over 500 grouped
+// ones (half to 2300 rows a group, ragged) 3.5: it does not know the groups' sizes.
 struct Variant {
     int rows, cols, few;             // outputs per workgroup; few: the few-rows kernel
     int per_cu, trip;                // workgroups on a CU; K blocks per trip of a few-rows workgroup
