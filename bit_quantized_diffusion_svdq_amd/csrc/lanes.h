@@ -16,7 +16,6 @@ DEV float lane16_other(float v) {
 // Two values to two bf16, nearest even, in one conversion (pack_bf16x2 gives
 // the same bits in four instructions).
 DEV uint32_t bf16x2(float lo, float hi) {
-    typedef float v2 __attribute__((ext_vector_type(2)));
     typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2{lo, hi}, b2));
+    return __builtin_bit_cast(uint32_t, b2{(__bf16)lo, (__bf16)hi});
 }
