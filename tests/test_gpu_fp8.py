@@ -283,6 +283,116 @@ def test_grouped_many_groups(E, M):
     check_product(y, ref, K)
 
 
+# ---------------------------------------------------------------- every tile size
+
+def check_all_and_some(y, qx, sx, qw, sw, bias, rows, K):
+    """Every output against an fp32 product of the codes' values on the GPU, a
+    few rows against the oracle. The loose bound of the first: the E4M3
+    instructions lose at most 7 x 2^-13 of the sum of the largest terms, which
+    the sum of all magnitudes bounds; the fp32 sums of either side at most
+    2 (K + 8) 2^-24 of it; bf16 outputs half a step, 2^-8 of the value."""
+    kb = sx.shape[0]
+    xv = qx.float() * sx.t().repeat_interleave(128, 1)[:, :K]
+    wv = qw.float() * sw.repeat_interleave(128, 0)[:qw.shape[0]].repeat_interleave(128, 1)[:, :K]
+    full, mag = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    if bias is not None:
+        full, mag = full + bias.float(), mag + bias.float().abs()
+    bf = y.dtype == torch.bfloat16
+    bound = ((7 * 2.0 ** -13 if bf else 0.0) + 4 * (K + kb + 8) * 2.0 ** -24) * mag
+    if bf:
+        bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * full.abs()
+    bad = ~((y.float() - full).abs() <= bound)
+    assert not bad.any(), f"{int(bad.sum())} outputs outside the bound, first at {bad.nonzero()[0].tolist()}"
+    ref = ofp8.linear(np64(qx[rows]), sx[:, rows].cpu().numpy(), np64(qw), sw.cpu().numpy(),
+                      None if bias is None else np64(bias))
+    check_product(y[rows], ref, K)
+
+
+# sizes that between them take every tile size
+TILES = [(2405, 400, 6152), (4700, 144, 2603), (2405, 1168, 4104), (6007, 400, 1288), (4111, 1168, 1001), (700, 144, 3000),
+         (6007, 400, 6152), (3600, 400, 520), (700, 1168, 3000), (130, 400, 6152), (6007, 1168, 129), (257, 1168, 1001),
+         # more than 64 blocks of K: the weight's scales come in two runs
+         (2405, 8336, 6152), (4700, 8336, 2603), (2405, 8336, 4104), (6007, 8336, 1288), (4111, 8336, 1001), (700, 8336, 3000),
+         (3600, 8336, 520), (130, 8336, 6152), (257, 16400, 1001)]
+
+
+@pytest.mark.parametrize("M,K,N", TILES)
+def test_every_tile_size(M, K, N):
+    note(f"fp8_linear tiles {M} x {K} x {N}")
+    d = svdq.quantize_fp8(weights(K, N, N), biases(N, K) if M % 2 else None)
+    qx, sx = svdq.quantize_act_fp8(acts(M, K, M))
+    y = svdq.fp8_linear(qx, sx, d["qw"], d["sw"], d["bias"])
+    check_all_and_some(y, qx, sx, d["qw"], d["sw"], d["bias"], [0, 1, M // 3, M // 2 + 5, M - 2, M - 1], K)
+
+
+@pytest.mark.parametrize("M,K,N", [(4111, 400, 520), (2405, 144, 1001), (300, 1168, 520), (4111, 8336, 520), (257, 16400, 520)])
+def test_every_tile_size_fp32(M, K, N):
+    note(f"fp8_linear tiles, fp32 outputs {M} x {K} x {N}")
+    d = svdq.quantize_fp8(weights(K, N, N), biases(N, K))
+    qx, sx = svdq.quantize_act_fp8(acts(M, K, M))
+    y = svdq.fp8_linear(qx, sx, d["qw"], d["sw"], d["bias"], out_dtype=torch.float32)
+    check_all_and_some(y, qx, sx, d["qw"], d["sw"], d["bias"], [0, 17, M // 2, M - 1], K)
+
+
+@pytest.mark.parametrize("M,K,N", [(2000, 400, 6152), (4700, 144, 2603), (1030, 1168, 9001), (6007, 400, 1288), (4111, 1168, 1001),
+                                   (300, 400, 6152), (1500, 400, 1288), (257, 400, 3000), (90, 1168, 1288)])
+def test_every_tile_size_grouped(M, K, N):
+    """Three groups, one of a single row, the last tiles of the others with few
+    or no rows for half of their waves; rows of no group stay."""
+    note(f"fp8_grouped_linear tiles {M} x {K} x {N}")
+    d = svdq.quantize_fp8(weights(K, N, N, groups=3), biases((3, N), K))
+    qx, sx = svdq.quantize_act_fp8(acts(M, K, M))
+    cut = M * 3 // 5 // 32 * 32 + 5                       # a tile's first rows at the end of the first group
+    offs = [0, cut, cut + 1, M - 2]
+    y = torch.full((M, N), -3.0, dtype=torch.bfloat16, device="cuda")
+    svdq.fp8_grouped_linear(qx, sx, torch.tensor(offs, dtype=torch.int32, device="cuda"), d["qw"], d["sw"], d["bias"], y=y)
+    assert (y[M - 2:] == -3.0).all()
+    for g in range(3):
+        r = slice(offs[g], offs[g + 1])
+        n = offs[g + 1] - offs[g]
+        check_all_and_some(y[r], qx[r], sx[:, r].contiguous(), d["qw"][g], d["sw"][g], d["bias"][g], sorted({0, n // 2, n - 1}), K)
+
+
+def test_offsets_past_32_bits():
+    """A batch whose values, codes and outputs each pass 2^31: the last rows
+    are those of a small batch."""
+    note("fp8 batch past 2^31 values")
+    M, K, N = 264_007, 8208, 8200
+    assert M * K > 2 ** 31 and M * N > 2 ** 31
+    d = svdq.quantize_fp8(weights(K, N, 1), biases(N, 2))
+    tail = acts(300, K, 3)
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[-300:] = tail
+    qx, sx = svdq.quantize_act_fp8(x)
+    qt, st = svdq.quantize_act_fp8(tail)
+    assert torch.equal(qx[-300:].view(torch.uint8), qt.view(torch.uint8)) and torch.equal(sx[:, -300:], st)
+    assert (qx[:-300].view(torch.uint8) == 0).all()
+    del x
+    y = svdq.fp8_linear(qx, sx, d["qw"], d["sw"], d["bias"])
+    assert torch.equal(y[:1], d["bias"][None]) and torch.equal(y[M - 302:M - 300], d["bias"].expand(2, N))
+    check_all_and_some(y[-300:], qt, st, d["qw"], d["sw"], d["bias"], [0, 150, 299], K)
+    # the same rows as the second of two groups that share one weight
+    two = svdq.fp8_grouped_linear(qx, sx, torch.tensor([0, M - 300, M], dtype=torch.int32, device="cuda"),
+                                  d["qw"].expand(2, N, K).contiguous(), d["sw"].expand(2, -1, -1).contiguous(), y=y)
+    assert (two[:1] == 0).all() and (two[M - 301] == 0).all()
+    check_all_and_some(two[-300:], qt, st, d["qw"], d["sw"], None, [0, 150, 299], K)
+
+
+@pytest.mark.parametrize("M", [7, 700])
+def test_weights_past_32_bits(M):
+    """Groups' weights past 2^31 bytes: all rows in the last one."""
+    note(f"fp8_grouped_linear weights past 2^31 bytes, {M} rows")
+    E, K, N = 33, 8208, 8200
+    assert (E - 1) * N * K > 2 ** 31
+    qw = torch.zeros((E, N, K), dtype=torch.uint8, device="cuda")
+    qw[-1] = torch.randint(0, 0x7F, (N, K), dtype=torch.uint8, generator=torch.Generator().manual_seed(M)).cuda()
+    qw = qw.view(E4M3)
+    sw = torch.rand((E, -(-N // 128), -(-K // 128)), generator=torch.Generator().manual_seed(1)).cuda()
+    qx, sx = svdq.quantize_act_fp8(acts(M, K, 3))
+    y = svdq.fp8_grouped_linear(qx, sx, torch.tensor([0] * E + [M], dtype=torch.int32, device="cuda"), qw, sw)
+    check_all_and_some(y, qx, sx, qw[-1], sw[-1], None, [0, M - 1], K)
+
+
 # ---------------------------------------------------------------- how a program has them
 
 def test_layers_on_streams_and_in_a_graph():

@@ -182,6 +182,21 @@ def test_streams_graphs_and_non_finite():
     assert bad[3, 1].all() and bad.sum() == D
 
 
+def test_offsets_past_32_bits():
+    """Heads past 2^31 values, in place: the last tokens are those of a short
+    sequence, and tokens of zeros stay zero."""
+    note("rope_axes past 2^31 values")
+    T, H, D = 530_003, 32, 128
+    assert T * H * D > 2 ** 31
+    plan = svdq.RopePlan((16, 56, 56))
+    q = torch.zeros((T, H, D), dtype=torch.bfloat16, device="cuda")
+    tail, pos = heads(40, H, D, 1), positions(T, 3, 2)
+    q[-40:] = tail
+    assert svdq.rope_axes(q, None, pos, plan, q_out=q) is q
+    want = svdq.rope_axes(tail, None, pos[-40:].contiguous(), plan)
+    assert torch.equal(q[-40:], want) and (q[0] == 0).all() and (q[-41] == 0).all()
+
+
 @pytest.mark.parametrize("T", [1, 9])
 def test_no_pairs_no_positions(T):
     """The C entry without pairs takes no positions and no plan: the norm
