@@ -747,10 +747,13 @@ double estimate(const Variant& v, const Args& a, int cus) {
         const double trips = turns * v.lone * __builtin_ceil(kb / v.trip), reads = g * (v.cols + rows) * a.K / 2.9e4;
         t = trips > reads ? trips : reads;
     } else {
+        // exact products for fp32 outputs take the bf16 instructions twice the time (over
+        // 660 sizes 1.8 % behind the best variant, 2.2 without)
+        const double kt = a.y_f32 ? 2.0 * kb : kb;
         const double slots = (double)cus * v.per_cu, rounds = __builtin_floor(tiles / slots);
         const double rest = __builtin_ceil((tiles - rounds * slots) / cus);
         const double share = v.full * rest / v.per_cu, out = 4.0 * v.rows * v.cols * v.per_cu / 65536.0;
-        t = rounds * (kb * v.full + out) + (rest > 0 ? kb * (share > v.lone ? share : v.lone) + out * rest / v.per_cu : 0.0);
+        t = rounds * (kt * v.full + out) + (rest > 0 ? kt * (share > v.lone ? share : v.lone) + out * rest / v.per_cu : 0.0);
     }
     return 3.0 + (t > weights ? t : weights);
 }
