@@ -654,16 +654,22 @@ __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
     }
 }
 
+// the most row tiles that M rows in E ragged groups (0: one batch) can need; each has a row
+int64_t row_tiles(const Args& a, int bm) {
+    const int64_t t = a.offs ? (a.M + (int64_t)a.E * (bm - 1)) / bm : (a.M + bm - 1) / bm;
+    return t < a.M ? t : a.M;
+}
+
 template <class C, bool GROUPED>
 void launch_tiles(const Args& a, hipStream_t stream) {
-    const int64_t tm = GROUPED ? (a.M + (int64_t)a.E * (C::BM - 1)) / C::BM : (a.M + C::BM - 1) / C::BM;
+    const int64_t tm = row_tiles(a, C::BM);
     const int64_t tn = (a.N + C::BN - 1) / C::BN;
     hipLaunchKernelGGL((gemm_fp8_kernel<C, GROUPED>), dim3((unsigned)(tm * tn)), dim3(C::NT), 0, stream, a);
 }
 
 template <class C, bool GROUPED>
 void launch_few(const Args& a, hipStream_t stream) {
-    const int64_t tm = GROUPED ? (a.M + (int64_t)a.E * (16 * C::MT - 1)) / (16 * C::MT) : (a.M + 16 * C::MT - 1) / (16 * C::MT);
+    const int64_t tm = row_tiles(a, 16 * C::MT);
     const int64_t tn = (a.N + 16 * C::NT - 1) / (16 * C::NT);
     hipLaunchKernelGGL((gemm_fp8_few_kernel<C, GROUPED ? GROUPS : DENSE>), dim3((unsigned)(tm * tn)), dim3(64 * C::NW), 0, stream, a);
 }
