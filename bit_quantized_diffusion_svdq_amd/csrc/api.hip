@@ -63,8 +63,8 @@ hipError_t launch_gemm_fp8(const uint8_t* qx, const float* sx, int64_t M, int64_
                            int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
                            int64_t ldy, int cus, hipStream_t stream);
 hipError_t launch_linear_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw, const float* sw,
-                             int64_t N, const uint16_t* bias, int act, void* y, int y_f32, int64_t ldy, int cus,
-                             hipStream_t stream);
+                             int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
+                             int64_t ldy, int cus, hipStream_t stream);
 hipError_t launch_gemm_w4a4_next(const uint8_t* qx, const uint16_t* sx, const uint8_t* qw,
                                  const uint16_t* sw, const float* xl1, const uint16_t* l2t, int rank,
                                  const uint16_t* bias, int act, int64_t M, int64_t N, int64_t K,
@@ -787,6 +787,40 @@ svdq_status gemm_fp8_impl(const void* qx, const float* sx, int64_t M, int64_t K,
                     what);
 }
 
+svdq_status linear_fp8_impl(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
+                            int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act, void* y,
+                            int32_t y_dtype, int64_t ldy, void* stream, const char* what) {
+    svdq_status s;
+    if (M < 0 || M > 16) return fail(SVDQ_ERR_SHAPE, "M = %lld must be in [0, 16]", (long long)M);
+    if ((s = check_k_fp8(K)) != SVDQ_OK) return s;
+    if (M * ((K + 127) / 128) > 256)
+        return fail(SVDQ_ERR_SHAPE, "M = %lld times the %lld blocks of K must not pass 256", (long long)M, (long long)((K + 127) / 128));
+    if (N <= 0 || N >= (int64_t)1 << 26) return fail(SVDQ_ERR_SHAPE, "N = %lld must be in [1, 2^26)", (long long)N);
+    // a row tile a row at the most, 512 lanes a workgroup
+    if (groups && M * ((N + 15) / 16) >= ((int64_t)1 << 23))
+        return fail(SVDQ_ERR_SHAPE, "M = %lld x N = %lld needs more tiles than one launch holds", (long long)M, (long long)N);
+    if (groups < 0 || groups > 65536) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
+    if (ldx < K) return fail(SVDQ_ERR_SHAPE, "ldx = %lld < K = %lld", (long long)ldx, (long long)K);
+    if (ldx % 8) return fail(SVDQ_ERR_ALIGN, "ldx = %lld must be a multiple of 8", (long long)ldx);
+    if (ldy < N) return fail(SVDQ_ERR_SHAPE, "ldy = %lld < N = %lld", (long long)ldy, (long long)N);
+    if (ldy >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "ldy = %lld must be below 2^31", (long long)ldy);
+    if ((s = check_act(act)) != SVDQ_OK) return s;
+    if (y_dtype != SVDQ_DT_BF16 && y_dtype != SVDQ_DT_F32)
+        return fail(SVDQ_ERR_UNSUPPORTED, "output dtype %d is not supported", y_dtype);
+    if (M == 0) { g_last_error.clear(); return SVDQ_OK; }
+    if (!x || !qw || !sw || !y || (groups && !offsets))
+        return fail(SVDQ_ERR_NULL, "x, qw, sw and y%s are required", groups ? ", offsets" : "");
+    if (!aligned(x, 16) || !aligned(qw, 16) || !aligned(sw, 4) || (bias && !aligned(bias, 2)) ||
+        !aligned(y, y_dtype == SVDQ_DT_F32 ? 4 : 2) || (offsets && !aligned(offsets, 4)))
+        return fail(SVDQ_ERR_ALIGN, "x, qw need 16-byte alignment, sw, offsets 4, bias 2, y its element's");
+    int cus = 0;
+    if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
+    return launched(launch_linear_fp8((const uint16_t*)x, M, K, ldx, (const uint8_t*)qw, sw, N, offsets, groups,
+                                      (const uint16_t*)bias, act, y, y_dtype == SVDQ_DT_F32, ldy, cus,
+                                      (hipStream_t)stream),
+                    what);
+}
+
 svdq_status check_rope_heads(const svdq_rope_heads* h, const char* name, int min_heads, int64_t T, int64_t D) {
     if (h->heads < min_heads || h->heads > 65536)
         return fail(SVDQ_ERR_SHAPE, "%s: %d heads must be in [%d, 65536]", name, h->heads, min_heads);
@@ -866,29 +900,16 @@ svdq_status svdq_gemm_fp8_grouped(const void* qx, const float* sx, int64_t M, in
 svdq_status svdq_linear_fp8(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
                             int64_t N, const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
                             void* stream) {
-    svdq_status s;
-    if (M < 0 || M > 16) return fail(SVDQ_ERR_SHAPE, "M = %lld must be in [0, 16]", (long long)M);
-    if ((s = check_k_fp8(K)) != SVDQ_OK) return s;
-    if (M * ((K + 127) / 128) > 256)
-        return fail(SVDQ_ERR_SHAPE, "M = %lld times the %lld blocks of K must not pass 256", (long long)M, (long long)((K + 127) / 128));
-    if (N <= 0 || N >= (int64_t)1 << 26) return fail(SVDQ_ERR_SHAPE, "N = %lld must be in [1, 2^26)", (long long)N);
-    if (ldx < K) return fail(SVDQ_ERR_SHAPE, "ldx = %lld < K = %lld", (long long)ldx, (long long)K);
-    if (ldx % 8) return fail(SVDQ_ERR_ALIGN, "ldx = %lld must be a multiple of 8", (long long)ldx);
-    if (ldy < N) return fail(SVDQ_ERR_SHAPE, "ldy = %lld < N = %lld", (long long)ldy, (long long)N);
-    if (ldy >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "ldy = %lld must be below 2^31", (long long)ldy);
-    if ((s = check_act(act)) != SVDQ_OK) return s;
-    if (y_dtype != SVDQ_DT_BF16 && y_dtype != SVDQ_DT_F32)
-        return fail(SVDQ_ERR_UNSUPPORTED, "output dtype %d is not supported", y_dtype);
-    if (M == 0) { g_last_error.clear(); return SVDQ_OK; }
-    if (!x || !qw || !sw || !y) return fail(SVDQ_ERR_NULL, "x, qw, sw and y are required");
-    if (!aligned(x, 16) || !aligned(qw, 16) || !aligned(sw, 4) || (bias && !aligned(bias, 2)) ||
-        !aligned(y, y_dtype == SVDQ_DT_F32 ? 4 : 2))
-        return fail(SVDQ_ERR_ALIGN, "x, qw need 16-byte alignment, sw 4, bias 2, y its element's");
-    int cus = 0;
-    if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
-    return launched(launch_linear_fp8((const uint16_t*)x, M, K, ldx, (const uint8_t*)qw, sw, N, (const uint16_t*)bias,
-                                      act, y, y_dtype == SVDQ_DT_F32, ldy, cus, (hipStream_t)stream),
-                    "svdq_linear_fp8 launch");
+    return linear_fp8_impl(x, M, K, ldx, qw, sw, N, nullptr, 0, bias, act, y, y_dtype, ldy, stream,
+                           "svdq_linear_fp8 launch");
+}
+
+svdq_status svdq_linear_fp8_grouped(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
+                                    int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act,
+                                    void* y, int32_t y_dtype, int64_t ldy, void* stream) {
+    if (groups < 1) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
+    return linear_fp8_impl(x, M, K, ldx, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, stream,
+                           "svdq_linear_fp8_grouped launch");
 }
 
 svdq_status svdq_rope_axes(const svdq_rope_heads* q, const svdq_rope_heads* k, int64_t T, int32_t D, int32_t dtype,

@@ -1,4 +1,4 @@
-// svdq_gemm_fp8 / svdq_gemm_fp8_grouped / svdq_linear_fp8: E4M3 x E4M3 products with one fp32
+// svdq_gemm_fp8, svdq_linear_fp8 and their grouped forms: E4M3 x E4M3 products with one fp32
 // scale per block of 128 input channels,
 //
 //   Y[m, n] = act( sum_b sx[b, m] sw[n / 128, b] P_b[m, n] + bias[n] ),
@@ -505,28 +505,31 @@ struct FewCfg {
 };
 
 // What its activations are: codes of one batch, codes of ragged groups, or bf16
-// values, which every workgroup turns into codes in LDS for itself while its
-// first weights are on their way (LAYER: one launch instead of two). That
+// values of either, which every workgroup turns into codes in LDS for itself while
+// its first weights are on their way (one launch instead of two). That
 // costs rows x blocks of vector work per workgroup, so it is for few of them:
 // 1 x 4096 x 18432 takes 16.3 us (20.2 in two launches, 16.9 their product
 // alone), 1 x 18432 x 4096 18.2 (22.4), 16 x 1536 x 6144 7.3 (8.2); even at 256
 // rows x blocks, 8 x 4096 x 18432 24.6 (24.9), 8 x 4096 x 4096 9.4 (9.1); behind
-// at 384, 4 x 12288 x 4096 17.6 (16.1). The codes are the activation pass's.
-enum { DENSE, GROUPS, LAYER };
+// at 384, 4 x 12288 x 4096 17.6 (16.1). Grouped, 2 rows of 8 groups x 2048 x 4096
+// take 5.8 (8.4), 4 of 8 x 4096 x 4096 13.9 (14.7). The codes are the activation
+// pass's.
+enum { DENSE, GROUPS, LAYER, LAYER_GROUPS };
 
 template <class C, int KIND>
 __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
     constexpr int MT = C::MT, NT = C::NT, NW = C::NW, U = C::U;
-    static_assert(KIND != LAYER || MT == 1, "up to 16 rows");
+    constexpr bool OWN = KIND >= LAYER, RAGGED = KIND == GROUPS || KIND == LAYER_GROUPS;
+    static_assert(!OWN || MT == 1, "up to 16 rows");
     constexpr int QB = 3;                                // blocks of activations in flight per 16 lanes
     __shared__ __attribute__((aligned(16))) v4f red[NW][MT * NT][64];
-    extern __shared__ __attribute__((aligned(16))) char codes[];   // LAYER: M rows of codes, then M rows of scales
+    extern __shared__ __attribute__((aligned(16))) char codes[];   // OWN: its rows of codes, then their scales
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q4 = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int tiles_n = (a.N + 16 * NT - 1) / (16 * NT);
     const int t = blockIdx.x;
     Rows rr;
-    if constexpr (KIND == GROUPS) {
+    if constexpr (RAGGED) {
         int total;
         rr = group_rows(a, t / tiles_n, 16 * MT, &total);
         if (t / tiles_n >= total) return;
@@ -538,7 +541,7 @@ __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
     const int n0 = (t % tiles_n) * 16 * NT;
     const int K = a.K, KB = (K + 127) / 128, NB = (a.N + 127) / 128;
     const int nrows = a.N - n0 < 16 * NT ? a.N - n0 : 16 * NT;
-    const rsrc_t rx = make_rsrc(a.qx + rr.m0 * K, KIND == LAYER ? 0 : (int64_t)rr.rows * K);
+    const rsrc_t rx = make_rsrc(a.qx + rr.m0 * K, OWN ? 0 : (int64_t)rr.rows * K);
     const rsrc_t rw = make_rsrc(a.qw + ((int64_t)rr.g * a.N + n0) * K, (int64_t)nrows * K);
     const float* swp = a.sw + ((int64_t)rr.g * NB + n0 / 128) * KB;
     const float* sxp = a.sx + rr.m0;
@@ -570,7 +573,7 @@ __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
             sw[u] = swp[kb < KB ? kb : KB - 1];
         }
     };
-    if constexpr (KIND == LAYER) {
+    if constexpr (OWN) {
         load_w(wave);                                    // on their way while the activations are turned
         const int pairs = rr.rows * KB;                  // (row, block): 16 lanes each
         for (int p0 = tid >> 4; p0 < pairs; p0 += QB * NW * 4) {
@@ -579,7 +582,7 @@ __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
             for (int b = 0; b < QB; ++b) {
                 const int p = p0 + b * NW * 4, m = p / KB, k = (p - m * KB) * 128 + l16 * 8;
                 v[b] = make_uint4(0u, 0u, 0u, 0u);
-                if (p < pairs && k < K) v[b] = *(const uint4*)(a.x + m * a.ldx + k);
+                if (p < pairs && k < K) v[b] = *(const uint4*)(a.x + (rr.m0 + m) * a.ldx + k);
             }
 #pragma unroll
             for (int b = 0; b < QB; ++b) {
@@ -596,7 +599,7 @@ __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
     for (int kb0 = wave; kb0 < KB; kb0 += NW * U) {
         uint4 x[U][MT][2];
         float s[U][MT];
-        if (KIND != LAYER || kb0 != wave) load_w(kb0);
+        if (!OWN || kb0 != wave) load_w(kb0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int kb = kb0 + u * NW, kc = kb < KB ? kb : KB - 1;
@@ -606,12 +609,12 @@ __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
                 const int v = 64 * h < left ? vo + 64 * h : kBeyond;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
-                    if constexpr (KIND == LAYER) x[u][i][h] = *(const uint4*)(codes + ms[i] * pitch + kc * 128 + 64 * h + 16 * q4);
+                    if constexpr (OWN) x[u][i][h] = *(const uint4*)(codes + ms[i] * pitch + kc * 128 + 64 * h + 16 * q4);
                     else x[u][i][h] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rx, v, kb * 128 + i * 16 * K, 0));
                 }
             }
 #pragma unroll
-            for (int i = 0; i < MT; ++i) s[u][i] = (KIND == LAYER ? scales[ms[i] * KB + kc] : sxp[(int64_t)kc * a.M + ms[i]]) * sw[u];
+            for (int i = 0; i < MT; ++i) s[u][i] = (OWN ? scales[ms[i] * KB + kc] : sxp[(int64_t)kc * a.M + ms[i]]) * sw[u];
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -678,16 +681,17 @@ void launch_few(const Args& a, hipStream_t stream) {
 // K and the narrow ones would come in turns: 1 x 1536 x 6144 takes 5.1 us with
 // 32 (5.6 with 16), but 1 x 4096 x 18432 21.4 (16.2) and 1 x 1024 x 1024, 64
 // narrow workgroups, 4.1 (3.7).
-template <int PREC>
+template <int PREC, int KIND>
 void launch_layer(const Args& a, int cus, hipStream_t stream) {
     const int KB = (a.K + 127) / 128;
     const size_t lds = (size_t)a.M * (KB * 128 + 16 + KB * 4);
-    if (KB <= 16 && (a.N + 15) / 16 > cus) {
+    const int64_t tm = row_tiles(a, 16), narrow = tm * ((a.N + 15) / 16);
+    if (KB <= 16 && narrow > cus) {
         typedef FewCfg<1, 2, 8, 2, PREC> C;
-        hipLaunchKernelGGL((gemm_fp8_few_kernel<C, LAYER>), dim3((unsigned)((a.N + 31) / 32)), dim3(64 * C::NW), lds, stream, a);
+        hipLaunchKernelGGL((gemm_fp8_few_kernel<C, KIND>), dim3((unsigned)(tm * ((a.N + 31) / 32))), dim3(64 * C::NW), lds, stream, a);
     } else {
         typedef FewCfg<1, 1, 8, 4, PREC> C;
-        hipLaunchKernelGGL((gemm_fp8_few_kernel<C, LAYER>), dim3((unsigned)((a.N + 15) / 16)), dim3(64 * C::NW), lds, stream, a);
+        hipLaunchKernelGGL((gemm_fp8_few_kernel<C, KIND>), dim3((unsigned)narrow), dim3(64 * C::NW), lds, stream, a);
     }
 }
 
@@ -821,11 +825,11 @@ hipError_t launch_gemm_fp8(const uint8_t* qx, const float* sx, int64_t M, int64_
 }
 
 hipError_t launch_linear_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw, const float* sw,
-                             int64_t N, const uint16_t* bias, int act, void* y, int y_f32, int64_t ldy, int cus,
-                             hipStream_t stream) {
+                             int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
+                             int64_t ldy, int cus, hipStream_t stream) {
     const int vec = ldy % (y_f32 ? 4 : 8) == 0 && (uintptr_t)y % 16 == 0;
-    const Args a{nullptr, nullptr, qw, sw, bias, y, nullptr, M, ldy, (int)N, (int)K, 0, act, y_f32, vec, x, ldx};
-    if (y_f32) launch_layer<1>(a, cus, stream);
-    else launch_layer<0>(a, cus, stream);
+    const Args a{nullptr, nullptr, qw, sw, bias, y, offs, M, ldy, (int)N, (int)K, E, act, y_f32, vec, x, ldx};
+    if (offs) y_f32 ? launch_layer<1, LAYER_GROUPS>(a, cus, stream) : launch_layer<0, LAYER_GROUPS>(a, cus, stream);
+    else y_f32 ? launch_layer<1, LAYER>(a, cus, stream) : launch_layer<0, LAYER>(a, cus, stream);
     return hipGetLastError();
 }

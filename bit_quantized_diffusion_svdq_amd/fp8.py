@@ -137,6 +137,13 @@ def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfl
     return y
 
 
+def _groups(offsets) -> int:
+    if not (offsets.dtype is torch.int32 and offsets.dim() == 1 and offsets.numel() >= 2 and offsets.is_contiguous()):
+        raise ValueError(f"offsets must be a contiguous int32 vector of groups + 1 values, got {tuple(offsets.shape)} "
+                         f"{offsets.dtype}")
+    return offsets.numel() - 1
+
+
 def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfloat16, y=None,
                        stream=None):
     """fp8_linear with a weight per group: rows offsets[g] .. offsets[g + 1] - 1
@@ -144,10 +151,7 @@ def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", ou
     the GPU, rising, within [0, M] (read there: no synchronisation). Rows of
     no group (before offsets[0], from offsets[-1] on) are left as they are in
     a given y and are unspecified in a new one."""
-    if not (offsets.dtype is torch.int32 and offsets.dim() == 1 and offsets.numel() >= 2 and offsets.is_contiguous()):
-        raise ValueError(f"offsets must be a contiguous int32 vector of groups + 1 values, got {tuple(offsets.shape)} "
-                         f"{offsets.dtype}")
-    groups = offsets.numel() - 1
+    groups = _groups(offsets)
     M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, groups)
     if offsets.device != qx.device:
         raise ValueError(f"offsets is on {offsets.device}, expected {qx.device}")
@@ -158,25 +162,27 @@ def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", ou
     return y
 
 
-# what svdq_linear_fp8 takes: rows, and rows x blocks of 128 channels
+# what svdq_linear_fp8 and its grouped form take: rows, and rows x blocks of 128 channels
 _FEW_ROWS, _FEW_BLOCKS = 16, 256
 
 
-def _linear_few(x, qw, sw, bias, act, out_dtype, y):
+def _linear_few(x, qw, sw, bias, act, out_dtype, y, offsets=None):
     """The layer of few rows in one launch, or None for a call that has more
     or that is not the usual one (the two passes then say what is wrong)."""
     M, K = x.shape
     kb = blocks(K)
     dev = x.device
+    lead = () if offsets is None else (offsets.numel() - 1,)
     if not (0 < M <= _FEW_ROWS and M * kb <= _FEW_BLOCKS and x.is_cuda and x.dtype is _BF16 and K >= 16 and K % 16 == 0
             and x.stride(1) == 1 and qw.dtype is E4M3 and sw.dtype is _F32 and qw.device == dev and sw.device == dev
-            and qw.dim() == 2 and qw.is_contiguous() and sw.is_contiguous() and act in _lib.ACT):
+            and qw.dim() == 2 + len(lead) and qw.is_contiguous() and sw.is_contiguous() and act in _lib.ACT):
         return None
-    N = qw.shape[0]
+    N = qw.shape[-2]
     ldx = x.stride(0) if M > 1 else K
-    if not (N >= 1 and sw.shape == (blocks(N), kb)
-            and (bias is None or (bias.dtype is _BF16 and bias.shape == (N,) and bias.is_contiguous()
-                                  and bias.device == dev))):
+    if not (N >= 1 and M * N <= 1 << 26 and qw.shape == (*lead, N, K) and sw.shape == (*lead, blocks(N), kb)
+            and (bias is None or (bias.dtype is _BF16 and bias.shape == (*lead, N) and bias.is_contiguous()
+                                  and bias.device == dev))
+            and (offsets is None or offsets.device == dev)):
         return None
     if y is None:
         if not (out_dtype is _BF16 or out_dtype is _F32):
@@ -191,7 +197,11 @@ def _linear_few(x, qw, sw, bias, act, out_dtype, y):
             x, ldx = x.clone(memory_format=torch.contiguous_format), K   # in place: y is written while x is read
     if ldx < K or ldx % 8:                      # a broadcast or unaligned row stride
         x, ldx = x.contiguous(), K
-    _lib.svdq_linear_fp8(x, M, K, ldx, qw, sw, N, bias, _lib.ACT[act], y, int(y.dtype is _F32), ldy)
+    f32 = int(y.dtype is _F32)
+    if offsets is None:
+        _lib.svdq_linear_fp8(x, M, K, ldx, qw, sw, N, bias, _lib.ACT[act], y, f32, ldy)
+    else:
+        _lib.svdq_linear_fp8_grouped(x, M, K, ldx, qw, sw, N, offsets, lead[0], bias, _lib.ACT[act], y, f32, ldy)
     return y
 
 
@@ -257,11 +267,15 @@ class Fp8GroupedLinear:
     def __call__(self, x: torch.Tensor, offsets: torch.Tensor, act: str = "none", out_dtype=torch.bfloat16, y=None,
                  stream=None) -> torch.Tensor:
         """Y [M, N] for bf16 activations x [M, K] sorted by group
-        (fp8_grouped_linear's offsets)."""
+        (fp8_grouped_linear's offsets); in one launch for few rows, as
+        Fp8Linear."""
         if x.dim() != 2 or x.shape[1] != self.K:
             raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
-        if offsets.numel() != self.groups + 1:
+        if _groups(offsets) != self.groups:
             raise ValueError(f"offsets must hold {self.groups + 1} values, got {offsets.numel()}")
         with _on(x, stream):
+            out = _linear_few(x, self.qw, self.sw, self.bias, act, out_dtype, y, offsets)
+            if out is not None:
+                return out
             qx, sx = quantize_act_fp8(x)
             return fp8_grouped_linear(qx, sx, offsets, self.qw, self.sw, self.bias, act, out_dtype, y)

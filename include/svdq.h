@@ -562,6 +562,11 @@ svdq_status svdq_quantize_weight_fp8(const void* w, int64_t K, int64_t N, int64_
  *   N < 2^26. Equal to the two calls but for the order in which a row's
  *   blocks are summed in fp32. y must not overlap x (workgroups write it
  *   while others read x). M == 0 is valid.
+ *
+ * svdq_linear_fp8_grouped -- the same with a weight per group of rows
+ *   (svdq_gemm_fp8_grouped's offsets, arrays and untouched rows): the few
+ *   tokens of a step on their experts. Limits as above, over all M rows;
+ *   M * ceil(N/16) < 2^23.
  */
 svdq_status svdq_gemm_fp8(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
                           int64_t N, const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
@@ -573,6 +578,9 @@ svdq_status svdq_gemm_fp8_grouped(const void* qx, const float* sx, int64_t M, in
 svdq_status svdq_linear_fp8(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
                             int64_t N, const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
                             void* stream);
+svdq_status svdq_linear_fp8_grouped(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
+                                    int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act,
+                                    void* y, int32_t y_dtype, int64_t ldy, void* stream);
 
 /* ------------------------------------------------------------------------
  * svdq_rope_axes -- rotary positions with several axes (time, height, width

@@ -116,7 +116,25 @@ def test_layer_of_few_rows_rejects(lib, kw, status):
     assert status == OK or lib.svdq_last_error()
 
 
+def _few_grouped(lib, **kw):
+    a = dict(x=A, M=16, K=2048, ldx=2048, qw=C, sw=D, N=77, offs=E, groups=5, bias=None, act=0, y=F, ydt=0, ldy=77)
+    a.update(kw)
+    return lib.svdq_linear_fp8_grouped(a["x"], a["M"], a["K"], a["ldx"], a["qw"], a["sw"], a["N"], a["offs"], a["groups"],
+                                       a["bias"], a["act"], a["y"], a["ydt"], a["ldy"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=17, K=128), SHAPE), (dict(K=2064, ldx=2064), SHAPE), (dict(groups=0), SHAPE), (dict(groups=-1), SHAPE),
+    (dict(groups=65537), SHAPE), (dict(N=1 << 23, ldy=1 << 23), SHAPE), (dict(offs=None), NULL), (dict(offs=E + 2), ALIGN),
+    (dict(x=None), NULL), (dict(ldx=2052), ALIGN), (dict(y=F + 1), ALIGN), (dict(act=2), UNSUP), (dict(M=0, offs=None), OK),
+])
+def test_grouped_layer_of_few_rows_rejects(lib, kw, status):
+    assert _few_grouped(lib, **kw) == status
+    assert status == OK or lib.svdq_last_error()
+
+
 def test_layer_of_few_rows_limits(lib):
+    valid(_few_grouped(lib))
     valid(_few(lib))
     valid(_few(lib, M=1, K=32768, ldx=1 << 40, bias=E, N=(1 << 26) - 1, ldy=1 << 26))
 
@@ -279,9 +297,21 @@ def test_layer_refuses(M, kw, text):
         svdq.Fp8Linear(a["qw"], a["sw"])(x)
 
 
+@pytest.mark.parametrize("M", [2, 16, 400])
+@pytest.mark.parametrize("kw,text", [
+    (dict(offsets=torch.zeros(4, dtype=torch.int64)), "offsets must be"), (dict(offsets=torch.zeros(3, dtype=torch.int32)), "offsets must hold"),
+    (dict(x=torch.zeros((2, 128), dtype=bf)), "x must be"), (dict(), "GPU device"),
+])
+def test_grouped_layer_refuses(M, kw, text):
+    a = _prod(groups=3)
+    a = dict(qw=a["qw"], sw=a["sw"], x=torch.zeros((M, 144), dtype=bf), offsets=torch.zeros(4, dtype=torch.int32)) | kw
+    with pytest.raises(ValueError, match=text):
+        svdq.Fp8GroupedLinear(a["qw"], a["sw"])(a["x"], a["offsets"])
+
+
 def test_names_are_public():
     names = ("svdq_quantize_act_fp8", "svdq_quantize_weight_fp8", "svdq_gemm_fp8", "svdq_gemm_fp8_grouped",
-             "svdq_linear_fp8", "svdq_rope_axes", "Fp8Linear", "Fp8GroupedLinear", "fp8_linear", "fp8_grouped_linear",
+             "svdq_linear_fp8", "svdq_linear_fp8_grouped", "svdq_rope_axes", "Fp8Linear", "Fp8GroupedLinear", "fp8_linear", "fp8_grouped_linear",
              "quantize_act_fp8", "quantize_fp8", "RopePlan", "rope_axes", "FusedQKV", "save_fp8_layer", "load_fp8_layer")
     assert all(n in svdq.__all__ and hasattr(svdq, n) for n in names)
 

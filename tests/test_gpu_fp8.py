@@ -482,6 +482,44 @@ def test_layer_of_few_rows_views(dt, N, ld, off):
     assert (buf[rest] == -3.0).all()
 
 
+@pytest.mark.parametrize("offs,M,K,N", [([0, 1], 1, 144, 40), ([0, 0, 2, 2, 3], 4, 2048, 264), ([0, 16], 16, 2048, 100),
+                                        ([1, 4, 4, 15], 16, 400, 4200), ([0] * 70 + [3, 3, 7], 9, 1040, 72),
+                                        ([2, 3, 5, 8], 8, 4096, 129), ([0, 0, 0], 5, 128, 24), ([0, 9, 17], 17, 128, 40)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_grouped_layer_of_few_rows(offs, M, K, N, out):
+    """Grouped layers on a few bf16 rows: rows of no group stay."""
+    note(f"Fp8GroupedLinear {offs[-5:]} of {M} x {K} x {N} {out}")
+    E = len(offs) - 1
+    lay = svdq.Fp8GroupedLinear.from_quantized(svdq.quantize_fp8(weights(K, N, N, groups=E), biases((E, N), K)))
+    x = acts(M + 3, K + 24, M)[2:2 + M, 8:8 + K]
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    y = torch.full((M, N), -3.0, dtype=out, device="cuda")
+    act = "gelu_tanh" if E % 2 else "none"
+    assert lay(x, o, act=act, y=y) is y
+    qx, sx = ofp8.quantize_act(np64(x))
+    ref = ofp8.grouped_linear(qx, sx, offs, np64(lay.qw), lay.sw.cpu().numpy(), np64(lay.bias))
+    inside = ~np.isnan(ref[0][:, 0])
+    assert (np64(y)[~inside] == -3.0).all()
+    if inside.any():
+        check_product(y[torch.from_numpy(inside).cuda()], [r[inside] for r in ref], K, act)
+        keep = torch.from_numpy(inside).cuda()
+        assert torch.equal(lay(x, o, act=act, out_dtype=out)[keep], y[keep])
+
+
+@pytest.mark.parametrize("M", [6, 40])
+def test_grouped_offsets_that_are_wrong_stay_inside(M):
+    """Offsets outside [0, M] or falling are clamped: nothing outside y is
+    written (the rows themselves are then unspecified)."""
+    note(f"Fp8GroupedLinear with wrong offsets {M}")
+    K, N = 272, 72
+    lay = svdq.Fp8GroupedLinear.from_quantized(svdq.quantize_fp8(weights(K, N, 1, groups=4)))
+    x = acts(M, K, 2)
+    for offs in ([-5, 3, 1 << 30, 2, 4], [9, 7, 5, 3, 1], [0, M, 0, M, 0], [-(1 << 31)] * 4 + [(1 << 31) - 1]):
+        buf = torch.full((M + 80, N), -3.0, dtype=torch.bfloat16, device="cuda")
+        lay(x, torch.tensor(offs, dtype=torch.int32, device="cuda"), y=buf[40:40 + M])
+        assert (buf[:40] == -3.0).all() and (buf[40 + M:] == -3.0).all()
+
+
 @pytest.mark.parametrize("M", [1, 8, 16])
 def test_layer_of_few_rows_over_its_input(M):
     note(f"Fp8Linear in place {M}")
