@@ -60,8 +60,9 @@ _SIGS = {
     "svdq_quantize_weight_fp8": [_P, _I64, _I64, _I64, _P, _P, _P],
     "svdq_gemm_fp8": [_P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _I64, _P],
     "svdq_gemm_fp8_grouped": [_P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _P, _I32, _I64, _P],
-    "svdq_linear_fp8": [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _I64, _P],
-    "svdq_linear_fp8_grouped": [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _P, _I32, _I64, _P],
+    "svdq_linear_fp8_workspace_size": [_I64, _I64, _P],
+    "svdq_linear_fp8": [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _I64, _P, _I64, _P],
+    "svdq_linear_fp8_grouped": [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _P, _I32, _I64, _P, _I64, _P],
     "svdq_rope_axes": [_P, _P, _I64, _I32, _I32, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P],
 }
 
@@ -322,15 +323,22 @@ def svdq_gemm_fp8_grouped(qx, sx, M, K, qw, sw, N, offsets, groups, bias, act, y
            "svdq_gemm_fp8_grouped")
 
 
-def svdq_linear_fp8(x, M, K, ldx, qw, sw, N, bias, act, y, y_dtype, ldy, stream=None):
+def svdq_linear_fp8_workspace_size(M, K) -> int:
+    out = ctypes.c_int64(0)
+    _check(load_library().svdq_linear_fp8_workspace_size(M, K, ctypes.byref(out)), "svdq_linear_fp8_workspace_size")
+    return out.value
+
+
+def svdq_linear_fp8(x, M, K, ldx, qw, sw, N, bias, act, y, y_dtype, ldy, workspace=None, workspace_bytes=0, stream=None):
     _check(load_library().svdq_linear_fp8(_ptr(x), M, K, ldx, _ptr(qw), _ptr(sw), N, _ptr(bias), act, _ptr(y), y_dtype,
-                                          ldy, _stream(stream)), "svdq_linear_fp8")
+                                          ldy, _ptr(workspace), workspace_bytes, _stream(stream)), "svdq_linear_fp8")
 
 
-def svdq_linear_fp8_grouped(x, M, K, ldx, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, stream=None):
+def svdq_linear_fp8_grouped(x, M, K, ldx, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, workspace=None,
+                            workspace_bytes=0, stream=None):
     _check(load_library().svdq_linear_fp8_grouped(_ptr(x), M, K, ldx, _ptr(qw), _ptr(sw), N, _ptr(offsets), groups,
-                                                  _ptr(bias), act, _ptr(y), y_dtype, ldy, _stream(stream)),
-           "svdq_linear_fp8_grouped")
+                                                  _ptr(bias), act, _ptr(y), y_dtype, ldy, _ptr(workspace),
+                                                  workspace_bytes, _stream(stream)), "svdq_linear_fp8_grouped")
 
 
 def svdq_rope_axes(q, k, T, D, dtype, pos, pos_dtype, axes, turns, axis, pairs, pairing, inverse, eps, stream=None):

@@ -787,18 +787,28 @@ svdq_status gemm_fp8_impl(const void* qx, const float* sx, int64_t M, int64_t K,
                     what);
 }
 
+// bytes of a layer's workspace: the codes and scales between its two launches
+int64_t linear_fp8_workspace(int64_t M, int64_t K) {
+    const int64_t KB = (K + 127) / 128;
+    return M <= 16 && M * KB <= 256 ? 0 : M * K + 4 * KB * M;
+}
+
+svdq_status check_linear_fp8_mk(int64_t M, int64_t K) {
+    svdq_status s;
+    if (M < 0 || M >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "M = %lld must be in [0, 2^31)", (long long)M);
+    if ((s = check_k_fp8(K)) != SVDQ_OK) return s;
+    // the activation pass: one row and four blocks a wave at the least, 2^32 lanes a launch
+    if ((M / 4 + 1) * ((K + 511) / 512) >= ((int64_t)1 << 25))
+        return fail(SVDQ_ERR_SHAPE, "M = %lld x K = %lld needs more waves than one launch holds", (long long)M, (long long)K);
+    return SVDQ_OK;
+}
+
 svdq_status linear_fp8_impl(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
                             int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act, void* y,
-                            int32_t y_dtype, int64_t ldy, void* stream, const char* what) {
+                            int32_t y_dtype, int64_t ldy, void* ws, int64_t ws_bytes, void* stream, const char* what) {
     svdq_status s;
-    if (M < 0 || M > 16) return fail(SVDQ_ERR_SHAPE, "M = %lld must be in [0, 16]", (long long)M);
-    if ((s = check_k_fp8(K)) != SVDQ_OK) return s;
-    if (M * ((K + 127) / 128) > 256)
-        return fail(SVDQ_ERR_SHAPE, "M = %lld times the %lld blocks of K must not pass 256", (long long)M, (long long)((K + 127) / 128));
-    if (N <= 0 || N >= (int64_t)1 << 26) return fail(SVDQ_ERR_SHAPE, "N = %lld must be in [1, 2^26)", (long long)N);
-    // a row tile a row at the most, 512 lanes a workgroup
-    if (groups && M * ((N + 15) / 16) >= ((int64_t)1 << 23))
-        return fail(SVDQ_ERR_SHAPE, "M = %lld x N = %lld needs more tiles than one launch holds", (long long)M, (long long)N);
+    if ((s = check_linear_fp8_mk(M, K)) != SVDQ_OK) return s;
+    if (N <= 0 || N >= (int64_t)1 << 23) return fail(SVDQ_ERR_SHAPE, "N = %lld must be in [1, 2^23)", (long long)N);
     if (groups < 0 || groups > 65536) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
     if (ldx < K) return fail(SVDQ_ERR_SHAPE, "ldx = %lld < K = %lld", (long long)ldx, (long long)K);
     if (ldx % 8) return fail(SVDQ_ERR_ALIGN, "ldx = %lld must be a multiple of 8", (long long)ldx);
@@ -807,17 +817,31 @@ svdq_status linear_fp8_impl(const void* x, int64_t M, int64_t K, int64_t ldx, co
     if ((s = check_act(act)) != SVDQ_OK) return s;
     if (y_dtype != SVDQ_DT_BF16 && y_dtype != SVDQ_DT_F32)
         return fail(SVDQ_ERR_UNSUPPORTED, "output dtype %d is not supported", y_dtype);
+    const int64_t need = linear_fp8_workspace(M, K);
+    // few rows: up to a tile of 16 outputs per row, 512 lanes each
+    if (!gemm_fp8_fits(M, N, groups) || (!need && groups && M * ((N + 15) / 16) >= (int64_t)1 << 23))
+        return fail(SVDQ_ERR_SHAPE, "M = %lld x N = %lld needs more tiles than one launch holds", (long long)M, (long long)N);
+    if (ws_bytes < need)
+        return fail(SVDQ_ERR_SHAPE, "workspace of %lld bytes, %lld are needed", (long long)ws_bytes, (long long)need);
     if (M == 0) { g_last_error.clear(); return SVDQ_OK; }
-    if (!x || !qw || !sw || !y || (groups && !offsets))
-        return fail(SVDQ_ERR_NULL, "x, qw, sw and y%s are required", groups ? ", offsets" : "");
+    if (!x || !qw || !sw || !y || (groups && !offsets) || (need && !ws))
+        return fail(SVDQ_ERR_NULL, "x, qw, sw and y%s%s are required", groups ? ", offsets" : "", need ? ", workspace" : "");
     if (!aligned(x, 16) || !aligned(qw, 16) || !aligned(sw, 4) || (bias && !aligned(bias, 2)) ||
-        !aligned(y, y_dtype == SVDQ_DT_F32 ? 4 : 2) || (offsets && !aligned(offsets, 4)))
-        return fail(SVDQ_ERR_ALIGN, "x, qw need 16-byte alignment, sw, offsets 4, bias 2, y its element's");
+        !aligned(y, y_dtype == SVDQ_DT_F32 ? 4 : 2) || (offsets && !aligned(offsets, 4)) || (need && !aligned(ws, 16)))
+        return fail(SVDQ_ERR_ALIGN, "x, qw, workspace need 16-byte alignment, sw, offsets 4, bias 2, y its element's");
     int cus = 0;
     if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
-    return launched(launch_linear_fp8((const uint16_t*)x, M, K, ldx, (const uint8_t*)qw, sw, N, offsets, groups,
-                                      (const uint16_t*)bias, act, y, y_dtype == SVDQ_DT_F32, ldy, cus,
-                                      (hipStream_t)stream),
+    if (!need)
+        return launched(launch_linear_fp8((const uint16_t*)x, M, K, ldx, (const uint8_t*)qw, sw, N, offsets, groups,
+                                          (const uint16_t*)bias, act, y, y_dtype == SVDQ_DT_F32, ldy, cus,
+                                          (hipStream_t)stream),
+                        what);
+    uint8_t* qx = (uint8_t*)ws;
+    float* sx = (float*)(qx + M * K);                    // (K is a multiple of 16)
+    if ((s = launched(launch_quant_act_fp8((const uint16_t*)x, M, K, ldx, qx, sx, cus, (hipStream_t)stream), what)) != SVDQ_OK)
+        return s;
+    return launched(launch_gemm_fp8(qx, sx, M, K, (const uint8_t*)qw, sw, N, offsets, groups, (const uint16_t*)bias, act,
+                                    y, y_dtype == SVDQ_DT_F32, ldy, cus, (hipStream_t)stream),
                     what);
 }
 
@@ -897,19 +921,29 @@ svdq_status svdq_gemm_fp8_grouped(const void* qx, const float* sx, int64_t M, in
                          "svdq_gemm_fp8_grouped launch");
 }
 
+svdq_status svdq_linear_fp8_workspace_size(int64_t M, int64_t K, int64_t* bytes) {
+    svdq_status s;
+    if ((s = check_linear_fp8_mk(M, K)) != SVDQ_OK) return s;
+    if (!bytes) return fail(SVDQ_ERR_NULL, "bytes is required");
+    *bytes = linear_fp8_workspace(M, K);
+    g_last_error.clear();
+    return SVDQ_OK;
+}
+
 svdq_status svdq_linear_fp8(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
                             int64_t N, const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
-                            void* stream) {
-    return linear_fp8_impl(x, M, K, ldx, qw, sw, N, nullptr, 0, bias, act, y, y_dtype, ldy, stream,
-                           "svdq_linear_fp8 launch");
+                            void* workspace, int64_t workspace_bytes, void* stream) {
+    return linear_fp8_impl(x, M, K, ldx, qw, sw, N, nullptr, 0, bias, act, y, y_dtype, ldy, workspace, workspace_bytes,
+                           stream, "svdq_linear_fp8 launch");
 }
 
 svdq_status svdq_linear_fp8_grouped(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
                                     int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act,
-                                    void* y, int32_t y_dtype, int64_t ldy, void* stream) {
+                                    void* y, int32_t y_dtype, int64_t ldy, void* workspace, int64_t workspace_bytes,
+                                    void* stream) {
     if (groups < 1) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
-    return linear_fp8_impl(x, M, K, ldx, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, stream,
-                           "svdq_linear_fp8_grouped launch");
+    return linear_fp8_impl(x, M, K, ldx, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, workspace,
+                           workspace_bytes, stream, "svdq_linear_fp8_grouped launch");
 }
 
 svdq_status svdq_rope_axes(const svdq_rope_heads* q, const svdq_rope_heads* k, int64_t T, int32_t D, int32_t dtype,

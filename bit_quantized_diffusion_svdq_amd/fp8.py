@@ -162,28 +162,31 @@ def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", ou
     return y
 
 
-# what svdq_linear_fp8 and its grouped form take: rows, and rows x blocks of 128 channels
-_FEW_ROWS, _FEW_BLOCKS = 16, 256
+def _workspace_bytes(M, K) -> int:
+    """svdq_linear_fp8_workspace_size, without the call."""
+    kb = blocks(K)
+    return 0 if M <= 16 and M * kb <= 256 else M * K + 4 * kb * M
 
 
-def _linear_few(x, qw, sw, bias, act, out_dtype, y, offsets=None):
-    """The layer of few rows in one launch, or None for a call that has more
-    or that is not the usual one (the two passes then say what is wrong)."""
+def _layer(x, qw, sw, bias, act, out_dtype, y, offsets=None):
+    """The layer in one call, or None for a call that is not the usual one
+    (the two passes then do it, or say what is wrong)."""
     M, K = x.shape
     kb = blocks(K)
     dev = x.device
     lead = () if offsets is None else (offsets.numel() - 1,)
-    if not (0 < M <= _FEW_ROWS and M * kb <= _FEW_BLOCKS and x.is_cuda and x.dtype is _BF16 and K >= 16 and K % 16 == 0
+    if not (M > 0 and x.is_cuda and x.dtype is _BF16 and K >= 16 and K % 16 == 0
             and x.stride(1) == 1 and qw.dtype is E4M3 and sw.dtype is _F32 and qw.device == dev and sw.device == dev
             and qw.dim() == 2 + len(lead) and qw.is_contiguous() and sw.is_contiguous() and act in _lib.ACT):
         return None
     N = qw.shape[-2]
-    ldx = x.stride(0) if M > 1 else K
-    if not (N >= 1 and M * N <= 1 << 26 and qw.shape == (*lead, N, K) and sw.shape == (*lead, blocks(N), kb)
+    if not (1 <= N < 1 << 22 and qw.shape == (*lead, N, K) and sw.shape == (*lead, blocks(N), kb)
             and (bias is None or (bias.dtype is _BF16 and bias.shape == (*lead, N) and bias.is_contiguous()
                                   and bias.device == dev))
             and (offsets is None or offsets.device == dev)):
         return None
+    need = _workspace_bytes(M, K)
+    ldx = x.stride(0) if M > 1 else K
     if y is None:
         if not (out_dtype is _BF16 or out_dtype is _F32):
             return None
@@ -193,15 +196,16 @@ def _linear_few(x, qw, sw, bias, act, out_dtype, y, offsets=None):
         if not (y.shape == (M, N) and (y.dtype is _BF16 or y.dtype is _F32) and y.device == dev
                 and (y.stride(1) == 1 or N == 1) and ldy >= N):
             return None
-        if y.untyped_storage().data_ptr() == x.untyped_storage().data_ptr():
+        if not need and y.untyped_storage().data_ptr() == x.untyped_storage().data_ptr():
             x, ldx = x.clone(memory_format=torch.contiguous_format), K   # in place: y is written while x is read
     if ldx < K or ldx % 8:                      # a broadcast or unaligned row stride
         x, ldx = x.contiguous(), K
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
     f32 = int(y.dtype is _F32)
     if offsets is None:
-        _lib.svdq_linear_fp8(x, M, K, ldx, qw, sw, N, bias, _lib.ACT[act], y, f32, ldy)
+        _lib.svdq_linear_fp8(x, M, K, ldx, qw, sw, N, bias, _lib.ACT[act], y, f32, ldy, ws, need)
     else:
-        _lib.svdq_linear_fp8_grouped(x, M, K, ldx, qw, sw, N, offsets, lead[0], bias, _lib.ACT[act], y, f32, ldy)
+        _lib.svdq_linear_fp8_grouped(x, M, K, ldx, qw, sw, N, offsets, lead[0], bias, _lib.ACT[act], y, f32, ldy, ws, need)
     return y
 
 
@@ -228,12 +232,13 @@ class Fp8Linear:
     def __call__(self, x: torch.Tensor, act: str = "none", out_dtype=torch.bfloat16, y=None,
                  stream=None) -> torch.Tensor:
         """Y [M, N] for bf16 activations x [M, K]: the activation pass, then
-        the product, on one stream; in one launch for few rows (M <= 16 and
-        M * ceil(K / 128) <= 256: single tokens, pooled conditioning)."""
+        the product, in one call on one stream; in one launch for few rows (M
+        <= 16 and M * ceil(K / 128) <= 256: single tokens, pooled
+        conditioning)."""
         if x.dim() != 2 or x.shape[1] != self.K:
             raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
         with _on(x, stream):                     # (the codes are freed on the stream that reads them)
-            out = _linear_few(x, self.qw, self.sw, self.bias, act, out_dtype, y)
+            out = _layer(x, self.qw, self.sw, self.bias, act, out_dtype, y)
             if out is not None:
                 return out
             qx, sx = quantize_act_fp8(x)
@@ -267,14 +272,14 @@ class Fp8GroupedLinear:
     def __call__(self, x: torch.Tensor, offsets: torch.Tensor, act: str = "none", out_dtype=torch.bfloat16, y=None,
                  stream=None) -> torch.Tensor:
         """Y [M, N] for bf16 activations x [M, K] sorted by group
-        (fp8_grouped_linear's offsets); in one launch for few rows, as
-        Fp8Linear."""
+        (fp8_grouped_linear's offsets); one call, and one launch for few
+        rows, as Fp8Linear."""
         if x.dim() != 2 or x.shape[1] != self.K:
             raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
         if _groups(offsets) != self.groups:
             raise ValueError(f"offsets must hold {self.groups + 1} values, got {offsets.numel()}")
         with _on(x, stream):
-            out = _linear_few(x, self.qw, self.sw, self.bias, act, out_dtype, y, offsets)
+            out = _layer(x, self.qw, self.sw, self.bias, act, out_dtype, y, offsets)
             if out is not None:
                 return out
             qx, sx = quantize_act_fp8(x)

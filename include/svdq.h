@@ -556,17 +556,19 @@ svdq_status svdq_quantize_weight_fp8(const void* w, int64_t K, int64_t N, int64_
  *   above for all M rows. Rows of y before offsets[0] and from
  *   offsets[groups] on are not written. groups in [1, 65536], M < 2^31.
  *
- * svdq_linear_fp8 -- the layer of few rows in one launch: x bf16 [M][ldx] as
- *   svdq_quantize_act_fp8 takes it, turned into the codes and scales that it
- *   gives, and their product as above. M <= 16, M * ceil(K/128) <= 256,
- *   N < 2^26. Equal to the two calls but for the order in which a row's
- *   blocks are summed in fp32. y must not overlap x (workgroups write it
- *   while others read x). M == 0 is valid.
+ * svdq_linear_fp8 -- the layer: x bf16 [M][ldx] as svdq_quantize_act_fp8 takes
+ *   it, turned into the codes and scales that it gives, and their product as
+ *   above, N < 2^23. Few rows (M <= 16 and M * ceil(K/128) <= 256) take one
+ *   launch, equal to the two calls but for the order in which a row's blocks
+ *   are summed in fp32; y must not overlap x then (workgroups write it while
+ *   others read x). More take two, with the codes and scales in the
+ *   caller's workspace (16-byte aligned, M * K + 4 * ceil(K/128) * M bytes;
+ *   svdq_linear_fp8_workspace_size gives 0 for few rows, which need none).
+ *   M == 0 is valid.
  *
  * svdq_linear_fp8_grouped -- the same with a weight per group of rows
- *   (svdq_gemm_fp8_grouped's offsets, arrays and untouched rows): the few
- *   tokens of a step on their experts. Limits as above, over all M rows;
- *   M * ceil(N/16) < 2^23.
+ *   (svdq_gemm_fp8_grouped's offsets, arrays and untouched rows; the few
+ *   tokens of a step on their experts take one launch).
  */
 svdq_status svdq_gemm_fp8(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
                           int64_t N, const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
@@ -575,12 +577,14 @@ svdq_status svdq_gemm_fp8_grouped(const void* qx, const float* sx, int64_t M, in
                                   const float* sw, int64_t N, const int32_t* offsets, int32_t groups,
                                   const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
                                   void* stream);
+svdq_status svdq_linear_fp8_workspace_size(int64_t M, int64_t K, int64_t* bytes);
 svdq_status svdq_linear_fp8(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
                             int64_t N, const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
-                            void* stream);
+                            void* workspace, int64_t workspace_bytes, void* stream);
 svdq_status svdq_linear_fp8_grouped(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
                                     int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act,
-                                    void* y, int32_t y_dtype, int64_t ldy, void* stream);
+                                    void* y, int32_t y_dtype, int64_t ldy, void* workspace, int64_t workspace_bytes,
+                                    void* stream);
 
 /* ------------------------------------------------------------------------
  * svdq_rope_axes -- rotary positions with several axes (time, height, width

@@ -97,16 +97,18 @@ def test_well_formed_calls_reach_the_device_check(lib):
 
 
 def _few(lib, **kw):
-    a = dict(x=A, M=16, K=2048, ldx=2048, qw=C, sw=D, N=77, bias=None, act=0, y=F, ydt=0, ldy=77)
+    a = dict(x=A, M=16, K=2048, ldx=2048, qw=C, sw=D, N=77, bias=None, act=0, y=F, ydt=0, ldy=77, ws=None, wsb=0)
     a.update(kw)
     return lib.svdq_linear_fp8(a["x"], a["M"], a["K"], a["ldx"], a["qw"], a["sw"], a["N"], a["bias"], a["act"], a["y"],
-                               a["ydt"], a["ldy"], None)
+                               a["ydt"], a["ldy"], a["ws"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(M=-1), SHAPE), (dict(M=17, K=128), SHAPE), (dict(K=2064, ldx=2064), SHAPE), (dict(M=1, K=32784, ldx=32784), SHAPE),
+    (dict(M=17, wsb=17 * 2048 + 17 * 64 - 1, ws=B), SHAPE), (dict(M=17, wsb=17 * 2048 + 17 * 64), NULL),
+    (dict(M=17, wsb=1 << 20, ws=B + 8), ALIGN), (dict(M=1 << 31), SHAPE), (dict(M=1 << 30, K=1 << 16, ldx=1 << 16), SHAPE),
     (dict(K=40), SHAPE), (dict(K=0), SHAPE), (dict(K=1 << 22), SHAPE), (dict(N=0), SHAPE),
-    (dict(N=1 << 26, ldy=1 << 26), SHAPE), (dict(ldx=2032), SHAPE), (dict(ldx=2052), ALIGN), (dict(ldy=76), SHAPE),
+    (dict(N=1 << 23, ldy=1 << 23), SHAPE), (dict(ldx=2032), SHAPE), (dict(ldx=2052), ALIGN), (dict(ldy=76), SHAPE),
     (dict(ldy=1 << 31), SHAPE), (dict(act=2), UNSUP), (dict(ydt=2), UNSUP), (dict(x=None), NULL), (dict(qw=None), NULL),
     (dict(sw=None), NULL), (dict(y=None), NULL), (dict(x=A + 8), ALIGN), (dict(qw=C + 4), ALIGN), (dict(sw=D + 2), ALIGN),
     (dict(bias=E + 1), ALIGN), (dict(y=F + 1), ALIGN), (dict(y=F + 2, ydt=1), ALIGN), (dict(M=0, x=None), OK),
@@ -117,14 +119,15 @@ def test_layer_of_few_rows_rejects(lib, kw, status):
 
 
 def _few_grouped(lib, **kw):
-    a = dict(x=A, M=16, K=2048, ldx=2048, qw=C, sw=D, N=77, offs=E, groups=5, bias=None, act=0, y=F, ydt=0, ldy=77)
+    a = dict(x=A, M=16, K=2048, ldx=2048, qw=C, sw=D, N=77, offs=E, groups=5, bias=None, act=0, y=F, ydt=0, ldy=77, ws=None,
+             wsb=0)
     a.update(kw)
     return lib.svdq_linear_fp8_grouped(a["x"], a["M"], a["K"], a["ldx"], a["qw"], a["sw"], a["N"], a["offs"], a["groups"],
-                                       a["bias"], a["act"], a["y"], a["ydt"], a["ldy"], None)
+                                       a["bias"], a["act"], a["y"], a["ydt"], a["ldy"], a["ws"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(M=17, K=128), SHAPE), (dict(K=2064, ldx=2064), SHAPE), (dict(groups=0), SHAPE), (dict(groups=-1), SHAPE),
+    (dict(M=17, K=128), SHAPE), (dict(N=(1 << 23) - 8, ldy=1 << 23), SHAPE), (dict(M=17, wsb=1 << 20), NULL), (dict(K=2064, ldx=2064), SHAPE), (dict(groups=0), SHAPE), (dict(groups=-1), SHAPE),
     (dict(groups=65537), SHAPE), (dict(N=1 << 23, ldy=1 << 23), SHAPE), (dict(offs=None), NULL), (dict(offs=E + 2), ALIGN),
     (dict(x=None), NULL), (dict(ldx=2052), ALIGN), (dict(y=F + 1), ALIGN), (dict(act=2), UNSUP), (dict(M=0, offs=None), OK),
 ])
@@ -136,7 +139,20 @@ def test_grouped_layer_of_few_rows_rejects(lib, kw, status):
 def test_layer_of_few_rows_limits(lib):
     valid(_few_grouped(lib))
     valid(_few(lib))
-    valid(_few(lib, M=1, K=32768, ldx=1 << 40, bias=E, N=(1 << 26) - 1, ldy=1 << 26))
+    valid(_few(lib, M=1, K=32768, ldx=1 << 40, bias=E, N=(1 << 23) - 1, ldy=1 << 23))
+    valid(_few(lib, M=17, ws=B, wsb=17 * 2048 + 17 * 64))
+    valid(_few_grouped(lib, M=4000, ws=B, wsb=4000 * 2048 + 4000 * 64))
+
+
+def test_layer_workspace(lib):
+    from bit_quantized_diffusion_svdq_amd.fp8 import _workspace_bytes
+    for M, K in ((0, 16), (1, 16), (1, 32768), (1, 32784), (16, 2048), (16, 2064), (17, 16), (4608, 12288)):
+        assert svdq.svdq_linear_fp8_workspace_size(M, K) == _workspace_bytes(M, K)
+    assert _workspace_bytes(16, 2048) == 0 and _workspace_bytes(17, 144) == 17 * 144 + 17 * 8
+    for M, K in ((-1, 16), (1, 24), (1 << 31, 16)):
+        with pytest.raises(svdq.SvdqError):
+            svdq.svdq_linear_fp8_workspace_size(M, K)
+    assert lib.svdq_linear_fp8_workspace_size(1, 16, None) == NULL
 
 
 def _heads(**kw):
@@ -311,7 +327,7 @@ def test_grouped_layer_refuses(M, kw, text):
 
 def test_names_are_public():
     names = ("svdq_quantize_act_fp8", "svdq_quantize_weight_fp8", "svdq_gemm_fp8", "svdq_gemm_fp8_grouped",
-             "svdq_linear_fp8", "svdq_linear_fp8_grouped", "svdq_rope_axes", "Fp8Linear", "Fp8GroupedLinear", "fp8_linear", "fp8_grouped_linear",
+             "svdq_linear_fp8", "svdq_linear_fp8_grouped", "svdq_linear_fp8_workspace_size", "svdq_rope_axes", "Fp8Linear", "Fp8GroupedLinear", "fp8_linear", "fp8_grouped_linear",
              "quantize_act_fp8", "quantize_fp8", "RopePlan", "rope_axes", "FusedQKV", "save_fp8_layer", "load_fp8_layer")
     assert all(n in svdq.__all__ and hasattr(svdq, n) for n in names)
 
