@@ -21,7 +21,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import _check_rows, _check_same_device, _require
+from ._lib import _check, _check_rows, _check_same_device, _require, load_library
 
 BLOCK = 128
 E4M3 = torch.float8_e4m3fn
@@ -43,6 +43,16 @@ def _on(t: torch.Tensor, stream=None):
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
     return torch.cuda.stream(stream)
+
+
+def _stream_now() -> int:
+    """The current stream's handle (small calls are bound by Python: these
+    entry points marshal by hand what _lib's functions take apart)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 _HERE = contextlib.nullcontext()
@@ -67,7 +77,8 @@ def quantize_act_fp8(x: torch.Tensor, stream=None):
             x, ldx = x.contiguous(), K
         # (x.new_empty costs half a us less than torch.empty)
         qx, sx = x.new_empty(M, K, dtype=E4M3), x.new_empty(blocks(K), M, dtype=_F32)
-        _lib.svdq_quantize_act_fp8(x, M, K, ldx, qx, sx)
+        _check(load_library().svdq_quantize_act_fp8(x.data_ptr(), M, K, ldx, qx.data_ptr(), sx.data_ptr(), _stream_now()),
+               "svdq_quantize_act_fp8")
     return qx, sx
 
 
@@ -133,7 +144,9 @@ def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfl
     M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, 0)
     with _on(qx, stream):
         y, ldy = _output(y, M, N, out_dtype, qx)
-        _lib.svdq_gemm_fp8(qx, sx, M, K, qw, sw, N, bias, _lib.ACT[act], y, int(out_dtype is _F32), ldy)
+        _check(load_library().svdq_gemm_fp8(qx.data_ptr(), sx.data_ptr(), M, K, qw.data_ptr(), sw.data_ptr(), N,
+                                            _address(bias), _lib.ACT[act], y.data_ptr(), out_dtype is _F32, ldy,
+                                            _stream_now()), "svdq_gemm_fp8")
     return y
 
 
@@ -157,8 +170,10 @@ def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", ou
         raise ValueError(f"offsets is on {offsets.device}, expected {qx.device}")
     with _on(qx, stream):
         y, ldy = _output(y, M, N, out_dtype, qx)
-        _lib.svdq_gemm_fp8_grouped(qx, sx, M, K, qw, sw, N, offsets, groups, bias, _lib.ACT[act], y,
-                                   int(out_dtype is _F32), ldy)
+        _check(load_library().svdq_gemm_fp8_grouped(qx.data_ptr(), sx.data_ptr(), M, K, qw.data_ptr(), sw.data_ptr(), N,
+                                                    offsets.data_ptr(), groups, _address(bias), _lib.ACT[act],
+                                                    y.data_ptr(), out_dtype is _F32, ldy, _stream_now()),
+               "svdq_gemm_fp8_grouped")
     return y
 
 
@@ -201,11 +216,16 @@ def _layer(x, qw, sw, bias, act, out_dtype, y, offsets=None):
     if ldx < K or ldx % 8:                      # a broadcast or unaligned row stride
         x, ldx = x.contiguous(), K
     ws = x.new_empty(need, dtype=torch.uint8) if need else None
-    f32 = int(y.dtype is _F32)
+    f32 = y.dtype is _F32
     if offsets is None:
-        _lib.svdq_linear_fp8(x, M, K, ldx, qw, sw, N, bias, _lib.ACT[act], y, f32, ldy, ws, need)
+        _check(load_library().svdq_linear_fp8(x.data_ptr(), M, K, ldx, qw.data_ptr(), sw.data_ptr(), N, _address(bias),
+                                              _lib.ACT[act], y.data_ptr(), f32, ldy, _address(ws), need, _stream_now()),
+               "svdq_linear_fp8")
     else:
-        _lib.svdq_linear_fp8_grouped(x, M, K, ldx, qw, sw, N, offsets, lead[0], bias, _lib.ACT[act], y, f32, ldy, ws, need)
+        _check(load_library().svdq_linear_fp8_grouped(x.data_ptr(), M, K, ldx, qw.data_ptr(), sw.data_ptr(), N,
+                                                      offsets.data_ptr(), lead[0], _address(bias), _lib.ACT[act],
+                                                      y.data_ptr(), f32, ldy, _address(ws), need, _stream_now()),
+               "svdq_linear_fp8_grouped")
     return y
 
 

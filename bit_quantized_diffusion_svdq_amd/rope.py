@@ -11,14 +11,14 @@ Marshalling only: the arithmetic is the library's.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 from typing import Sequence
 
 import torch
 
-from . import _lib
-from ._lib import RopeHeads, _require
-from .fp8 import _on
+from ._lib import RopeHeads, _check, _require, load_library
+from .fp8 import _on, _stream_now
 
 PAIRING = {"interleaved": 0, "half": 1}
 
@@ -64,6 +64,19 @@ def _heads(x, name, D):
         raise ValueError(f"{name} must have contiguous heads (stride(2) == 1)")
 
 
+def _check_side(name, x, norm, out, D, dt, dev):
+    if norm is not None and not (norm.dtype is dt and norm.shape == (D,) and norm.is_contiguous()):
+        raise ValueError(f"{name}_norm must be a contiguous {dt} vector of {D} values")
+    if out is not None:
+        _heads(out, f"{name}_out", D)
+        if out.shape != x.shape or out.dtype is not dt:
+            raise ValueError(f"{name}_out must be {tuple(x.shape)} {dt}")
+    if dev.type == "cuda":
+        for t in (norm, out):
+            if t is not None and t.device != dev:
+                raise ValueError(f"{name}_norm or {name}_out is on {t.device}, expected {dev}")
+
+
 def _strides(x, T, H, D):
     """Token and head stride; an axis of one element has none of its own."""
     ts, hs, _ = x.stride()
@@ -103,26 +116,24 @@ def rope_axes(q, k, pos, plan: RopePlan, q_norm=None, k_norm=None, eps: float = 
             raise ValueError(f"k must have {T} tokens of {dt}, got {tuple(k.shape)} {k.dtype}")
     elif k_norm is not None or k_out is not None:
         raise ValueError("k_norm and k_out need k")
-    for name, x, norm, out in (("q", q, q_norm, q_out), ("k", k, k_norm, k_out)):
-        if norm is not None and not (norm.dtype is dt and norm.shape == (D,) and norm.is_contiguous()):
-            raise ValueError(f"{name}_norm must be a contiguous {dt} vector of {D} values")
-        if out is not None:
-            _heads(out, f"{name}_out", D)
-            if out.shape != x.shape or out.dtype is not dt:
-                raise ValueError(f"{name}_out must be {tuple(x.shape)} {dt}")
+    if q_norm is not None or q_out is not None:
+        _check_side("q", q, q_norm, q_out, D, dt, dev)
+    if k_norm is not None or k_out is not None:
+        _check_side("k", k, k_norm, k_out, D, dt, dev)
     f32_pos = pos.dtype is torch.float32
     if not ((f32_pos or pos.dtype is torch.int32) and pos.shape == (T, plan.axes) and pos.is_contiguous()):
         raise ValueError(f"pos must be contiguous int32 or fp32 [{T}, {plan.axes}], got {tuple(pos.shape)} {pos.dtype}")
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a GPU device, got {dev}")
-    for t in (k, pos, q_norm, k_norm, q_out, k_out, plan.turns):
-        if t is not None and t.device != dev:
-            raise ValueError(f"a tensor or the plan is on {t.device}, expected {dev}")
+    if pos.device != dev or plan.turns.device != dev or (k is not None and k.device != dev):
+        raise ValueError(f"k, pos or the plan is not on {dev}")
     with _on(q, stream):
         q_out, qs = _side(q, q_out, q_norm, T, hq, D)
         ks = None
         if k is not None:
             k_out, ks = _side(k, k_out, k_norm, T, hk, D)
-        _lib.svdq_rope_axes(qs, ks, T, D, int(dt is torch.float32), pos, int(f32_pos), plan.axes, plan.turns, plan.axis,
-                            plan.pairs, PAIRING[plan.pairing], int(inverse), eps)
+        _check(load_library().svdq_rope_axes(ctypes.addressof(qs), None if ks is None else ctypes.addressof(ks), T, D,
+                                             dt is torch.float32, pos.data_ptr(), f32_pos, plan.axes,
+                                             plan.turns.data_ptr(), plan.axis.data_ptr(), plan.pairs,
+                                             PAIRING[plan.pairing], bool(inverse), eps, _stream_now()), "svdq_rope_axes")
     return q_out if k is None else (q_out, k_out)
