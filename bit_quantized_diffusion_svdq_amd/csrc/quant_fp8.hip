@@ -5,16 +5,18 @@
 // The activation pass is bound by memory: 2 bytes in and 1 byte out per value
 // (plus 4 bytes per 128). A wave takes four blocks of a row at a time (16
 // lanes and 16 bytes per lane each: 1 KB contiguous) and walks `rpw`
-// consecutive rows with eight rows' loads in flight, so the scales of its
-// rows, which are stored block-major ([ceil(K / 128)][M]), leave as one
-// contiguous run per block instead of one 4-byte store per row. Maxima are
-// taken on the bf16 bits, two at a time, and across lanes without LDS; with
-// that 4608 x 12288 went from 37.4 to 34.6 us, 4.9 TB/s (a plain copy: 5.5).
+// consecutive rows two at a time, so the scales of its rows, which are stored
+// block-major ([ceil(K / 128)][M]), leave as one contiguous run per block.
+// Maxima are taken on the bf16 bits, two at a time, and across lanes without
+// LDS. 4608 x 12288 takes 29.5 us, 5.8 TB/s with what the last-level cache
+// keeps of the output (a plain copy: 5.5).
 #include "fp8.h"
 
 namespace {
 
-constexpr int UNROLL = 8;                               // rows in flight per wave
+// rows in flight per wave: few registers, many waves (with 8, 512 x 4096 took 4.2 us instead
+// of 3.6, 64 x 4096 2.9 instead of 2.5; with 1, 4608 x 4096 13.3 instead of 12.4)
+constexpr int UNROLL = 2;
 
 __global__ __launch_bounds__(256) void quant_act_fp8_kernel(const uint16_t* __restrict__ x, int64_t M, int K,
                                                             int64_t ldx, int rpw, uint8_t* __restrict__ qx,
@@ -45,7 +47,7 @@ __global__ __launch_bounds__(256) void quant_act_fp8_kernel(const uint16_t* __re
             if (r0 + u < rows) {
                 float s;
                 const uint2 o = block_codes(v[u], s);
-                if (((r0 + u) & 15) == l16) mine = s;
+                if (r0 + u == l16) mine = s;
                 if (in) *(uint2*)(qp + (int64_t)(r0 + u) * K) = o;
             }
         }
@@ -110,9 +112,11 @@ __global__ __launch_bounds__(256) void quant_weight_fp8_kernel(const uint16_t* _
 hipError_t launch_quant_act_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, uint8_t* qx, float* sx, int cus,
                                 hipStream_t stream) {
     const int64_t QB = (K + 511) / 512;
-    // 16 rows per wave once that leaves every SIMD two waves (4608 x 4096: 12.9 us); fewer rows
-    // fill the chip sooner (512 x 4096: 4.6 us with 4)
-    const int rpw = (M + 15) / 16 * QB >= (int64_t)cus * 8 ? 16 : (M + 3) / 4 * QB >= (int64_t)cus * 8 ? 4 : 1;
+    // few rows a wave fill the chip sooner, more make fewer and longer runs of scales (1, 2, 4,
+    // 8 rows: 512 x 4096 3.6, 3.8, 4.4, 5.9 us; 1024 x 4096 4.8, 4.6, 4.9, 6.3; 1024 x 12288
+    // 10.2, 9.7, 9.0, 9.7; 4608 x 4096 13.7, 12.8, 12.4, 12.0)
+    const int64_t waves = M * QB;
+    const int rpw = waves > (int64_t)cus * 48 ? 4 : waves > (int64_t)cus * 16 ? 2 : 1;
     const int64_t items = (M + rpw - 1) / rpw * QB;
     hipLaunchKernelGGL(quant_act_fp8_kernel, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, x, M, (int)K, ldx,
                        rpw, qx, sx);
