@@ -80,10 +80,10 @@ DEV void store8(void* p, int64_t at, int e0, int e1, const float* v) {
 }
 
 constexpr int kMaxPairs = 256;
-constexpr int U = 4;                     // loads of a wave in flight (16 bytes a lane each, bf16)
 
-// HALF 0: pairs are neighbours (2i, 2i + 1); 1: pair i is (i, i + pairs)
-template <int F32, int HALF>
+// HALF 0: pairs are neighbours (2i, 2i + 1); 1: pair i is (i, i + pairs). U:
+// loads of a wave in flight (16 bytes a lane each, bf16)
+template <int F32, int HALF, int U>
 __global__ __launch_bounds__(256) void rope_axes_kernel(RopeArgs a) {
     __shared__ float2 cs[4][kMaxPairs];
     const int lane = threadIdx.x & 63;
@@ -195,7 +195,8 @@ __global__ __launch_bounds__(256) void rope_axes_kernel(RopeArgs a) {
 
 }  // namespace
 
-hipError_t launch_rope_axes(RopeArgs a, int f32, int half, int cus, hipStream_t stream) {
+template <int U>
+static hipError_t launch(RopeArgs a, int f32, int half, int cus, hipStream_t stream) {
     a.lp = 1;
     while (a.lp * 8 < a.D) a.lp *= 2;
     const int per = 64 / a.lp, loads = (a.heads[0] + per - 1) / per + (a.heads[1] + per - 1) / per;
@@ -209,11 +210,18 @@ hipError_t launch_rope_axes(RopeArgs a, int f32, int half, int cus, hipStream_t 
     a.chunk = (int)((loads + chunks - 1) / chunks);
     const dim3 grid((unsigned)((a.T + 3) / 4), (unsigned)((loads + a.chunk - 1) / a.chunk)), block(256);
     if (f32) {
-        if (half) hipLaunchKernelGGL((rope_axes_kernel<1, 1>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((rope_axes_kernel<1, 0>), grid, block, 0, stream, a);
+        if (half) hipLaunchKernelGGL((rope_axes_kernel<1, 1, U>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((rope_axes_kernel<1, 0, U>), grid, block, 0, stream, a);
     } else {
-        if (half) hipLaunchKernelGGL((rope_axes_kernel<0, 1>), grid, block, 0, stream, a);
-        else hipLaunchKernelGGL((rope_axes_kernel<0, 0>), grid, block, 0, stream, a);
+        if (half) hipLaunchKernelGGL((rope_axes_kernel<0, 1, U>), grid, block, 0, stream, a);
+        else hipLaunchKernelGGL((rope_axes_kernel<0, 0, U>), grid, block, 0, stream, a);
     }
     return hipGetLastError();
+}
+
+hipError_t launch_rope_axes(RopeArgs a, int f32, int half, int cus, hipStream_t stream) {
+    // Few tokens: one load a wave at a time, more waves (24 + 24 heads of 128: 1 token 3.2 us, 4.4
+    // with four loads; 77 tokens 3.8, 5.6; 512 6.4, 7.1). More tokens: four loads in flight (1024
+    // tokens 8.8, 9.4 with one; 4608 of 32 + 8 heads, half-split 22.3, 25.3).
+    return a.T <= 2 * (int64_t)cus ? launch<1>(a, f32, half, cus, stream) : launch<4>(a, f32, half, cus, stream);
 }
