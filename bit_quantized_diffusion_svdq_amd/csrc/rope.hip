@@ -186,6 +186,16 @@ __global__ __launch_bounds__(256) void rope_axes_kernel(RopeArgs a) {
                 o[ex] = __builtin_fmaf(v[ex], m[i][0], -(v[ey] * m[i][1]));
                 o[ey] = __builtin_fmaf(v[ex], m[i][2], v[ey] * m[i][3]);
             }
+            // Channels past the pairs take their weight alone: as pairs with sine 0, an
+            // infinity or a NaN in one would spoil the other (heads that turn whole skip this)
+            if (2 * a.pairs < a.D && !turned) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int ex = HALF ? i : 2 * i, ey = HALF ? 4 + i : 2 * i + 1;
+                    o[ex] = v[ex] * m[i][0];
+                    o[ey] = v[ey] * m[i][3];
+                }
+            }
             const int h = h0 + k * per;
             if (in && h + slot < a.heads[side]) store8<F32, HALF>(a.y[side], at0 + h * hs, e0, e1, o);
         }
