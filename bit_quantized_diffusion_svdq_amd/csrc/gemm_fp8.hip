@@ -127,12 +127,15 @@ struct Rows {
 
 // Row tile `mt` of `bm` rows in the ragged groups, found by every wave on its
 // own: 64 groups at a time, their tile counts are summed along the lanes.
-// Offsets are clamped into [0, M] and to rising order, so bad ones cannot
-// lead outside the arrays. Returns the number of tiles in *total.
+// Offsets are clamped into [0, M], and one that falls counts as the largest
+// before it: bad offsets lead nowhere outside the arrays, no row belongs to
+// two groups (two workgroups would write it), and the tiles stay within the
+// launch's. Returns the number of tiles in *total.
 DEV Rows group_rows(const Args& a, int mt, int bm, int* total) {
     const int lane = threadIdx.x & 63;
     Rows r{0, 0, 0};
     int before = 0;
+    int done = 0;                                        // the largest offset so far (M < 2^31)
     for (int g0 = 0; g0 < a.E; g0 += 64) {
         const int g = g0 + lane;
         int64_t lo = 0, hi = 0;
@@ -140,8 +143,20 @@ DEV Rows group_rows(const Args& a, int mt, int bm, int* total) {
             lo = a.offs[g];
             hi = a.offs[g + 1];
             lo = lo < 0 ? 0 : lo > a.M ? a.M : lo;
-            hi = hi < lo ? lo : hi > a.M ? a.M : hi;
+            hi = hi < 0 ? 0 : hi > a.M ? a.M : hi;
         }
+        if (__builtin_amdgcn_readfirstlane((int)lo) < done || __ballot(hi < lo)) {
+            // somewhere they fall: each becomes the largest up to it (never with good offsets)
+            int top = (int)lo > done ? (int)lo : done;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int o = __shfl_up(top, d);
+                if (lane >= d && o > top) top = o;
+            }
+            lo = top;
+            hi = hi < lo ? lo : hi;
+        }
+        done = __builtin_amdgcn_readlane((int)hi, 63);   // (nobody asks after the last 64)
         const int cnt = (int)((hi - lo + bm - 1) / bm);
         int inc = cnt;
 #pragma unroll

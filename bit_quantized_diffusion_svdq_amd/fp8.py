@@ -161,7 +161,9 @@ def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", ou
                        stream=None):
     """fp8_linear with a weight per group: rows offsets[g] .. offsets[g + 1] - 1
     of qx meet qw[g] [N, K], sw[g], bias[g]. offsets: int32 [groups + 1] on
-    the GPU, rising, within [0, M] (read there: no synchronisation). Rows of
+    the GPU, rising, within [0, M] (read there: no synchronisation, so bad
+    values are not reported: they are clamped, and one that falls counts as
+    the largest before it). Rows of
     no group (before offsets[0], from offsets[-1] on) are left as they are in
     a given y and are unspecified in a new one."""
     groups = _groups(offsets)

@@ -550,8 +550,9 @@ svdq_status svdq_quantize_weight_fp8(const void* w, int64_t K, int64_t N, int64_
  *   offsets[g + 1] - 1 of qx meet weight g (the experts of a
  *   mixture, or the text and image streams of a joint block). offsets is a
  *   DEVICE array int32 [groups + 1], rising, within [0, M] (read by the
- *   kernel; values outside are clamped, so they cannot lead outside the
- *   arrays); groups may be empty. qw [groups][N][K], sw
+ *   kernel, so no status reports bad ones: a value outside is clamped, one
+ *   that falls counts as the largest before it, and nothing outside the
+ *   arrays is touched); groups may be empty. qw [groups][N][K], sw
  *   [groups][ceil(N/128)][ceil(K/128)], bias [groups][N] or NULL; sx as
  *   above for all M rows. Rows of y before offsets[0] and from
  *   offsets[groups] on are not written. groups in [1, 65536], M < 2^31.

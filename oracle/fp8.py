@@ -92,6 +92,12 @@ def linear(qx, sx, qw, sw, bias=None):
     return y, mag, peak
 
 
+def rising(offsets, M):
+    """Group bounds as the kernels read them: values clamped into [0, M], one
+    that falls counting as the largest before it."""
+    return np.maximum.accumulate(np.clip(np.asarray(offsets, np.int64), 0, M)).tolist()
+
+
 def grouped_linear(qx, sx, offsets, qw, sw, bias=None):
     """linear() with group g's weight for the rows offsets[g] .. offsets[g + 1]; other rows are NaN."""
     y = np.full((qx.shape[0], qw.shape[1]), np.nan)
