@@ -59,9 +59,17 @@ _HERE = contextlib.nullcontext()
 _F32, _BF16 = torch.float32, torch.bfloat16
 
 
+def _aligned_copy(x):
+    """Dense rows at an address that the kernels can read, for rows at one they
+    cannot (16 bytes at a time: a broadcast or unaligned stride or address).
+    (contiguous() would keep a dense view where it is.)"""
+    return x.clone(memory_format=torch.contiguous_format)
+
+
 def quantize_act_fp8(x: torch.Tensor, stream=None):
-    """x: bf16 [M, K] on the GPU (K a multiple of 16; rows may be strided, the
-    row stride a multiple of 8) -> (qx E4M3 [M, K], sx fp32 [ceil(K/128), M]):
+    """x: bf16 [M, K] on the GPU (K a multiple of 16; rows may be strided; where
+    the row stride is not a multiple of 8 or the address not one of 16 bytes a
+    copy is read) -> (qx E4M3 [M, K], sx fp32 [ceil(K/128), M]):
     per row and 128 channels s = max(amax / 448, 2^-120), code = e4m3(x / s)
     (include/svdq.h gives every rounding)."""
     if not (x.is_cuda and x.dtype is _BF16 and x.dim() == 2 and x.is_contiguous()):
@@ -73,8 +81,8 @@ def quantize_act_fp8(x: torch.Tensor, stream=None):
         raise ValueError(f"x must have K a positive multiple of 16, got {K}")
     ldx = x.stride(0) if M > 1 else K
     with _on(x, stream):
-        if ldx < K or ldx % 8:                  # a broadcast or unaligned row stride
-            x, ldx = x.contiguous(), K
+        if ldx < K or ldx % 8 or x.data_ptr() % 16:
+            x, ldx = _aligned_copy(x), K
         # (x.new_empty costs half a us less than torch.empty)
         qx, sx = x.new_empty(M, K, dtype=E4M3), x.new_empty(blocks(K), M, dtype=_F32)
         _check(load_library().svdq_quantize_act_fp8(x.data_ptr(), M, K, ldx, qx.data_ptr(), sx.data_ptr(), _stream_now()),
@@ -214,9 +222,9 @@ def _layer(x, qw, sw, bias, act, out_dtype, y, offsets=None):
                 and (y.stride(1) == 1 or N == 1) and ldy >= N):
             return None
         if not need and y.untyped_storage().data_ptr() == x.untyped_storage().data_ptr():
-            x, ldx = x.clone(memory_format=torch.contiguous_format), K   # in place: y is written while x is read
-    if ldx < K or ldx % 8:                      # a broadcast or unaligned row stride
-        x, ldx = x.contiguous(), K
+            x, ldx = _aligned_copy(x), K         # in place: y is written while x is read
+    if ldx < K or ldx % 8 or x.data_ptr() % 16:
+        x, ldx = _aligned_copy(x), K
     ws = x.new_empty(need, dtype=torch.uint8) if need else None
     f32 = y.dtype is _F32
     if offsets is None:

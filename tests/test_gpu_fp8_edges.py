@@ -1,4 +1,5 @@
-"""The 8-bit layers where a call can go wrong: offsets that fall."""
+"""The 8-bit layers where a call can go wrong: offsets that fall, rows at
+addresses that the kernels cannot read."""
 import numpy as np
 import pytest
 import torch
@@ -50,3 +51,25 @@ def test_offsets_that_fall(M, N, layer, kind, out):
     assert (np64(y)[~inside] == -3.0).all()
     if inside.any():
         check_product(y[torch.from_numpy(inside).cuda()], [r[inside] for r in ref], K)
+
+
+@pytest.mark.parametrize("M,K", [(1, 400), (5, 400), (16, 4096), (40, 272), (300, 144)])
+def test_rows_at_any_address(M, K):
+    """Activations at any address of a bf16 value, dense or strided, are those
+    of an aligned copy: the activation pass, a dense and a grouped layer."""
+    note(f"8-bit layers on unaligned rows {M} x {K}")
+    N = 136
+    x = acts(M, K, 1)
+    lay = svdq.Fp8Linear.from_quantized(svdq.quantize_fp8(weights(K, N, 2), biases(N, 3)))
+    grp = svdq.Fp8GroupedLinear(torch.stack([lay.qw.view(torch.uint8)] * 2).view(lay.qw.dtype), torch.stack([lay.sw] * 2))
+    offs = torch.tensor([0, M // 2, M], dtype=torch.int32, device="cuda")
+    want_q, want_s = svdq.quantize_act_fp8(x)
+    want, want_g = lay(x), grp(x, offs)
+    buf = torch.zeros(M * (K + 48) + 64, dtype=torch.bfloat16, device="cuda")
+    for off in (1, 4, 7):
+        for ld in (K, K + 40, K + 3):
+            v = buf[off:off + M * ld].view(M, ld)[:, :K]
+            v.copy_(x)
+            q, s = svdq.quantize_act_fp8(v)
+            assert torch.equal(q.view(torch.uint8), want_q.view(torch.uint8)) and torch.equal(s, want_s)
+            assert torch.equal(lay(v), want) and torch.equal(grp(v, offs), want_g)
