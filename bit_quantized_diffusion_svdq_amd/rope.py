@@ -99,8 +99,11 @@ def rope_axes(q, k, pos, plan: RopePlan, q_norm=None, k_norm=None, eps: float = 
     allowed (token and head strides multiples of 8), rotated by pos [T, axes]
     (int32 or fp32) after an RMS norm of each head where q_norm / k_norm [D]
     is given: (q', k'), or q' alone if k is None. q_out / k_out may be q / k
-    themselves (in place) or buffers of any such layout. inverse undoes the
-    rotation; without a norm it is also its gradient."""
+    themselves (in place) or buffers of any such layout; addresses are
+    multiples of 16 bytes. inverse undoes the rotation; without a norm that is
+    also how a gradient goes back through it. Nothing is recorded for
+    autograd: q and k that require a gradient are refused while it is on, the
+    norms' weights are taken as constants."""
     D, dt, dev = plan.head_dim, q.dtype, q.device
     _heads(q, "q", D)
     T, hq, _ = q.shape
@@ -108,6 +111,9 @@ def rope_axes(q, k, pos, plan: RopePlan, q_norm=None, k_norm=None, eps: float = 
         raise ValueError(f"q must be bf16 or fp32, got {dt}")
     if hq < 1:
         raise ValueError("q must have at least one head")
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        raise ValueError("q or k requires a gradient, which this call does not record: call it under torch.no_grad() or "
+                         "on detached tensors (inverse=True turns a gradient back)")
     hk = 0
     if k is not None:
         _heads(k, "k", D)

@@ -21,3 +21,23 @@ def test_rising_bounds_share_no_row(offs):
     assert owners.max() <= 1
     if all(x <= y for x, y in zip(offs, offs[1:])):
         assert b == offs
+
+
+# ---------------------------------------------------------------- gradients
+
+def _rope_args():
+    return dict(q=torch.zeros((4, 3, 32), dtype=torch.bfloat16), k=torch.zeros((4, 1, 32), dtype=torch.bfloat16),
+                pos=torch.zeros((4, 2), dtype=torch.int32), plan=svdq.RopePlan((16, 16), device="cpu"))
+
+
+@pytest.mark.parametrize("name", ["q", "k"])
+def test_rope_axes_refuses_to_lose_a_gradient(name):
+    a = _rope_args()
+    a[name].requires_grad_()
+    with pytest.raises(ValueError, match="requires a gradient"):
+        svdq.rope_axes(**a)
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU device"):     # the next check: the call itself is fine
+        svdq.rope_axes(**a)
+    a[name] = a[name].detach()
+    with pytest.raises(ValueError, match="GPU device"):
+        svdq.rope_axes(**a, q_norm=torch.zeros(32, dtype=torch.bfloat16, requires_grad=True))
