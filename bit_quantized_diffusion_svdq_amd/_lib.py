@@ -64,6 +64,8 @@ _SIGS = {
     "svdq_linear_fp8": [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _I64, _P, _I64, _P],
     "svdq_linear_fp8_grouped": [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _P, _I32, _I64, _P, _I64, _P],
     "svdq_rope_axes": [_P, _P, _I64, _I32, _I32, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P],
+    "svdq_rope_axes_grouped": [_P, _P, _I64, _I32, _I32, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P,
+                               _I32, _P],
 }
 
 
@@ -347,6 +349,15 @@ def svdq_rope_axes(q, k, T, D, dtype, pos, pos_dtype, axes, turns, axis, pairs, 
                                          None if k is None else ctypes.addressof(k), T, D, dtype, _ptr(pos), pos_dtype,
                                          axes, _ptr(turns), _ptr(axis), pairs, pairing, inverse, eps, _stream(stream)),
            "svdq_rope_axes")
+
+
+def svdq_rope_axes_grouped(q, k, T, D, dtype, pos, pos_dtype, axes, turns, axis, pairs, pairing, inverse, eps, offsets,
+                           groups, stream=None):
+    """svdq_rope_axes for tokens sorted by group (offsets int32 [groups + 1])."""
+    _check(load_library().svdq_rope_axes_grouped(None if q is None else ctypes.addressof(q),
+                                                 None if k is None else ctypes.addressof(k), T, D, dtype, _ptr(pos),
+                                                 pos_dtype, axes, _ptr(turns), _ptr(axis), pairs, pairing, inverse, eps,
+                                                 _ptr(offsets), groups, _stream(stream)), "svdq_rope_axes_grouped")
 
 
 # ---------------------------------------------------------------- tensor helpers

@@ -166,7 +166,9 @@ class FusedQKV:
 
     def __call__(self, x: torch.Tensor, pos: torch.Tensor, offsets=None, y=None, stream=None):
         """x bf16 [M, K], pos [M, axes]; offsets for a grouped layer (rows
-        sorted by stream); y: the buffer for the projection, bf16 [M, N]."""
+        sorted by stream; rows of no group are left as they are in a given y
+        and are unspecified in a new one); y: the buffer for the projection,
+        bf16 [M, N]."""
         grouped = isinstance(self.layer, Fp8GroupedLinear)
         _lib._require(grouped == (offsets is not None), "offsets belong to a grouped layer, and it needs them")
         with _on(x, stream):
@@ -174,5 +176,6 @@ class FusedQKV:
             _lib._require(y.dtype == torch.bfloat16, f"y must be bf16, got {y.dtype}")
             h = y.unflatten(1, (self.heads + 2 * self.kv_heads, self.plan.head_dim))
             q, k, v = h.split((self.heads, self.kv_heads, self.kv_heads), dim=1)
-            rope_axes(q, k, pos, self.plan, self.q_norm, self.k_norm, self.eps, q_out=q, k_out=k)
+            rope_axes(q, k, pos, self.plan, self.q_norm, self.k_norm, self.eps, q_out=q, k_out=k,
+                      offsets=offsets)
         return q, k, v

@@ -866,6 +866,67 @@ svdq_status check_rope_heads(const svdq_rope_heads* h, const char* name, int min
     return SVDQ_OK;
 }
 
+svdq_status rope_axes_impl(const svdq_rope_heads* q, const svdq_rope_heads* k, int64_t T, int32_t D, int32_t dtype,
+                           const void* pos, int32_t pos_dtype, int32_t axes, const double* turns,
+                           const int32_t* axis, int32_t pairs, int32_t pairing, int32_t inverse, float eps,
+                           const int32_t* offsets, int32_t groups, void* stream, const char* what) {
+    svdq_status s;
+    if (!q) return fail(SVDQ_ERR_NULL, "q is required");
+    if (T < 0 || T >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "T = %lld must be in [0, 2^31)", (long long)T);
+    if (D < 8 || D > 512 || D % 8) return fail(SVDQ_ERR_SHAPE, "D = %d must be a multiple of 8 in [8, 512]", D);
+    if (pairs < 0 || pairs % 4 || 2 * (int64_t)pairs > D)
+        return fail(SVDQ_ERR_SHAPE, "pairs = %d must be a multiple of 4 with 2 * pairs <= D = %d", pairs, D);
+    if (axes < 1 || axes > 8) return fail(SVDQ_ERR_SHAPE, "axes = %d must be in [1, 8]", axes);
+    if (dtype != SVDQ_DT_BF16 && dtype != SVDQ_DT_F32) return fail(SVDQ_ERR_UNSUPPORTED, "dtype %d is not supported", dtype);
+    if (pos_dtype != SVDQ_POS_I32 && pos_dtype != SVDQ_POS_F32)
+        return fail(SVDQ_ERR_UNSUPPORTED, "position dtype %d is not supported", pos_dtype);
+    if (pairing != SVDQ_PAIRS_INTERLEAVED && pairing != SVDQ_PAIRS_HALF)
+        return fail(SVDQ_ERR_UNSUPPORTED, "pairing %d is not supported", pairing);
+    if (inverse != 0 && inverse != 1) return fail(SVDQ_ERR_UNSUPPORTED, "inverse must be 0 or 1");
+    if (!(eps >= 0.0f)) return fail(SVDQ_ERR_UNSUPPORTED, "eps must be >= 0");
+    if (groups < 0 || groups > 65536) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
+    if ((s = check_rope_heads(q, "q", 1, T, D)) != SVDQ_OK) return s;
+    if (k && (s = check_rope_heads(k, "k", 0, T, D)) != SVDQ_OK) return s;
+    const int64_t heads = (int64_t)q->heads + (k ? k->heads : 0);
+    if (T * ((heads * D + 511) / 512 + 1) >= ((int64_t)1 << 26))
+        return fail(SVDQ_ERR_SHAPE, "T = %lld with %lld heads needs more waves than one launch holds", (long long)T, (long long)heads);
+    if (T == 0) { g_last_error.clear(); return SVDQ_OK; }
+    if (pairs > 0 && (!pos || !turns || !axis)) return fail(SVDQ_ERR_NULL, "pos, turns and axis are required");
+    if (groups && !offsets) return fail(SVDQ_ERR_NULL, "offsets is required");
+    if (offsets && !aligned(offsets, 4)) return fail(SVDQ_ERR_ALIGN, "offsets needs 4-byte alignment");
+    if (pairs > 0 && (!aligned(pos, 4) || !aligned(turns, 8) || !aligned(axis, 4)))
+        return fail(SVDQ_ERR_ALIGN, "pos, axis need 4-byte alignment, turns 8");
+    int cus = 0;
+    if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
+    RopeArgs a = {};
+    const svdq_rope_heads* side[2] = {q, k};
+    for (int i = 0; i < 2; ++i) {
+        if (!side[i]) continue;
+        a.x[i] = side[i]->x;
+        a.y[i] = side[i]->y;
+        a.norm[i] = side[i]->norm;
+        a.ts[i] = side[i]->token_stride;
+        a.hs[i] = side[i]->head_stride;
+        a.yts[i] = side[i]->y_token_stride;
+        a.yhs[i] = side[i]->y_head_stride;
+        a.heads[i] = side[i]->heads;
+    }
+    a.pos = pos;
+    a.turns = turns;
+    a.axis = axis;
+    a.offs = offsets;
+    a.groups = groups;
+    a.T = T;
+    a.D = D;
+    a.pairs = pairs;
+    a.axes = axes;
+    a.pos_f32 = pos_dtype == SVDQ_POS_F32;
+    a.inverse = inverse;
+    a.eps = eps;
+    return launched(launch_rope_axes(a, dtype == SVDQ_DT_F32, pairing == SVDQ_PAIRS_HALF, cus, (hipStream_t)stream),
+                    what);
+}
+
 }  // namespace
 
 extern "C" {
@@ -950,56 +1011,17 @@ svdq_status svdq_rope_axes(const svdq_rope_heads* q, const svdq_rope_heads* k, i
                            const void* pos, int32_t pos_dtype, int32_t axes, const double* turns,
                            const int32_t* axis, int32_t pairs, int32_t pairing, int32_t inverse, float eps,
                            void* stream) {
-    svdq_status s;
-    if (!q) return fail(SVDQ_ERR_NULL, "q is required");
-    if (T < 0 || T >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "T = %lld must be in [0, 2^31)", (long long)T);
-    if (D < 8 || D > 512 || D % 8) return fail(SVDQ_ERR_SHAPE, "D = %d must be a multiple of 8 in [8, 512]", D);
-    if (pairs < 0 || pairs % 4 || 2 * (int64_t)pairs > D)
-        return fail(SVDQ_ERR_SHAPE, "pairs = %d must be a multiple of 4 with 2 * pairs <= D = %d", pairs, D);
-    if (axes < 1 || axes > 8) return fail(SVDQ_ERR_SHAPE, "axes = %d must be in [1, 8]", axes);
-    if (dtype != SVDQ_DT_BF16 && dtype != SVDQ_DT_F32) return fail(SVDQ_ERR_UNSUPPORTED, "dtype %d is not supported", dtype);
-    if (pos_dtype != SVDQ_POS_I32 && pos_dtype != SVDQ_POS_F32)
-        return fail(SVDQ_ERR_UNSUPPORTED, "position dtype %d is not supported", pos_dtype);
-    if (pairing != SVDQ_PAIRS_INTERLEAVED && pairing != SVDQ_PAIRS_HALF)
-        return fail(SVDQ_ERR_UNSUPPORTED, "pairing %d is not supported", pairing);
-    if (inverse != 0 && inverse != 1) return fail(SVDQ_ERR_UNSUPPORTED, "inverse must be 0 or 1");
-    if (!(eps >= 0.0f)) return fail(SVDQ_ERR_UNSUPPORTED, "eps must be >= 0");
-    if ((s = check_rope_heads(q, "q", 1, T, D)) != SVDQ_OK) return s;
-    if (k && (s = check_rope_heads(k, "k", 0, T, D)) != SVDQ_OK) return s;
-    const int64_t heads = (int64_t)q->heads + (k ? k->heads : 0);
-    if (T * ((heads * D + 511) / 512 + 1) >= ((int64_t)1 << 26))
-        return fail(SVDQ_ERR_SHAPE, "T = %lld with %lld heads needs more waves than one launch holds", (long long)T, (long long)heads);
-    if (T == 0) { g_last_error.clear(); return SVDQ_OK; }
-    if (pairs > 0 && (!pos || !turns || !axis)) return fail(SVDQ_ERR_NULL, "pos, turns and axis are required");
-    if (pairs > 0 && (!aligned(pos, 4) || !aligned(turns, 8) || !aligned(axis, 4)))
-        return fail(SVDQ_ERR_ALIGN, "pos, axis need 4-byte alignment, turns 8");
-    int cus = 0;
-    if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
-    RopeArgs a = {};
-    const svdq_rope_heads* side[2] = {q, k};
-    for (int i = 0; i < 2; ++i) {
-        if (!side[i]) continue;
-        a.x[i] = side[i]->x;
-        a.y[i] = side[i]->y;
-        a.norm[i] = side[i]->norm;
-        a.ts[i] = side[i]->token_stride;
-        a.hs[i] = side[i]->head_stride;
-        a.yts[i] = side[i]->y_token_stride;
-        a.yhs[i] = side[i]->y_head_stride;
-        a.heads[i] = side[i]->heads;
-    }
-    a.pos = pos;
-    a.turns = turns;
-    a.axis = axis;
-    a.T = T;
-    a.D = D;
-    a.pairs = pairs;
-    a.axes = axes;
-    a.pos_f32 = pos_dtype == SVDQ_POS_F32;
-    a.inverse = inverse;
-    a.eps = eps;
-    return launched(launch_rope_axes(a, dtype == SVDQ_DT_F32, pairing == SVDQ_PAIRS_HALF, cus, (hipStream_t)stream),
-                    "svdq_rope_axes launch");
+    return rope_axes_impl(q, k, T, D, dtype, pos, pos_dtype, axes, turns, axis, pairs, pairing, inverse, eps, nullptr, 0,
+                          stream, "svdq_rope_axes launch");
+}
+
+svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_heads* k, int64_t T, int32_t D,
+                                   int32_t dtype, const void* pos, int32_t pos_dtype, int32_t axes,
+                                   const double* turns, const int32_t* axis, int32_t pairs, int32_t pairing,
+                                   int32_t inverse, float eps, const int32_t* offsets, int32_t groups, void* stream) {
+    if (groups < 1) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
+    return rope_axes_impl(q, k, T, D, dtype, pos, pos_dtype, axes, turns, axis, pairs, pairing, inverse, eps, offsets,
+                          groups, stream, "svdq_rope_axes_grouped launch");
 }
 
 }  // extern "C"

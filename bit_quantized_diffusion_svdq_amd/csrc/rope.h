@@ -12,6 +12,8 @@ struct RopeArgs {
     const void* pos;
     const double* turns;            // [pairs] turns per unit of position
     const int* axis;                // [pairs]
+    const int* offs;                // rows in groups: [groups + 1] row offsets, else NULL
+    int groups;
     int64_t T;
     int D, pairs, axes, pos_f32, inverse;
     float eps;

@@ -18,7 +18,7 @@ from typing import Sequence
 import torch
 
 from ._lib import RopeHeads, _check, _require, load_library
-from .fp8 import _on, _stream_now
+from .fp8 import _groups, _on, _stream_now
 
 PAIRING = {"interleaved": 0, "half": 1}
 
@@ -94,7 +94,7 @@ def _side(x, y, norm, T, H, D):
 
 
 def rope_axes(q, k, pos, plan: RopePlan, q_norm=None, k_norm=None, eps: float = 1e-6, inverse: bool = False,
-              q_out=None, k_out=None, stream=None):
+              q_out=None, k_out=None, stream=None, offsets=None):
     """q [T, Hq, D] and k [T, Hk, D] (or None), bf16 or fp32, strided views
     allowed (token and head strides multiples of 8), rotated by pos [T, axes]
     (int32 or fp32) after an RMS norm of each head where q_norm / k_norm [D]
@@ -103,7 +103,9 @@ def rope_axes(q, k, pos, plan: RopePlan, q_norm=None, k_norm=None, eps: float = 
     multiples of 16 bytes. inverse undoes the rotation; without a norm that is
     also how a gradient goes back through it. Nothing is recorded for
     autograd: q and k that require a gradient are refused while it is on, the
-    norms' weights are taken as constants."""
+    norms' weights are taken as constants. offsets (int32 [groups + 1] on the
+    GPU, as a grouped layer takes them): tokens of no group are left as they
+    are in a given output and are unspecified in a new one."""
     D, dt, dev = plan.head_dim, q.dtype, q.device
     _heads(q, "q", D)
     T, hq, _ = q.shape
@@ -133,13 +135,22 @@ def rope_axes(q, k, pos, plan: RopePlan, q_norm=None, k_norm=None, eps: float = 
         raise ValueError(f"tensors must be on a GPU device, got {dev}")
     if pos.device != dev or plan.turns.device != dev or (k is not None and k.device != dev):
         raise ValueError(f"k, pos or the plan is not on {dev}")
+    groups = 0
+    if offsets is not None:
+        groups = _groups(offsets)
+        if offsets.device != dev:
+            raise ValueError(f"offsets is on {offsets.device}, expected {dev}")
     with _on(q, stream):
         q_out, qs = _side(q, q_out, q_norm, T, hq, D)
         ks = None
         if k is not None:
             k_out, ks = _side(k, k_out, k_norm, T, hk, D)
-        _check(load_library().svdq_rope_axes(ctypes.addressof(qs), None if ks is None else ctypes.addressof(ks), T, D,
-                                             dt is torch.float32, pos.data_ptr(), f32_pos, plan.axes,
-                                             plan.turns.data_ptr(), plan.axis.data_ptr(), plan.pairs,
-                                             PAIRING[plan.pairing], bool(inverse), eps, _stream_now()), "svdq_rope_axes")
+        args = (ctypes.addressof(qs), None if ks is None else ctypes.addressof(ks), T, D, dt is torch.float32,
+                pos.data_ptr(), f32_pos, plan.axes, plan.turns.data_ptr(), plan.axis.data_ptr(), plan.pairs,
+                PAIRING[plan.pairing], bool(inverse), eps)
+        if groups:
+            _check(load_library().svdq_rope_axes_grouped(*args, offsets.data_ptr(), groups, _stream_now()),
+                   "svdq_rope_axes_grouped")
+        else:
+            _check(load_library().svdq_rope_axes(*args, _stream_now()), "svdq_rope_axes")
     return q_out if k is None else (q_out, k_out)

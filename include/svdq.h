@@ -620,6 +620,11 @@ svdq_status svdq_linear_fp8_grouped(const void* x, int64_t M, int64_t K, int64_t
  * fp32 sine and cosine; the rest is fp32 with one rounding of the output.
  * heads of q >= 1, of k >= 0, axes in [1, 8]. T == 0 is valid, and so is
  * pairs == 0 (the norm alone; pos, turns and axis may then be NULL).
+ *
+ * svdq_rope_axes_grouped -- the same for tokens sorted by group, as
+ * svdq_gemm_fp8_grouped leaves them (its offsets: DEVICE int32 [groups + 1]):
+ * tokens before offsets[0] and from offsets[groups] on are of no group, and
+ * their y is not written.
  */
 typedef enum { SVDQ_POS_I32 = 0, SVDQ_POS_F32 = 1 } svdq_pos_dtype;
 typedef enum { SVDQ_PAIRS_INTERLEAVED = 0, SVDQ_PAIRS_HALF = 1 } svdq_pairing;
@@ -635,6 +640,10 @@ svdq_status svdq_rope_axes(const svdq_rope_heads* q, const svdq_rope_heads* k, i
                            const void* pos, int32_t pos_dtype, int32_t axes, const double* turns,
                            const int32_t* axis, int32_t pairs, int32_t pairing, int32_t inverse, float eps,
                            void* stream);
+svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_heads* k, int64_t T, int32_t D,
+                                   int32_t dtype, const void* pos, int32_t pos_dtype, int32_t axes,
+                                   const double* turns, const int32_t* axis, int32_t pairs, int32_t pairing,
+                                   int32_t inverse, float eps, const int32_t* offsets, int32_t groups, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,11 +1,14 @@
 """Host-side checks of the 8-bit layers and the rotary positions at the calls
 that could go wrong, without a GPU."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import bit_quantized_diffusion_svdq_amd as svdq
 from oracle import fp8 as ofp8
+from test_fp8_rope_cpu import ALIGN, C, D, E, NULL, OK, SHAPE, _heads, _prod, lib, valid
 
 
 # ---------------------------------------------------------------- offsets that fall
@@ -41,3 +44,32 @@ def test_rope_axes_refuses_to_lose_a_gradient(name):
     a[name] = a[name].detach()
     with pytest.raises(ValueError, match="GPU device"):
         svdq.rope_axes(**a, q_norm=torch.zeros(32, dtype=torch.bfloat16, requires_grad=True))
+
+
+# ---------------------------------------------------------------- tokens in groups
+
+def _rope(lib, q=None, k=None, offs=E + 64, groups=2, T=5):
+    q = _heads() if q is None else q
+    return lib.svdq_rope_axes_grouped(ctypes.addressof(q), ctypes.addressof(k) if k else None, T, 64, 0, C, 0, 3, D, E, 32, 0, 0,
+                                      1e-6, offs, groups, None)
+
+
+def test_rope_axes_grouped_rejects(lib):
+    assert _rope(lib, groups=0) == SHAPE and _rope(lib, groups=-1) == SHAPE and _rope(lib, groups=65537) == SHAPE
+    assert _rope(lib, offs=None) == NULL and _rope(lib, offs=E + 2) == ALIGN
+    assert _rope(lib, T=0, offs=None) == OK
+    valid(_rope(lib))
+    valid(_rope(lib, k=_heads(heads=0), groups=65536))
+
+
+@pytest.mark.parametrize("offs", [torch.zeros(3, dtype=torch.int64), torch.zeros(1, dtype=torch.int32),
+                                  torch.zeros((2, 2), dtype=torch.int32), torch.zeros(6, dtype=torch.int32)[::2]])
+def test_rope_axes_refuses_offsets(offs, monkeypatch):
+    class Gpu(torch.Tensor):
+        """A host tensor that says it is on a GPU: the checks before the call."""
+        device = torch.device("cuda", 0)
+
+    a = {n: t.as_subclass(Gpu) if isinstance(t, torch.Tensor) else t for n, t in _rope_args().items()}
+    a["plan"].turns = a["plan"].turns.as_subclass(Gpu)
+    with pytest.raises(ValueError, match="offsets must be"):
+        svdq.rope_axes(**a, offsets=offs)

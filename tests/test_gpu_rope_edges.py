@@ -1,5 +1,5 @@
 """Rotary positions where a call can go wrong: values that are not finite
-beside channels that do not turn."""
+beside channels that do not turn, tokens of no group."""
 import numpy as np
 import pytest
 import torch
@@ -39,3 +39,54 @@ def test_values_past_the_pairs_stand_alone(T, dt, pairing, dims):
     keep = torch.isfinite(w)
     assert torch.equal(got[..., keep], want[..., keep])
     assert torch.isinf(got[..., 41]).all() and got[..., 50].isnan().all()
+
+
+@pytest.mark.parametrize("T,offs", [(7, [0, 7]), (30, [2, 10, 10, 20]), (30, [30, 30]), (1, [0, 0]), (700, [3, 500, 690])])
+def test_tokens_of_no_group_stay(T, offs):
+    note(f"rope_axes groups {T} {offs}")
+    H, HK, D = 3, 1, 64
+    q, k, pos, plan = heads(T, H, D, 1), heads(T, HK, D, 2), positions(T, 2, 3), svdq.RopePlan((32, 32))
+    w = (1 + 0.1 * heads(1, 1, D, 7)).flatten()
+    want_q, want_k = svdq.rope_axes(q, k, pos, plan, q_norm=w, k_norm=w)
+    o = torch.tensor(offs, dtype=torch.int32, device="cuda")
+    inside = torch.zeros(T, dtype=torch.bool, device="cuda")
+    inside[offs[0]:offs[-1]] = True
+    for in_place in (False, True):
+        qo, ko = (q.clone(), k.clone()) if in_place else (torch.full_like(q, -3.0), torch.full_like(k, -3.0))
+        before = qo.clone(), ko.clone()
+        src = (qo, ko) if in_place else (q, k)
+        svdq.rope_axes(*src, pos, plan, q_norm=w, k_norm=w, q_out=qo, k_out=ko, offsets=o)
+        for got, want, old in ((qo, want_q, before[0]), (ko, want_k, before[1])):
+            assert torch.equal(got[inside], want[inside]) and torch.equal(got[~inside], old[~inside])
+
+
+def test_qkv_block_leaves_rows_of_no_group():
+    """FusedQKV over a grouped layer into a given buffer: the rows that the
+    projection leaves as they are are not turned either; a graph of it, its
+    offsets moving between replays, does the same."""
+    note("FusedQKV over Fp8GroupedLinear, rows of no group")
+    from test_gpu_fp8 import acts, weights
+    T, K, H, D = 50, 144, 2, 32
+    N = 3 * H * D
+    layer = svdq.Fp8GroupedLinear.from_quantized(svdq.quantize_fp8(weights(K, N, 1, groups=2)))
+    plan = svdq.RopePlan((16, 16))
+    block = svdq.FusedQKV(layer, plan, H)
+    x, pos = acts(T, K, 2), positions(T, 2, 3)
+    y, o = torch.empty((T, N), dtype=torch.bfloat16, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    graph = svdq.CapturedSequence(lambda: block(x, pos, o, y=y))
+    for offs in ([4, 20, 41], [0, 0, 50], [7, 7, 7], [0, 30, 33]):
+        o.copy_(torch.tensor(offs, dtype=torch.int32))
+        full = layer(x, o)
+        wq, wk, wv = full.unflatten(1, (3 * H, D)).split(H, dim=1)
+        rq, rk = svdq.rope_axes(wq, wk, pos, plan)
+        for replay in (False, True):
+            y.fill_(-3.0)
+            q, k, v = y.unflatten(1, (3 * H, D)).split(H, dim=1)
+            if replay:
+                graph.replay()
+            else:
+                block(x, pos, o, y=y)
+            torch.cuda.synchronize()
+            r = slice(offs[0], offs[-1])
+            assert torch.equal(q[r], rq[r]) and torch.equal(k[r], rk[r]) and torch.equal(v[r], wv[r])
+            assert (y[:offs[0]] == -3.0).all() and (y[offs[-1]:] == -3.0).all()
