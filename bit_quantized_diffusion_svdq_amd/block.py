@@ -159,21 +159,38 @@ class FusedQKV:
                       f"the layer has {layer.N} outputs, {heads} query and 2 x {kv_heads} key and value heads of {D} "
                       f"need {(heads + 2 * kv_heads) * D}")
         for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-            _lib._require(w is None or (tuple(w.shape) == (D,) and w.dtype == torch.bfloat16),
-                          f"{name} must be a bf16 vector of {D} values")
+            _lib._require(w is None or (tuple(w.shape) == (D,) and w.dtype == torch.bfloat16 and w.is_contiguous()),
+                          f"{name} must be a contiguous bf16 vector of {D} values")
         self.layer, self.plan, self.heads, self.kv_heads = layer, plan, heads, kv_heads
         self.q_norm, self.k_norm, self.eps = q_norm, k_norm, eps
+
+    def _check(self, x, pos, y):
+        """What the rotation would refuse, before the projection writes anything."""
+        if x.dim() != 2:
+            raise ValueError(f"x must be [M, {self.layer.K}], got {tuple(x.shape)}")
+        M, N, dev, plan = x.shape[0], self.layer.N, x.device, self.plan
+        if not ((pos.dtype is torch.int32 or pos.dtype is torch.float32) and pos.shape == (M, plan.axes)
+                and pos.is_contiguous()):
+            raise ValueError(f"pos must be contiguous int32 or fp32 [{M}, {plan.axes}], got {tuple(pos.shape)} {pos.dtype}")
+        if y is not None:
+            if not (y.dtype is torch.bfloat16 and y.shape == (M, N) and y.stride(1) == 1
+                    and (M <= 1 or (y.stride(0) >= N and y.stride(0) % 8 == 0)) and y.data_ptr() % 16 == 0):
+                raise ValueError(f"y must be bf16 [{M}, {N}] with contiguous columns, a row stride that is a multiple of 8 "
+                                 f"and an address that is one of 16 bytes, got {tuple(y.shape)} {y.dtype}, strides {y.stride()}")
+        for name, t in (("pos", pos), ("y", y), ("q_norm", self.q_norm), ("k_norm", self.k_norm), ("the plan", plan.turns)):
+            if t is not None and t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
     def __call__(self, x: torch.Tensor, pos: torch.Tensor, offsets=None, y=None, stream=None):
         """x bf16 [M, K], pos [M, axes]; offsets for a grouped layer (rows
         sorted by stream; rows of no group are left as they are in a given y
         and are unspecified in a new one); y: the buffer for the projection,
-        bf16 [M, N]."""
+        bf16 [M, N], the row stride a multiple of 8, on 16 bytes."""
         grouped = isinstance(self.layer, Fp8GroupedLinear)
         _lib._require(grouped == (offsets is not None), "offsets belong to a grouped layer, and it needs them")
+        self._check(x, pos, y)
         with _on(x, stream):
             y = self.layer(x, offsets, y=y) if grouped else self.layer(x, y=y)
-            _lib._require(y.dtype == torch.bfloat16, f"y must be bf16, got {y.dtype}")
             h = y.unflatten(1, (self.heads + 2 * self.kv_heads, self.plan.head_dim))
             q, k, v = h.split((self.heads, self.kv_heads, self.kv_heads), dim=1)
             rope_axes(q, k, pos, self.plan, self.q_norm, self.k_norm, self.eps, q_out=q, k_out=k,

@@ -73,3 +73,43 @@ def test_rope_axes_refuses_offsets(offs, monkeypatch):
     a["plan"].turns = a["plan"].turns.as_subclass(Gpu)
     with pytest.raises(ValueError, match="offsets must be"):
         svdq.rope_axes(**a, offsets=offs)
+
+
+# ---------------------------------------------------------------- a block's refusals come first
+
+class NotCalled:
+    """A layer that must not run: its call would overwrite y."""
+    N, K = 192, 144
+
+    def __call__(self, *a, **kw):
+        raise AssertionError("the projection ran")
+
+
+def _y(M=3, ld=192, off=0, dt=torch.bfloat16):
+    return torch.zeros(M * ld + off + 8, dtype=dt)[off:off + M * ld].view(M, ld)[:, :192]
+
+
+@pytest.mark.parametrize("kw,text", [
+    (dict(y=_y(dt=torch.float32)), "y must be"), (dict(y=_y(ld=196)), "y must be"), (dict(y=_y(off=4)), "y must be"),
+    (dict(y=_y(M=4)), "y must be"), (dict(y=torch.zeros((192, 3), dtype=torch.bfloat16).t()), "y must be"),
+    (dict(y=_y(M=1).expand(3, 192)), "y must be"), (dict(pos=torch.zeros((3, 3), dtype=torch.int32)), "pos must be"),
+    (dict(pos=torch.zeros((3, 2), dtype=torch.int64)), "pos must be"), (dict(x=torch.zeros(144, dtype=torch.bfloat16)), "x must be"),
+    (dict(pos=torch.zeros((3, 2), device="meta")), "pos is on"), (dict(y=torch.zeros((3, 192), dtype=torch.bfloat16, device="meta")), "y is on"),
+])
+def test_qkv_block_refuses_before_it_writes(kw, text):
+    block = svdq.FusedQKV(NotCalled(), svdq.RopePlan((16, 16), device="cpu"), 2)
+    a = dict(x=torch.zeros((3, 144), dtype=torch.bfloat16), pos=torch.zeros((3, 2), dtype=torch.int32)) | kw
+    with pytest.raises(ValueError, match=text):
+        block(**a)
+    for good in (None, _y(), _y(ld=200), _y(off=8)):
+        with pytest.raises(AssertionError, match="ran"):
+            block(torch.zeros((3, 144), dtype=torch.bfloat16), torch.zeros((3, 2), dtype=torch.int32), y=good)
+
+
+def test_qkv_block_refuses_norms_elsewhere():
+    norm = torch.ones(32, dtype=torch.bfloat16, device="meta")
+    block = svdq.FusedQKV(NotCalled(), svdq.RopePlan((16, 16), device="cpu"), 2, k_norm=norm)
+    with pytest.raises(ValueError, match="k_norm is on"):
+        block(torch.zeros((3, 144), dtype=torch.bfloat16), torch.zeros((3, 2), dtype=torch.int32))
+    with pytest.raises(ValueError, match="q_norm"):
+        svdq.FusedQKV(NotCalled(), svdq.RopePlan((16, 16), device="cpu"), 2, q_norm=torch.ones(64, dtype=torch.bfloat16)[::2])
