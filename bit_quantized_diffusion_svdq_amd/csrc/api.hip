@@ -866,6 +866,19 @@ svdq_status check_rope_heads(const svdq_rope_heads* h, const char* name, int min
     return SVDQ_OK;
 }
 
+// Outputs over other tensors of the call: a wave's stores would race with
+// another's loads. (By base address: what shares a base overlaps. Views that
+// overlap from different bases are the caller's to avoid.)
+svdq_status check_rope_overlap(const svdq_rope_heads* q, const svdq_rope_heads* k, int64_t T) {
+    for (const svdq_rope_heads* h : {q, k})
+        if (h && h->heads && h->y == h->x &&
+            ((T > 1 && h->y_token_stride != h->token_stride) || (h->heads > 1 && h->y_head_stride != h->head_stride)))
+            return fail(SVDQ_ERR_SHAPE, "%s: in place needs y's strides to be x's", h == q ? "q" : "k");
+    if (k && k->heads && (q->y == k->y || q->y == k->x || k->y == q->x))
+        return fail(SVDQ_ERR_SHAPE, "q's and k's outputs and inputs overlap");
+    return SVDQ_OK;
+}
+
 svdq_status rope_axes_impl(const svdq_rope_heads* q, const svdq_rope_heads* k, int64_t T, int32_t D, int32_t dtype,
                            const void* pos, int32_t pos_dtype, int32_t axes, const double* turns,
                            const int32_t* axis, int32_t pairs, int32_t pairing, int32_t inverse, float eps,
@@ -891,6 +904,7 @@ svdq_status rope_axes_impl(const svdq_rope_heads* q, const svdq_rope_heads* k, i
     if (T * ((heads * D + 511) / 512 + 1) >= ((int64_t)1 << 26))
         return fail(SVDQ_ERR_SHAPE, "T = %lld with %lld heads needs more waves than one launch holds", (long long)T, (long long)heads);
     if (T == 0) { g_last_error.clear(); return SVDQ_OK; }
+    if ((s = check_rope_overlap(q, k, T)) != SVDQ_OK) return s;
     if (pairs > 0 && (!pos || !turns || !axis)) return fail(SVDQ_ERR_NULL, "pos, turns and axis are required");
     if (groups && !offsets) return fail(SVDQ_ERR_NULL, "offsets is required");
     if (offsets && !aligned(offsets, 4)) return fail(SVDQ_ERR_ALIGN, "offsets needs 4-byte alignment");

@@ -605,7 +605,8 @@ svdq_status svdq_linear_fp8_grouped(const void* x, int64_t M, int64_t K, int64_t
  *             t * token_stride + h * head_stride + d), norm [D] of the same
  *             dtype or NULL, y the output with strides of its own; y may be x
  *             with the same strides (in place), other overlaps are not
- *             allowed. x, y and norm 16-byte aligned.
+ *             allowed (SVDQ_ERR_SHAPE where two of them start at one
+ *             address; others are not looked for). x, y and norm 16-byte aligned.
  *  dtype      SVDQ_DT_BF16 or SVDQ_DT_F32
  *  D          head width, a multiple of 8 in [8, 512]
  *  pos        [T][axes] int32 (pos_dtype SVDQ_POS_I32) or fp32 (SVDQ_POS_F32)

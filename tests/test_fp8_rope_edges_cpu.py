@@ -8,7 +8,7 @@ import torch
 
 import bit_quantized_diffusion_svdq_amd as svdq
 from oracle import fp8 as ofp8
-from test_fp8_rope_cpu import ALIGN, C, D, E, NULL, OK, SHAPE, _heads, _prod, lib, valid
+from test_fp8_rope_cpu import A, ALIGN, B, C, D, E, F, NULL, OK, SHAPE, _heads, lib, valid
 
 
 # ---------------------------------------------------------------- offsets that fall
@@ -113,3 +113,22 @@ def test_qkv_block_refuses_norms_elsewhere():
         block(torch.zeros((3, 144), dtype=torch.bfloat16), torch.zeros((3, 2), dtype=torch.int32))
     with pytest.raises(ValueError, match="q_norm"):
         svdq.FusedQKV(NotCalled(), svdq.RopePlan((16, 16), device="cpu"), 2, q_norm=torch.ones(64, dtype=torch.bfloat16)[::2])
+
+
+# ---------------------------------------------------------------- outputs over other tensors
+
+@pytest.mark.parametrize("q,k", [
+    (dict(x=A, y=C), dict(x=C, y=A)),                       # the outputs swapped
+    (dict(x=A, y=B), dict(x=C, y=B)), (dict(x=A, y=C), dict(x=C, y=B)), (dict(x=A, y=B), dict(x=C, y=A)),
+    (dict(x=A, y=A, yts=512), dict(x=C, y=C)), (dict(x=A, y=A, yts=64, yhs=320), dict(x=C, y=C)),
+    (dict(x=A, y=A), dict(x=C, y=C, ts=0)), (dict(x=A, y=A), dict(x=C, y=C, hs=0)),
+])
+def test_rope_axes_rejects_outputs_over_other_tensors(lib, q, k):
+    assert _rope(lib, q=_heads(**q), k=_heads(**k)) == SHAPE and b"" != lib.svdq_last_error()
+
+
+def test_rope_axes_accepts_in_place(lib):
+    valid(_rope(lib, q=_heads(x=A, y=A), k=_heads(x=C, y=C)))
+    valid(_rope(lib, q=_heads(x=A, y=B), k=_heads(x=A, y=F)))                            # one input for both
+    valid(_rope(lib, q=_heads(x=A, y=A, ts=0, hs=0, heads=1), T=1))                      # strides of one element
+    valid(_rope(lib, q=_heads(x=A, y=B), k=_heads(x=A, y=B, heads=0)))
