@@ -42,6 +42,8 @@ def _on(t: torch.Tensor, stream=None):
         return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
+    elif stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
     return torch.cuda.stream(stream)
 
 

@@ -132,3 +132,14 @@ def test_rope_axes_accepts_in_place(lib):
     valid(_rope(lib, q=_heads(x=A, y=B), k=_heads(x=A, y=F)))                            # one input for both
     valid(_rope(lib, q=_heads(x=A, y=A, ts=0, hs=0, heads=1), T=1))                      # strides of one element
     valid(_rope(lib, q=_heads(x=A, y=B), k=_heads(x=A, y=B, heads=0)))
+
+
+# ---------------------------------------------------------------- streams
+
+def test_a_stream_of_another_gpu_is_refused():
+    """Its kernels would run on the GPU that the tensors are not on."""
+    from types import SimpleNamespace
+    from bit_quantized_diffusion_svdq_amd.fp8 import _on
+    t = SimpleNamespace(is_cuda=True, device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="stream is on cuda:0"):
+        _on(t, SimpleNamespace(device=torch.device("cuda", 0)))
