@@ -156,4 +156,6 @@ def quantize_fp8(w: torch.Tensor, bias=None, stream=None) -> dict:
                 pad[:, :N].copy_(wg)
                 wg, ldw = pad, pad.stride(0)
             _lib.svdq_quantize_weight_fp8(wg, K, N, ldw, qw[g] if lead else qw, sw[g] if lead else sw)
+        if bias is not None:
+            bias = bias.contiguous()                             # as the layers take it
     return dict(qw=qw, sw=sw, bias=bias, K=K, N=N)

@@ -1,5 +1,5 @@
 """The 8-bit layers where a call can go wrong: offsets that fall, rows at
-addresses that the kernels cannot read."""
+addresses that the kernels cannot read, biases that are views."""
 import numpy as np
 import pytest
 import torch
@@ -73,3 +73,16 @@ def test_rows_at_any_address(M, K):
             q, s = svdq.quantize_act_fp8(v)
             assert torch.equal(q.view(torch.uint8), want_q.view(torch.uint8)) and torch.equal(s, want_s)
             assert torch.equal(lay(v), want) and torch.equal(grp(v, offs), want_g)
+
+
+def test_quantised_layers_take_any_bias_view():
+    """A bias that is a view of something wider makes a layer that runs."""
+    note("quantize_fp8 with a strided bias")
+    K, N = 144, 72
+    w, b = weights(K, N, 1, groups=2), biases((2, 2 * N), 2)
+    x, offs = acts(9, K, 3), torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda")
+    grp = svdq.Fp8GroupedLinear.from_quantized(svdq.quantize_fp8(w, b[:, ::2]))
+    want = svdq.Fp8GroupedLinear.from_quantized(svdq.quantize_fp8(w, b[:, ::2].contiguous()))(x, offs)
+    assert torch.equal(grp(x, offs), want)
+    lay = svdq.Fp8Linear.from_quantized(svdq.quantize_fp8(w[1], b[1, 1::2]))
+    assert torch.equal(lay(x), svdq.Fp8Linear(lay.qw, lay.sw, b[1, 1::2].contiguous())(x))
