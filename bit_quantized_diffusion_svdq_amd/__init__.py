@@ -16,7 +16,7 @@ from ._lib import (SvdqError, awq_gemv_w4a16, check_device, library_path, load_l
                    svdq_pack_lowrank, svdq_gemm_w4a4_quant_next, svdq_gemm_w4a4_quant_next_workspace_size,
                    w4a4_linear_quant_next, svdq_gemm_mxfp4_quant_next, mxfp4_linear_quant_next,
                    svdq_quantize_act_fp8, svdq_quantize_weight_fp8, svdq_gemm_fp8, svdq_gemm_fp8_grouped,
-                   svdq_linear_fp8, svdq_linear_fp8_grouped, svdq_linear_fp8_workspace_size, svdq_rope_axes,
+                   svdq_gemm_fp8_variant, svdq_linear_fp8, svdq_linear_fp8_grouped, svdq_linear_fp8_workspace_size, svdq_rope_axes,
                    svdq_rope_axes_grouped)
 from .fp8 import Fp8GroupedLinear, Fp8Linear, fp8_grouped_linear, fp8_linear, quantize_act_fp8
 from .offline import quantize_awq, quantize_fp8, quantize_layer
@@ -41,6 +41,6 @@ __all__ = ["SvdqError", "awq_gemv_w4a16", "check_device", "library_path", "load_
            "column_offsets", "column_slice", "projection_weights", "split_columns", "CapturedSequence",
            "save_layer", "load_layer", "read_metadata", "save_awq_layer", "load_awq_layer", "awq_linear",
            "svdq_quantize_act_fp8", "svdq_quantize_weight_fp8", "svdq_gemm_fp8", "svdq_gemm_fp8_grouped",
-           "svdq_linear_fp8", "svdq_linear_fp8_grouped", "svdq_linear_fp8_workspace_size", "svdq_rope_axes",
+           "svdq_linear_fp8", "svdq_linear_fp8_grouped", "svdq_linear_fp8_workspace_size", "svdq_gemm_fp8_variant", "svdq_rope_axes",
            "svdq_rope_axes_grouped", "Fp8GroupedLinear", "Fp8Linear", "fp8_grouped_linear", "fp8_linear",
            "quantize_act_fp8", "quantize_fp8", "RopePlan", "rope_axes", "FusedQKV", "save_fp8_layer", "load_fp8_layer"]

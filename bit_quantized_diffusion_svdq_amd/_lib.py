@@ -60,6 +60,7 @@ _SIGS = {
     "svdq_quantize_weight_fp8": [_P, _I64, _I64, _I64, _P, _P, _P],
     "svdq_gemm_fp8": [_P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _I64, _P],
     "svdq_gemm_fp8_grouped": [_P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _P, _I32, _I64, _P],
+    "svdq_gemm_fp8_variant": [_I64, _I64, _I64, _I32, _I32, _I32, _P],
     "svdq_linear_fp8_workspace_size": [_I64, _I64, _P],
     "svdq_linear_fp8": [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _I64, _P, _I64, _P],
     "svdq_linear_fp8_grouped": [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _P, _I32, _I64, _P, _I64, _P],
@@ -323,6 +324,12 @@ def svdq_gemm_fp8_grouped(qx, sx, M, K, qw, sw, N, offsets, groups, bias, act, y
     _check(load_library().svdq_gemm_fp8_grouped(_ptr(qx), _ptr(sx), M, K, _ptr(qw), _ptr(sw), N, _ptr(offsets), groups,
                                                 _ptr(bias), act, _ptr(y), y_dtype, ldy, _stream(stream)),
            "svdq_gemm_fp8_grouped")
+
+
+def svdq_gemm_fp8_variant(M, K, N, groups, y_dtype, cus) -> int:
+    out = ctypes.c_int32(-1)
+    _check(load_library().svdq_gemm_fp8_variant(M, K, N, groups, y_dtype, cus, ctypes.byref(out)), "svdq_gemm_fp8_variant")
+    return out.value
 
 
 def svdq_linear_fp8_workspace_size(M, K) -> int:

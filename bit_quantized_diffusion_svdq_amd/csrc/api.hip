@@ -59,6 +59,7 @@ hipError_t launch_quant_act_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t
 hipError_t launch_quant_weight_fp8(const uint16_t* w, int64_t K, int64_t N, int64_t ldw, uint8_t* qw, float* sw,
                                    hipStream_t stream);
 bool gemm_fp8_fits(int64_t M, int64_t N, int E);
+int gemm_fp8_variant(int64_t M, int64_t K, int64_t N, int groups, int y_f32, int cus);
 hipError_t launch_gemm_fp8(const uint8_t* qx, const float* sx, int64_t M, int64_t K, const uint8_t* qw, const float* sw,
                            int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
                            int64_t ldy, int cus, hipStream_t stream);
@@ -758,21 +759,28 @@ svdq_status check_k_fp8(int64_t K) {
     return SVDQ_OK;
 }
 
-svdq_status gemm_fp8_impl(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
-                          int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act, void* y,
-                          int32_t y_dtype, int64_t ldy, void* stream, const char* what) {
+// the product's sizes, host only
+svdq_status check_gemm_fp8_sizes(int64_t M, int64_t K, int64_t N, int32_t groups, int32_t y_dtype) {
     svdq_status s;
     if (M < 0 || M >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "M = %lld must be in [0, 2^31)", (long long)M);
     if ((s = check_k_fp8(K)) != SVDQ_OK) return s;
     if (N <= 0 || N >= (int64_t)1 << 30) return fail(SVDQ_ERR_SHAPE, "N = %lld must be in [1, 2^30)", (long long)N);
     if (groups < 0 || groups > 65536) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
-    if (ldy < N) return fail(SVDQ_ERR_SHAPE, "ldy = %lld < N = %lld", (long long)ldy, (long long)N);
-    if (ldy >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "ldy = %lld must be below 2^31", (long long)ldy);
-    if ((s = check_act(act)) != SVDQ_OK) return s;
     if (y_dtype != SVDQ_DT_BF16 && y_dtype != SVDQ_DT_F32)
         return fail(SVDQ_ERR_UNSUPPORTED, "output dtype %d is not supported", y_dtype);
     if (!gemm_fp8_fits(M, N, groups))
         return fail(SVDQ_ERR_SHAPE, "M = %lld x N = %lld needs more tiles than one launch holds", (long long)M, (long long)N);
+    return SVDQ_OK;
+}
+
+svdq_status gemm_fp8_impl(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
+                          int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act, void* y,
+                          int32_t y_dtype, int64_t ldy, void* stream, const char* what) {
+    svdq_status s;
+    if ((s = check_gemm_fp8_sizes(M, K, N, groups, y_dtype)) != SVDQ_OK) return s;
+    if (ldy < N) return fail(SVDQ_ERR_SHAPE, "ldy = %lld < N = %lld", (long long)ldy, (long long)N);
+    if (ldy >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "ldy = %lld must be below 2^31", (long long)ldy);
+    if ((s = check_act(act)) != SVDQ_OK) return s;
     if (M == 0) { g_last_error.clear(); return SVDQ_OK; }
     if (!qx || !sx || !qw || !sw || !y || (groups && !offsets))
         return fail(SVDQ_ERR_NULL, "qx, sx, qw, sw and y%s are required", groups ? ", offsets" : "");
@@ -994,6 +1002,17 @@ svdq_status svdq_gemm_fp8_grouped(const void* qx, const float* sx, int64_t M, in
     if (groups < 1) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
     return gemm_fp8_impl(qx, sx, M, K, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, stream,
                          "svdq_gemm_fp8_grouped launch");
+}
+
+svdq_status svdq_gemm_fp8_variant(int64_t M, int64_t K, int64_t N, int32_t groups, int32_t y_dtype, int32_t cus,
+                                  int32_t* variant) {
+    svdq_status s;
+    if ((s = check_gemm_fp8_sizes(M, K, N, groups, y_dtype)) != SVDQ_OK) return s;
+    if (M == 0 || cus < 1) return fail(SVDQ_ERR_SHAPE, "M = %lld and cus = %d must be positive", (long long)M, cus);
+    if (!variant) return fail(SVDQ_ERR_NULL, "variant is required");
+    *variant = gemm_fp8_variant(M, K, N, groups, y_dtype == SVDQ_DT_F32, cus);
+    g_last_error.clear();
+    return SVDQ_OK;
 }
 
 svdq_status svdq_linear_fp8_workspace_size(int64_t M, int64_t K, int64_t* bytes) {

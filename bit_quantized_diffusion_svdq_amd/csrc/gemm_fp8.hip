@@ -789,17 +789,23 @@ bool fits(const Variant& v, const Args& a) {
     return tm * tn * 512.0 < 4294967296.0;
 }
 
-template <int PREC, bool GROUPED>
-bool launch_variant(const Args& a, int cus, hipStream_t stream) {
+// The variant with the least estimate, or -1
+int pick_variant(const Args& a, int prec, int cus) {
     int best = -1;
     double least = 0.0;
     for (int i = 0; i < (int)(sizeof kVariants / sizeof kVariants[0]); ++i) {
         // fp32 outputs have the two tile sizes whose operands fit the registers when widened
-        if (PREC == 1 && i < 9 && i != 5 && i != 8) continue;
+        if (prec == 1 && i < 9 && i != 5 && i != 8) continue;
         if (!fits(kVariants[i], a)) continue;
         const double t = estimate(kVariants[i], a, cus);
         if (best < 0 || t < least) best = i, least = t;
     }
+    return best;
+}
+
+template <int PREC, bool GROUPED>
+bool launch_variant(const Args& a, int cus, hipStream_t stream) {
+    const int best = pick_variant(a, PREC, cus);
     switch (best) {
         case 0: if constexpr (PREC == 0) launch_tiles<Cfg<8, 4, 2, 4, 2, 0, 3, 2>, GROUPED>(a, stream); break;
         case 1: if constexpr (PREC == 0) launch_tiles<Cfg<7, 4, 2, 4, 2, 0, 3, 2>, GROUPED>(a, stream); break;
@@ -827,6 +833,19 @@ bool gemm_fp8_fits(int64_t M, int64_t N, int E) {
     a.N = (int)N;
     a.E = E;
     return fits(kVariants[5], a);
+}
+
+// what a product of these sizes runs
+int gemm_fp8_variant(int64_t M, int64_t K, int64_t N, int groups, int y_f32, int cus) {
+    static const int32_t ragged = 0;
+    Args a{};
+    a.M = M;
+    a.K = (int)K;
+    a.N = (int)N;
+    a.E = groups;
+    a.offs = groups ? &ragged : nullptr;                 // (only asked whether there are any)
+    a.y_f32 = y_f32;
+    return pick_variant(a, y_f32 ? 1 : 0, cus);
 }
 
 hipError_t launch_gemm_fp8(const uint8_t* qx, const float* sx, int64_t M, int64_t K, const uint8_t* qw, const float* sw,

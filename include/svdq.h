@@ -570,7 +570,15 @@ svdq_status svdq_quantize_weight_fp8(const void* w, int64_t K, int64_t N, int64_
  * svdq_linear_fp8_grouped -- the same with a weight per group of rows
  *   (svdq_gemm_fp8_grouped's offsets, arrays and untouched rows; the few
  *   tokens of a step on their experts take one launch).
+ *
+ * svdq_gemm_fp8_variant -- test hook, host only: the index of the kernel that a
+ *   product of these sizes runs on a device with `cus` compute units (groups
+ *   0: the dense form): 0 to 8 the tiles 256 x 256, 224 x 256, 192 x 256, 160
+ *   x 256, 256 x 128, 128 x 128 in four waves and in eight, 64 x 128, 64 x 64;
+ *   9 to 11 the few-rows kernels 16 x 16, 16 x 32, 32 x 32. M and cus >= 1.
  */
+svdq_status svdq_gemm_fp8_variant(int64_t M, int64_t K, int64_t N, int32_t groups, int32_t y_dtype, int32_t cus,
+                                  int32_t* variant);
 svdq_status svdq_gemm_fp8(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
                           int64_t N, const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
                           void* stream);

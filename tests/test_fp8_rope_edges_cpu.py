@@ -143,3 +143,30 @@ def test_a_stream_of_another_gpu_is_refused():
     t = SimpleNamespace(is_cuda=True, device=torch.device("cuda", 1))
     with pytest.raises(ValueError, match="stream is on cuda:0"):
         _on(t, SimpleNamespace(device=torch.device("cuda", 0)))
+
+
+# ---------------------------------------------------------------- which kernel a product runs
+
+def _geometric(lo, hi, n):
+    return sorted({int(round(lo * (hi / lo) ** (i / (n - 1)))) for i in range(n)})
+
+
+def test_every_kernel_that_a_product_can_run_has_a_gpu_test():
+    """Over sizes of one row to tens of thousands: no kernel outside the GPU
+    tests' list, and every size of the list still takes its kernel."""
+    from test_gpu_fp8_variants import VARIANTS
+    for (index, f32, groups), (M, K, N) in VARIANTS.items():
+        assert svdq.svdq_gemm_fp8_variant(M, K, N, groups, f32, 256) == index
+    seen = {(svdq.svdq_gemm_fp8_variant(M, max(16, K // 16 * 16), N, E, f32, 256), f32, E > 0)
+            for M in _geometric(1, 70000, 25) for K in _geometric(16, 24576, 14) for N in _geometric(1, 32768, 16)
+            for E in (0, 1, 3, 8, 33, 256) for f32 in (0, 1)}
+    assert seen == {(index, f32, groups > 0) for index, f32, groups in VARIANTS}
+
+
+@pytest.mark.parametrize("a", [(0, 16, 1, 0, 0, 256), (1, 24, 1, 0, 0, 256), (1, 16, 0, 0, 0, 256), (1, 16, 1, -1, 0, 256),
+                               (1, 16, 1, 65537, 0, 256), (1, 16, 1, 0, 2, 256), (1, 16, 1, 0, 0, 0), (1 << 31, 16, 1, 0, 0, 256),
+                               (1 << 30, 16, 1 << 20, 0, 0, 256)])
+def test_variant_refuses(lib, a):
+    with pytest.raises(svdq.SvdqError):
+        svdq.svdq_gemm_fp8_variant(*a)
+    assert lib.svdq_gemm_fp8_variant(1, 16, 1, 0, 0, 256, None) == NULL
