@@ -1,5 +1,6 @@
 """Rotary positions where a call can go wrong: values that are not finite
-beside channels that do not turn, tokens of no group."""
+beside channels that do not turn, tokens of no group, many tokens of every
+type and pairing."""
 import numpy as np
 import pytest
 import torch
@@ -90,3 +91,44 @@ def test_qkv_block_leaves_rows_of_no_group():
             r = slice(offs[0], offs[-1])
             assert torch.equal(q[r], rq[r]) and torch.equal(k[r], rk[r]) and torch.equal(v[r], wv[r])
             assert (y[:offs[0]] == -3.0).all() and (y[offs[-1]:] == -3.0).all()
+
+
+# More than two tokens a CU run other instances (four loads in flight) than fewer do, and up to
+# about 3000 of them several waves share a token: 1024 tokens of 24 + 24 heads of 128 are 6 + 6
+# loads in three shares, of which the second holds the last queries and the first keys.
+MANY = [
+    # T, Hq, Hk, D, dims, pairing, norm, dtype
+    (600, 3, 1, 64, (16, 24, 24), "interleaved", False, torch.float32),
+    (600, 3, 1, 64, (16, 24, 24), "half", True, torch.float32),
+    (700, 5, 2, 72, (24, 16, 24), "interleaved", True, torch.float32),
+    (700, 5, 2, 72, (24, 16, 24), "half", True, torch.bfloat16),
+    (530, 24, 24, 128, (32, 32), "half", True, torch.float32),
+    (530, 24, 24, 128, (32, 32), "interleaved", True, torch.float32),
+    (600, 4, 3, 128, (32, 32), "half", False, torch.bfloat16),
+    (600, 4, 3, 128, (32, 32), "interleaved", True, torch.bfloat16),
+    (1024, 24, 24, 128, (16, 56, 56), "interleaved", True, torch.bfloat16),
+    (1024, 24, 24, 128, (16, 56, 56), "half", True, torch.bfloat16),
+    (1024, 24, 8, 128, (16, 56, 56), "half", True, torch.float32),
+    (1024, 21, 27, 128, (16, 56, 56), "interleaved", False, torch.float32),
+    (3100, 7, 7, 128, (16, 56, 56), "half", True, torch.bfloat16),
+    (3100, 6, 2, 256, (64, 96, 96), "interleaved", True, torch.float32),
+    (520, 2, 1, 512, (128, 128, 128, 128), "half", True, torch.float32),
+    (2000, 40, 1, 8, (8,), "interleaved", True, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("T,hq,hk,D,dims,pairing,norm,dt", MANY)
+def test_many_tokens(T, hq, hk, D, dims, pairing, norm, dt):
+    note(f"rope_axes {T} x {hq}+{hk} x {D} {dims} {pairing} norm={norm} {dt}")
+    q, k, pos = heads(T, hq, D, 1, dt), heads(T, hk, D, 2, dt), positions(T, len(dims), 3)
+    qn = (1 + 0.3 * heads(1, 1, D, 4, torch.float32)).flatten().to(dt) if norm else None
+    kn = (1 + 0.3 * heads(1, 1, D, 5, torch.float32)).flatten().to(dt) if norm else None
+    plan = svdq.RopePlan(dims, head_dim=D, pairing=pairing)
+    qo, ko = svdq.rope_axes(q, k, pos, plan, q_norm=qn, k_norm=kn)
+    check(qo, q, pos, dims, pairing, qn)
+    check(ko, k, pos, dims, pairing, kn)
+    qi, ki = q.clone(), k.clone()
+    svdq.rope_axes(qi, ki, pos, plan, q_norm=qn, k_norm=kn, q_out=qi, k_out=ki)
+    assert torch.equal(qi, qo) and torch.equal(ki, ko)
+    back = svdq.rope_axes(q, None, pos, plan, q_norm=qn, inverse=True)
+    check(back, q, pos, dims, pairing, qn, inverse=True)
