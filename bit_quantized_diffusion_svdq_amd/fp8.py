@@ -150,7 +150,14 @@ def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfl
     """act(sum_b sx sw P_b + bias) for already quantised activations: qx E4M3
     [M, K], sx fp32 [ceil(K/128), M] (quantize_act_fp8), qw E4M3 [N, K], sw
     fp32 [ceil(N/128), ceil(K/128)], bias bf16 [N] or None -> y [M, N] (bf16
-    or fp32; rows of a given y may be strided)."""
+    or fp32; rows of a given y may be strided; y must not overlap the inputs).
+
+    The output type also chooses the sums. bf16: the E4M3 matrix instructions,
+    which drop what falls 13 bits below the largest of each 8 products, 1.4e-5
+    to 3.1e-5 of the outputs' rms (a fiftieth of their rounding; outputs that
+    cancel to a twentieth of the others lose as much as to the rounding).
+    fp32: every product and sum in fp32, at half the matrix rate; round its
+    result where bf16 outputs of such sums are wanted."""
     M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, 0)
     with _on(qx, stream):
         y, ldy = _output(y, M, N, out_dtype, qx)
@@ -175,7 +182,7 @@ def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", ou
     values are not reported: they are clamped, and one that falls counts as
     the largest before it). Rows of
     no group (before offsets[0], from offsets[-1] on) are left as they are in
-    a given y and are unspecified in a new one."""
+    a given y and are unspecified in a new one. The sums are fp8_linear's."""
     groups = _groups(offsets)
     M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, groups)
     if offsets.device != qx.device:
@@ -266,7 +273,8 @@ class Fp8Linear:
         """Y [M, N] for bf16 activations x [M, K]: the activation pass, then
         the product, in one call on one stream; in one launch for few rows (M
         <= 16 and M * ceil(K / 128) <= 256: single tokens, pooled
-        conditioning)."""
+        conditioning). bf16 outputs are summed by the E4M3 matrix
+        instructions, fp32 outputs in fp32 (fp8_linear gives the difference)."""
         if x.dim() != 2 or x.shape[1] != self.K:
             raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
         with _on(x, stream):                     # (the codes are freed on the stream that reads them)
@@ -304,8 +312,8 @@ class Fp8GroupedLinear:
     def __call__(self, x: torch.Tensor, offsets: torch.Tensor, act: str = "none", out_dtype=torch.bfloat16, y=None,
                  stream=None) -> torch.Tensor:
         """Y [M, N] for bf16 activations x [M, K] sorted by group
-        (fp8_grouped_linear's offsets); one call, and one launch for few
-        rows, as Fp8Linear."""
+        (fp8_grouped_linear's offsets); one call, one launch for few rows,
+        and the sums, as Fp8Linear."""
         if x.dim() != 2 or x.shape[1] != self.K:
             raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
         if _groups(offsets) != self.groups:

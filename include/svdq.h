@@ -537,12 +537,15 @@ svdq_status svdq_quantize_weight_fp8(const void* w, int64_t K, int64_t N, int64_
  *   y_dtype, ldy >= N (rows whose ldy is a multiple of 8 and whose base is
  *   16-byte aligned are written 16 bytes at a time, others by the element).
  *   One fp32 FMA per block joins its product to the fp32 result, and the
- *   output is rounded once. fp32 outputs: products and sums of a block keep
- *   fp32. bf16 outputs: the E4M3 matrix instructions add 8 consecutive
- *   channels' products at the exponent of the largest and drop what falls
- *   more than 13 bits below it (at most 7 * 2^-13 of the largest of each 8;
- *   about 3e-5 of the result for random operands), the rest is fp32. sx * sw has to stay finite
- *   in fp32. qx, qw 16-byte aligned, sx, sw 4, bias 2, y by its element.
+ *   output is rounded once. y_dtype also chooses the sums. fp32 outputs:
+ *   products and sums of a block keep fp32, at half the matrix rate. bf16
+ *   outputs: the E4M3 matrix instructions add 8 consecutive channels' products
+ *   at the exponent of the largest and drop what falls more than 13 bits below
+ *   it (at most 7 * 2^-13 of the largest of each 8; 1.4e-5 to 3.1e-5 of the
+ *   outputs' rms, measured: a fiftieth of their rounding, but as much as the
+ *   rounding itself for outputs that cancel to a twentieth of the others), the
+ *   rest is fp32. Who needs more asks for fp32 outputs. sx * sw has to stay
+ *   finite in fp32. y must not overlap the inputs. qx, qw 16-byte aligned, sx, sw 4, bias 2, y by its element.
  *   K < 2^22, ldy < 2^31; the grid of 128 x 128 tiles has to fit a launch
  *   ((M / 128 + 1 + groups) (N / 128 + 1) < 2^23).
  *
