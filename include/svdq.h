@@ -147,10 +147,13 @@ const char* svdq_status_string(svdq_status s);
 /* Detail of the last failure on the calling thread ("" if none). */
 const char* svdq_last_error(void);
 
-/* Library version: format version * 100 + revision (404: format 4, revision 4,
- * which adds awq_quantize_weight; revision 3 added
- * svdq_quantize_residual_mxfp4, revision 2 svdq_gemm_mxfp4_quant_next; the
- * formats are unchanged). */
+/* Version of the 4-bit layers' part of the library: format version * 100 +
+ * revision (404: format 4, revision 4, which adds awq_quantize_weight;
+ * revision 3 added svdq_quantize_residual_mxfp4, revision 2
+ * svdq_gemm_mxfp4_quant_next; the formats are unchanged). The 8-bit layers and
+ * the rotary positions (svdq_*_fp8*, svdq_rope_axes*) are not counted in it:
+ * they have arrays and a package format of their own, and a caller that may
+ * meet a library without them looks for the symbol. */
 int svdq_version(void);
 
 /*
