@@ -168,18 +168,23 @@ class FusedQKV:
         """What the rotation would refuse, before the projection writes anything."""
         if x.dim() != 2:
             raise ValueError(f"x must be [M, {self.layer.K}], got {tuple(x.shape)}")
-        M, N, dev, plan = x.shape[0], self.layer.N, x.device, self.plan
+        M, dev, plan = x.shape[0], x.device, self.plan
         if not ((pos.dtype is torch.int32 or pos.dtype is torch.float32) and pos.shape == (M, plan.axes)
                 and pos.is_contiguous()):
             raise ValueError(f"pos must be contiguous int32 or fp32 [{M}, {plan.axes}], got {tuple(pos.shape)} {pos.dtype}")
         if y is not None:
+            N = self.layer.N
             if not (y.dtype is torch.bfloat16 and y.shape == (M, N) and y.stride(1) == 1
                     and (M <= 1 or (y.stride(0) >= N and y.stride(0) % 8 == 0)) and y.data_ptr() % 16 == 0):
                 raise ValueError(f"y must be bf16 [{M}, {N}] with contiguous columns, a row stride that is a multiple of 8 "
                                  f"and an address that is one of 16 bytes, got {tuple(y.shape)} {y.dtype}, strides {y.stride()}")
-        for name, t in (("pos", pos), ("y", y), ("q_norm", self.q_norm), ("k_norm", self.k_norm), ("the plan", plan.turns)):
-            if t is not None and t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, expected {dev}")
+            if y.device != dev:
+                raise ValueError(f"y is on {y.device}, expected {dev}")
+        if pos.device != dev or plan.turns.device != dev:
+            raise ValueError(f"pos is on {pos.device}, the plan on {plan.turns.device}, expected {dev}")
+        for name, w in (("q_norm", self.q_norm), ("k_norm", self.k_norm)):
+            if w is not None and w.device != dev:
+                raise ValueError(f"{name} is on {w.device}, expected {dev}")
 
     def __call__(self, x: torch.Tensor, pos: torch.Tensor, offsets=None, y=None, stream=None):
         """x bf16 [M, K], pos [M, axes]; offsets for a grouped layer (rows

@@ -12,12 +12,12 @@ struct RopeArgs {
     const void* pos;
     const double* turns;            // [pairs] turns per unit of position
     const int* axis;                // [pairs]
-    const int* offs;                // rows in groups: [groups + 1] row offsets, else NULL
-    int groups;
     int64_t T;
     int D, pairs, axes, pos_f32, inverse;
     float eps;
     int lp, chunk;                  // lanes per head (a power of two), loads of heads per wave
+    const int* offs;                // rows in groups: [groups + 1] row offsets, else NULL
+    int groups;
 };
 
 hipError_t launch_rope_axes(RopeArgs a, int f32, int half, int cus, hipStream_t stream);

@@ -21,8 +21,10 @@
 // norm's sum of squares is a butterfly over a head's lanes without LDS. The
 // vector work counts beside the memory's: folding the weights into the
 // rotation, uniform sides and the hardware's reciprocal root took 4608 tokens
-// of 24 + 24 heads of 128 (normed) from 47.6 to 27.1 us, 4.2 TB/s; 32761 of
-// 16 + 4 without a norm run in 66.8 us, 5.0 TB/s (a plain copy: 5.5).
+// of 24 + 24 heads of 128 (normed) from 47.6 to 27.1 us, loads ahead of the
+// angles and less work a pair to 21.1, 5.4 TB/s; 32761 of 16 + 4 without a norm
+// run in 64.3 us, 5.2 TB/s (fp32: 41.8 and 127.7, 5.4 and 5.3; a plain copy: 5.5).
+// All figures of this file are kernels in a graph.
 #include "lanes.h"
 #include "rope.h"
 
@@ -214,9 +216,9 @@ static hipError_t launch(RopeArgs a, int f32, int half, int cus, hipStream_t str
     const int per = 64 / a.lp, loads = (a.heads[0] + per - 1) / per + (a.heads[1] + per - 1) / per;
     // A wave takes all of its token's heads where the tokens fill the chip (12
     // waves a CU), else a share of them, U loads at the least, and works the
-    // angles out again (1024 tokens of 24 + 24 heads of 128 take 9.9 us in two
-    // or three waves a token and 11.7 in one, 32761 of 16 + 4 72.7 in two and
-    // 66.8 in one).
+    // angles out again (1024 tokens of 24 + 24 heads of 128 take 7.3 us in three
+    // waves a token, 7.9 in two, 10.7 in one; 32761 of 16 + 4 69 in two and 64.3 in
+    // one).
     int64_t chunks = ((int64_t)cus * 12 + a.T - 1) / a.T;
     if (chunks > (loads + U - 1) / U) chunks = (loads + U - 1) / U;
     a.chunk = (int)((loads + chunks - 1) / chunks);
@@ -233,8 +235,8 @@ static hipError_t launch(RopeArgs a, int f32, int half, int cus, hipStream_t str
 }
 
 hipError_t launch_rope_axes(RopeArgs a, int f32, int half, int cus, hipStream_t stream) {
-    // Few tokens: one load a wave at a time, more waves (24 + 24 heads of 128: 1 token 3.2 us, 4.4
-    // with four loads; 77 tokens 3.8, 5.6; 512 6.4, 7.1). More tokens: four loads in flight (1024
-    // tokens 8.8, 9.4 with one; 4608 of 32 + 8 heads, half-split 22.3, 25.3).
+    // Few tokens: one load a wave at a time, more waves (24 + 24 heads of 128: 1 token 3.0 us, 4.5
+    // with four loads; 77 tokens 3.5, 5.3; 512 5.5, 6.1). More tokens: four loads in flight (1024
+    // tokens 7.3, 8.1 with one; 4608 of 32 + 8 heads, half-split 17.1, 18.6).
     return a.T <= 2 * (int64_t)cus ? launch<1>(a, f32, half, cus, stream) : launch<4>(a, f32, half, cus, stream);
 }

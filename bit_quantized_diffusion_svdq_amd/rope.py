@@ -113,7 +113,7 @@ def rope_axes(q, k, pos, plan: RopePlan, q_norm=None, k_norm=None, eps: float = 
         raise ValueError(f"q must be bf16 or fp32, got {dt}")
     if hq < 1:
         raise ValueError("q must have at least one head")
-    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+    if (q.requires_grad or (k is not None and k.requires_grad)) and torch.is_grad_enabled():
         raise ValueError("q or k requires a gradient, which this call does not record: call it under torch.no_grad() or "
                          "on detached tensors (inverse=True turns a gradient back)")
     hk = 0
@@ -145,12 +145,16 @@ def rope_axes(q, k, pos, plan: RopePlan, q_norm=None, k_norm=None, eps: float = 
         ks = None
         if k is not None:
             k_out, ks = _side(k, k_out, k_norm, T, hk, D)
-        args = (ctypes.addressof(qs), None if ks is None else ctypes.addressof(ks), T, D, dt is torch.float32,
-                pos.data_ptr(), f32_pos, plan.axes, plan.turns.data_ptr(), plan.axis.data_ptr(), plan.pairs,
-                PAIRING[plan.pairing], bool(inverse), eps)
-        if groups:
-            _check(load_library().svdq_rope_axes_grouped(*args, offsets.data_ptr(), groups, _stream_now()),
-                   "svdq_rope_axes_grouped")
+        q_at, k_at = ctypes.addressof(qs), None if ks is None else ctypes.addressof(ks)
+        if not groups:
+            _check(load_library().svdq_rope_axes(q_at, k_at, T, D, dt is torch.float32, pos.data_ptr(), f32_pos,
+                                                 plan.axes, plan.turns.data_ptr(), plan.axis.data_ptr(), plan.pairs,
+                                                 PAIRING[plan.pairing], bool(inverse), eps, _stream_now()),
+                   "svdq_rope_axes")
         else:
-            _check(load_library().svdq_rope_axes(*args, _stream_now()), "svdq_rope_axes")
+            _check(load_library().svdq_rope_axes_grouped(q_at, k_at, T, D, dt is torch.float32, pos.data_ptr(), f32_pos,
+                                                         plan.axes, plan.turns.data_ptr(), plan.axis.data_ptr(),
+                                                         plan.pairs, PAIRING[plan.pairing], bool(inverse), eps,
+                                                         offsets.data_ptr(), groups, _stream_now()),
+                   "svdq_rope_axes_grouped")
     return q_out if k is None else (q_out, k_out)
