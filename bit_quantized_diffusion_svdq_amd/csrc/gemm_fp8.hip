@@ -435,8 +435,8 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
     constexpr int TURN = TM % 2 && S % 2 ? 2 * S : S;              // (the registers' roles repeat after these)
     if ((GROUPED || BM <= 128) && wm * TM * 16 >= rr.rows) {
         // A wave without rows brings its part of the operands and meets the others,
-        // which then have the SIMD for themselves: 8200 rows of 16 groups x 4096 x
-        // 4096 take 157 us (161), 16 x 4096 x 12288 12.8 (13.2). (The large dense
+        // which then have the SIMD for themselves: 8200 rows of 16 ragged groups x
+        // 4096 x 4096 with GELU take 165.5 us (168.6), 16 x 4096 x 12288 12.8 (13.2). (The large dense
         // tiles, with one such row of tiles at most, would lose 1 % to the branch.)
         for (int kb = 0; kb < KB; kb += TURN) {
 #pragma unroll
@@ -725,7 +725,8 @@ void launch_layer(const Args& a, int cus, hipStream_t stream) {
 //    4096 x 4096 x 8192 takes 121 us with 256 x 256, 132 with 192 x 256, 143
 //    with 128 x 128 (two a CU), 184 with 64 x 128, 223 with 64 x 64. Which one
 //    wins is decided by how its tiles fill rounds of the CUs: 4608 x 12288 x 4096
-//    takes 211 us with 160 x 256 (1.8 rounds) and 272 with 256 x 256 (1.1),
+//    takes 211 us with 160 x 256 (1.8 rounds; 211 to 228 from box to box) and
+//    272 with 256 x 256 (1.1),
 //    4608 x 4096 x 12288 204 with 224 x 256 (3.9 rounds) and 233 with 160 x
 //    256. Where the tiles do not fill the CUs once, memory latency counts, and
 //    the small ones keep three or four slots: 256 x 4096 x 4096 takes 11.6 with
@@ -741,9 +742,11 @@ void launch_layer(const Args& a, int cus, hipStream_t stream) {
 //    (19.4 with 64 x 128), 16 x 1536 x 6144 6.6 with 16 columns and 5.1 with 32,
 //    64 x 4096 x 12288 26 (15 in tiles); 48 rows of 32 groups x 2048 x 4096 37
 //    with 32 columns, 43 in tiles.
-// Over 500 sizes of 1 to 64 rows and 435 of 77 to 4608 the variant it picks is
-// half a per cent slower than the best one on the average, over 500 grouped
-// ones (half to 2300 rows a group, ragged) 3.5: it does not know the groups' sizes.
+// Measured sizes and how far the variant it picks is behind the best one: 648 of
+// 1 to 64 rows 1.3 % on the average, 9 or more in one of 20, 23 at the worst; 467
+// of 77 to 4608 rows 0.6, 4, 22; 810 with fp32 outputs 2.2, 13, 68; 532 grouped
+// ones (half to 2300 rows a group, ragged) 4.1, 20, 46: it does not know the
+// groups' sizes.
 struct Variant {
     int rows, cols, few;             // outputs per workgroup; few: the few-rows kernel
     int per_cu, trip;                // workgroups on a CU; K blocks per trip of a few-rows workgroup
