@@ -787,6 +787,7 @@ svdq_status gemm_fp8_impl(const void* qx, const float* sx, int64_t M, int64_t K,
     if (!aligned(qx, 16) || !aligned(qw, 16) || !aligned(sx, 4) || !aligned(sw, 4) || (bias && !aligned(bias, 2)) ||
         !aligned(y, y_dtype == SVDQ_DT_F32 ? 4 : 2) || (offsets && !aligned(offsets, 4)))
         return fail(SVDQ_ERR_ALIGN, "qx, qw need 16-byte alignment, sx, sw, offsets 4, bias 2, y its element's");
+    if (y == qx || y == qw) return fail(SVDQ_ERR_SHAPE, "y overlaps an input");
     int cus = 0;
     if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
     return launched(launch_gemm_fp8((const uint8_t*)qx, sx, M, K, (const uint8_t*)qw, sw, N, offsets, groups,
@@ -837,6 +838,8 @@ svdq_status linear_fp8_impl(const void* x, int64_t M, int64_t K, int64_t ldx, co
     if (!aligned(x, 16) || !aligned(qw, 16) || !aligned(sw, 4) || (bias && !aligned(bias, 2)) ||
         !aligned(y, y_dtype == SVDQ_DT_F32 ? 4 : 2) || (offsets && !aligned(offsets, 4)) || (need && !aligned(ws, 16)))
         return fail(SVDQ_ERR_ALIGN, "x, qw, workspace need 16-byte alignment, sw, offsets 4, bias 2, y its element's");
+    if (y == qw || (need ? y == ws || x == ws : y == x))
+        return fail(SVDQ_ERR_SHAPE, need ? "y, x and the workspace overlap" : "y overlaps x (few rows)");
     int cus = 0;
     if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
     if (!need)
@@ -967,6 +970,7 @@ svdq_status svdq_quantize_act_fp8(const void* x, int64_t M, int64_t K, int64_t l
     if (!x || !qx || !sx) return fail(SVDQ_ERR_NULL, "x, qx and sx are required");
     if (!aligned(x, 16) || !aligned(qx, 16) || !aligned(sx, 4))
         return fail(SVDQ_ERR_ALIGN, "x, qx need 16-byte alignment, sx 4");
+    if (qx == x || sx == x || (const void*)sx == qx) return fail(SVDQ_ERR_SHAPE, "x, qx and sx overlap");
     int cus = 0;
     if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
     return launched(launch_quant_act_fp8((const uint16_t*)x, M, K, ldx, (uint8_t*)qx, sx, cus, (hipStream_t)stream),
@@ -983,6 +987,7 @@ svdq_status svdq_quantize_weight_fp8(const void* w, int64_t K, int64_t N, int64_
     if (!w || !qw || !sw) return fail(SVDQ_ERR_NULL, "w, qw and sw are required");
     if (!aligned(w, 16) || !aligned(qw, 16) || !aligned(sw, 4))
         return fail(SVDQ_ERR_ALIGN, "w, qw need 16-byte alignment, sw 4");
+    if (qw == w || sw == w || (const void*)sw == qw) return fail(SVDQ_ERR_SHAPE, "w, qw and sw overlap");
     if ((s = check_current_device()) != SVDQ_OK) return s;
     return launched(launch_quant_weight_fp8((const uint16_t*)w, K, N, ldw, (uint8_t*)qw, sw, (hipStream_t)stream),
                     "svdq_quantize_weight_fp8 launch");

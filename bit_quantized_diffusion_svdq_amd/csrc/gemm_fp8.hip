@@ -725,7 +725,7 @@ void launch_layer(const Args& a, int cus, hipStream_t stream) {
 //    4096 x 4096 x 8192 takes 121 us with 256 x 256, 132 with 192 x 256, 143
 //    with 128 x 128 (two a CU), 184 with 64 x 128, 223 with 64 x 64. Which one
 //    wins is decided by how its tiles fill rounds of the CUs: 4608 x 12288 x 4096
-//    takes 211 us with 160 x 256 (1.8 rounds; 211 to 228 from box to box) and
+//    takes 211 us with 160 x 256 (1.8 rounds; 211 to 228 from run to run) and
 //    272 with 256 x 256 (1.1),
 //    4608 x 4096 x 12288 204 with 224 x 256 (3.9 rounds) and 233 with 160 x
 //    256. Where the tiles do not fill the CUs once, memory latency counts, and

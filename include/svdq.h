@@ -529,6 +529,10 @@ svdq_status svdq_pack_lowrank(const void* l1, const void* l2, int64_t K, int64_t
  * svdq_quantize_weight_fp8: w bf16 [K][ldw] (row k = input channel, N <= ldw,
  * ldw % 8 == 0, 16-byte aligned) -> qw [N][K] (16-byte aligned), sw, by the
  * same rule per 128 x 128 block. N any size. Offline work.
+ *
+ * Outputs must not overlap inputs or each other, here and below, but where an
+ * entry says so (SVDQ_ERR_SHAPE where two start at one address; other overlaps
+ * are not looked for).
  */
 svdq_status svdq_quantize_act_fp8(const void* x, int64_t M, int64_t K, int64_t ldx, void* qx, float* sx,
                                   void* stream);

@@ -8,7 +8,8 @@ import torch
 
 import bit_quantized_diffusion_svdq_amd as svdq
 from oracle import fp8 as ofp8
-from test_fp8_rope_cpu import A, ALIGN, B, C, D, E, F, NULL, OK, SHAPE, _heads, lib, valid
+from test_fp8_rope_cpu import (A, ALIGN, B, C, D, E, F, NULL, OK, SHAPE, _act, _few, _few_grouped, _gemm, _heads, _weight, lib,
+                               valid)
 
 
 # ---------------------------------------------------------------- offsets that fall
@@ -170,3 +171,14 @@ def test_variant_refuses(lib, a):
     with pytest.raises(svdq.SvdqError):
         svdq.svdq_gemm_fp8_variant(*a)
     assert lib.svdq_gemm_fp8_variant(1, 16, 1, 0, 0, 256, None) == NULL
+
+
+# ---------------------------------------------------------------- outputs that start at another array
+
+def test_outputs_over_inputs_are_rejected(lib):
+    ws = dict(M=17, ws=B, wsb=17 * 2048 + 17 * 64)
+    for status in (_act(lib, qx=A), _act(lib, sx=A), _act(lib, sx=B), _weight(lib, qw=A), _weight(lib, sw=A), _weight(lib, sw=B),
+                   _gemm(lib, False, y=A), _gemm(lib, True, y=C), _few(lib, y=A), _few(lib, y=C), _few_grouped(lib, y=A),
+                   _few(lib, **ws, y=B), _few(lib, **{**ws, "ws": A}), _few_grouped(lib, **ws, y=C)):
+        assert status == SHAPE and b"overlap" in lib.svdq_last_error()
+    valid(_few(lib, **ws, y=A))                              # with a workspace x is read before y is written
