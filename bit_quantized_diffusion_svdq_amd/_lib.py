@@ -67,6 +67,10 @@ _SIGS = {
     "svdq_rope_axes": [_P, _P, _I64, _I32, _I32, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P],
     "svdq_rope_axes_grouped": [_P, _P, _I64, _I32, _I32, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P,
                                _I32, _P],
+    "svdq_kv_cache_sizes": [_P, _P, _P],
+    "svdq_kv_append": [_P, _P, _P, _P, _P, _P, _I32, _I32, _P, _P, _I32, _I32, ctypes.c_float, _P],
+    "svdq_kv_attend_workspace_size": [_P, _P, _I32, _P],
+    "svdq_kv_attend": [_P, _P, _P, ctypes.c_float, _I32, _I32, _P, _I64, _P],
 }
 
 
@@ -90,6 +94,18 @@ class RopeHeads(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("heads", ctypes.c_int32), ("norm", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    """svdq_kv_cache: a paged cache's arrays and sizes."""
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("D", ctypes.c_int32), ("page", ctypes.c_int32)]
+
+
+class KvBatchDesc(ctypes.Structure):
+    """svdq_kv_batch: the sequences and tokens of one call."""
+    _fields_ = [("table", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("T", ctypes.c_int64), ("sequences", ctypes.c_int32), ("width", ctypes.c_int32)]
 
 
 def load_library():
@@ -365,6 +381,36 @@ def svdq_rope_axes_grouped(q, k, T, D, dtype, pos, pos_dtype, axes, turns, axis,
                                                  None if k is None else ctypes.addressof(k), T, D, dtype, _ptr(pos),
                                                  pos_dtype, axes, _ptr(turns), _ptr(axis), pairs, pairing, inverse, eps,
                                                  _ptr(offsets), groups, _stream(stream)), "svdq_rope_axes_grouped")
+
+
+def _at(struct):
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def svdq_kv_cache_sizes(cache):
+    """(bytes of data, bytes of scales) of a KvCacheDesc."""
+    data, scales = ctypes.c_int64(0), ctypes.c_int64(0)
+    _check(load_library().svdq_kv_cache_sizes(_at(cache), ctypes.addressof(data), ctypes.addressof(scales)),
+           "svdq_kv_cache_sizes")
+    return data.value, scales.value
+
+
+def svdq_kv_append(cache, batch, q, k, v, pos, pos_dtype, axes, turns, axis, pairs, pairing, eps, stream=None):
+    """cache: KvCacheDesc, batch: KvBatchDesc, q (or None), k, v: RopeHeads."""
+    _check(load_library().svdq_kv_append(_at(cache), _at(batch), _at(q), _at(k), _at(v), _ptr(pos), pos_dtype, axes,
+                                         _ptr(turns), _ptr(axis), pairs, pairing, eps, _stream(stream)), "svdq_kv_append")
+
+
+def svdq_kv_attend_workspace_size(cache, batch, heads) -> int:
+    out = ctypes.c_int64(0)
+    _check(load_library().svdq_kv_attend_workspace_size(_at(cache), _at(batch), heads, ctypes.addressof(out)),
+           "svdq_kv_attend_workspace_size")
+    return out.value
+
+
+def svdq_kv_attend(cache, batch, q, scale, causal, window, workspace, workspace_bytes, stream=None):
+    _check(load_library().svdq_kv_attend(_at(cache), _at(batch), _at(q), scale, causal, window, _ptr(workspace),
+                                         workspace_bytes, _stream(stream)), "svdq_kv_attend")
 
 
 # ---------------------------------------------------------------- tensor helpers

@@ -10,6 +10,7 @@
 #include <string>
 
 #include "../../include/svdq.h"
+#include "kv.h"
 #include "rope.h"
 
 hipError_t launch_act_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ldx,
@@ -1060,6 +1061,231 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
     if (groups < 1) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
     return rope_axes_impl(q, k, T, D, dtype, pos, pos_dtype, axes, turns, axis, pairs, pairing, inverse, eps, offsets,
                           groups, stream, "svdq_rope_axes_grouped launch");
+}
+
+}  // extern "C"
+
+/* ------------------------------------------------------------------------ */
+/* Attention over a paged 8-bit cache                                        */
+
+namespace {
+
+constexpr int kChipCus = 256;            // the workspace's size must not depend on the device asked from
+
+svdq_status check_kv_cache(const svdq_kv_cache* c) {
+    if (!c) return fail(SVDQ_ERR_NULL, "cache is required");
+    if (c->pages < 1 || c->pages >= (int64_t)1 << 31)
+        return fail(SVDQ_ERR_SHAPE, "pages = %lld must be in [1, 2^31)", (long long)c->pages);
+    if (c->heads < 1 || c->heads > 65536) return fail(SVDQ_ERR_SHAPE, "heads = %d must be in [1, 65536]", c->heads);
+    if (c->D < 8 || c->D > 256 || c->D % 8) return fail(SVDQ_ERR_SHAPE, "D = %d must be a multiple of 8 in [8, 256]", c->D);
+    if (c->page < 64 || c->page > 65536 || c->page % 64)
+        return fail(SVDQ_ERR_SHAPE, "page = %d must be a multiple of 64 in [64, 65536]", c->page);
+    return SVDQ_OK;
+}
+
+svdq_status check_kv_batch(const svdq_kv_cache* c, const svdq_kv_batch* b) {
+    if (!b) return fail(SVDQ_ERR_NULL, "batch is required");
+    if (b->T < 0 || b->T >= (int64_t)1 << 30) return fail(SVDQ_ERR_SHAPE, "T = %lld must be in [0, 2^30)", (long long)b->T);
+    if (b->sequences < 1 || b->sequences > 65536)
+        return fail(SVDQ_ERR_SHAPE, "sequences = %d must be in [1, 65536]", b->sequences);
+    if (b->width < 0 || (int64_t)b->width * c->page >= ((int64_t)1 << 31) - 64)
+        return fail(SVDQ_ERR_SHAPE, "width = %d pages of %d tokens must stay below 2^31 - 64 tokens", b->width, c->page);
+    if (!b->offsets && b->T % b->sequences)
+        return fail(SVDQ_ERR_SHAPE, "T = %lld must be a multiple of sequences = %d without offsets", (long long)b->T, b->sequences);
+    return SVDQ_OK;
+}
+
+// pointers of a call that has tokens
+svdq_status check_kv_pointers(const svdq_kv_cache* c, const svdq_kv_batch* b) {
+    if (!c->data || !c->scales || !b->lengths || (b->width && !b->table))
+        return fail(SVDQ_ERR_NULL, "data, scales, table and lengths are required");
+    if (!aligned(c->data, 16) || !aligned(c->scales, 8) || !aligned(b->lengths, 4) || !aligned(b->table, 4) || !aligned(b->offsets, 4))
+        return fail(SVDQ_ERR_ALIGN, "data needs 16-byte alignment, scales 8, table, lengths and offsets 4");
+    return SVDQ_OK;
+}
+
+svdq_status check_kv_source(const svdq_rope_heads* h, const char* name, int heads) {
+    if (!h) return fail(SVDQ_ERR_NULL, "%s is required", name);
+    if (h->heads != heads) return fail(SVDQ_ERR_SHAPE, "%s: %d heads, the cache has %d", name, h->heads, heads);
+    for (int64_t v : {h->token_stride, h->head_stride}) {
+        if (v < 0 || v >= ((int64_t)1 << 40)) return fail(SVDQ_ERR_SHAPE, "%s: stride %lld is out of range", name, (long long)v);
+        if (v % 8) return fail(SVDQ_ERR_ALIGN, "%s: stride %lld must be a multiple of 8", name, (long long)v);
+    }
+    return SVDQ_OK;
+}
+
+KvCache kv_cache_of(const svdq_kv_cache* c) {
+    return KvCache{(uint8_t*)c->data, (uint8_t*)c->scales, c->pages, c->heads, c->D, c->page / 64};
+}
+
+KvBatch kv_batch_of(const svdq_kv_batch* b) {
+    return KvBatch{b->table, b->lengths, b->offsets, b->T, b->sequences, b->width, b->offsets ? 0 : (int)(b->T / b->sequences)};
+}
+
+// query heads of a key head, or a refusal
+svdq_status check_kv_heads(const svdq_kv_cache* c, const svdq_kv_batch* b, int32_t heads, int* G) {
+    if (heads < 1 || heads > 65536 || heads % c->heads)
+        return fail(SVDQ_ERR_SHAPE, "%d query heads must be a multiple of %d key heads, at most 65536", heads, c->heads);
+    *G = heads / c->heads;
+    // a row tile's workgroup has at least one row, or is one more of a sequence; lanes of a launch stay below 2^32
+    if (b->T * heads >= (int64_t)1 << 30 || (b->T * *G / 16 + b->sequences) * c->heads >= (int64_t)1 << 24)
+        return fail(SVDQ_ERR_SHAPE, "T = %lld with %d heads needs more workgroups than one launch holds", (long long)b->T, heads);
+    return SVDQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+svdq_status svdq_kv_cache_sizes(const svdq_kv_cache* cache, int64_t* data_bytes, int64_t* scale_bytes) {
+    svdq_status s;
+    if ((s = check_kv_cache(cache)) != SVDQ_OK) return s;
+    if (!data_bytes || !scale_bytes) return fail(SVDQ_ERR_NULL, "data_bytes and scale_bytes are required");
+    const int64_t tiles = cache->pages * cache->heads * (cache->page / 64);
+    *data_bytes = tiles * 8192 * ((cache->D + 63) / 64);
+    *scale_bytes = tiles * 8;
+    g_last_error.clear();
+    return SVDQ_OK;
+}
+
+svdq_status svdq_kv_append(const svdq_kv_cache* cache, const svdq_kv_batch* batch, const svdq_rope_heads* q,
+                           const svdq_rope_heads* k, const svdq_rope_heads* v, const void* pos, int32_t pos_dtype,
+                           int32_t axes, const double* turns, const int32_t* axis, int32_t pairs, int32_t pairing,
+                           float eps, void* stream) {
+    svdq_status s;
+    if ((s = check_kv_cache(cache)) != SVDQ_OK) return s;
+    if ((s = check_kv_batch(cache, batch)) != SVDQ_OK) return s;
+    const int64_t T = batch->T;
+    const int32_t D = cache->D;
+    if (pairs < 0 || pairs % 4 || 2 * (int64_t)pairs > D)
+        return fail(SVDQ_ERR_SHAPE, "pairs = %d must be a multiple of 4 with 2 * pairs <= D = %d", pairs, D);
+    if (axes < 1 || axes > 8) return fail(SVDQ_ERR_SHAPE, "axes = %d must be in [1, 8]", axes);
+    if (pos_dtype != SVDQ_POS_I32 && pos_dtype != SVDQ_POS_F32)
+        return fail(SVDQ_ERR_UNSUPPORTED, "position dtype %d is not supported", pos_dtype);
+    if (pairing != SVDQ_PAIRS_INTERLEAVED && pairing != SVDQ_PAIRS_HALF)
+        return fail(SVDQ_ERR_UNSUPPORTED, "pairing %d is not supported", pairing);
+    if (!(eps >= 0.0f)) return fail(SVDQ_ERR_UNSUPPORTED, "eps must be >= 0");
+    if ((s = check_kv_source(k, "k", cache->heads)) != SVDQ_OK) return s;
+    if ((s = check_kv_source(v, "v", cache->heads)) != SVDQ_OK) return s;
+    if (v->norm) return fail(SVDQ_ERR_UNSUPPORTED, "v takes no norm");
+    if (q && (s = check_rope_heads(q, "q", 1, T, D)) != SVDQ_OK) return s;
+    // workgroups: four key heads of a block each, four tokens of queries and one load of their heads
+    const int64_t blocks = (T / 16 + 2 * (int64_t)batch->sequences) * ((cache->heads + 3) / 4);
+    if (blocks + (q ? (T / 4 + 1) * (((int64_t)q->heads * D + 511) / 512 + 1) : 0) >= (int64_t)1 << 24)
+        return fail(SVDQ_ERR_SHAPE, "T = %lld tokens of %d sequences need more workgroups than one launch holds", (long long)T,
+                    batch->sequences);
+    if (T == 0) { g_last_error.clear(); return SVDQ_OK; }
+    if ((s = check_kv_pointers(cache, batch)) != SVDQ_OK) return s;
+    if (!k->x || !v->x) return fail(SVDQ_ERR_NULL, "k and v are required");
+    if (!aligned(k->x, 16) || !aligned(v->x, 16) || !aligned(k->norm, 16))
+        return fail(SVDQ_ERR_ALIGN, "k, v and the norm need 16-byte alignment");
+    if (pairs > 0 && (!pos || !turns || !axis)) return fail(SVDQ_ERR_NULL, "pos, turns and axis are required");
+    if (pairs > 0 && (!aligned(pos, 4) || !aligned(turns, 8) || !aligned(axis, 4)))
+        return fail(SVDQ_ERR_ALIGN, "pos, axis need 4-byte alignment, turns 8");
+    if (q && (s = check_rope_overlap(q, nullptr, T)) != SVDQ_OK) return s;
+    if (q && (q->y == k->x || q->y == v->x || q->y == cache->data || q->y == cache->scales))
+        return fail(SVDQ_ERR_SHAPE, "q's output overlaps k, v or the cache");
+    if (cache->data == k->x || cache->data == v->x || (q && cache->data == q->x) || cache->data == cache->scales)
+        return fail(SVDQ_ERR_SHAPE, "the cache overlaps q, k, v or its scales");
+    int cus = 0;
+    if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
+    RopeArgs r = {};
+    if (q) {
+        r.x[0] = q->x;
+        r.y[0] = q->y;
+        r.norm[0] = q->norm;
+        r.ts[0] = q->token_stride;
+        r.hs[0] = q->head_stride;
+        r.yts[0] = q->y_token_stride;
+        r.yhs[0] = q->y_head_stride;
+        r.heads[0] = q->heads;
+        r.pos = pos;
+        r.turns = turns;
+        r.axis = axis;
+        r.offs = batch->offsets;
+        r.groups = batch->offsets ? batch->sequences : 0;
+        r.T = T;
+        r.D = D;
+        r.pairs = pairs;
+        r.axes = axes;
+        r.pos_f32 = pos_dtype == SVDQ_POS_F32;
+        r.eps = eps;
+    }
+    KvAppendArgs a = {};
+    a.c = kv_cache_of(cache);
+    a.s = kv_batch_of(batch);
+    a.k = (const uint16_t*)k->x;
+    a.v = (const uint16_t*)v->x;
+    a.norm = (const uint16_t*)k->norm;
+    a.kts = k->token_stride;
+    a.khs = k->head_stride;
+    a.vts = v->token_stride;
+    a.vhs = v->head_stride;
+    a.pos = pos;
+    a.turns = turns;
+    a.axis = axis;
+    a.axes = axes;
+    a.pos_f32 = pos_dtype == SVDQ_POS_F32;
+    a.pairs = pairs;
+    a.eps = eps;
+    return launched(launch_kv_append(a, r, pairing == SVDQ_PAIRS_HALF, cus, (hipStream_t)stream), "svdq_kv_append launch");
+}
+
+svdq_status svdq_kv_attend_workspace_size(const svdq_kv_cache* cache, const svdq_kv_batch* batch, int32_t heads,
+                                          int64_t* bytes) {
+    svdq_status s;
+    int G = 0;
+    if ((s = check_kv_cache(cache)) != SVDQ_OK) return s;
+    if ((s = check_kv_batch(cache, batch)) != SVDQ_OK) return s;
+    if ((s = check_kv_heads(cache, batch, heads, &G)) != SVDQ_OK) return s;
+    if (!bytes) return fail(SVDQ_ERR_NULL, "bytes is required");
+    *bytes = kv_attend_workspace(kv_batch_of(batch), kv_cache_of(cache), G, kChipCus);
+    g_last_error.clear();
+    return SVDQ_OK;
+}
+
+svdq_status svdq_kv_attend(const svdq_kv_cache* cache, const svdq_kv_batch* batch, const svdq_rope_heads* q,
+                           float scale, int32_t causal, int32_t window, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+    svdq_status s;
+    int G = 0;
+    if ((s = check_kv_cache(cache)) != SVDQ_OK) return s;
+    if ((s = check_kv_batch(cache, batch)) != SVDQ_OK) return s;
+    if (!q) return fail(SVDQ_ERR_NULL, "q is required");
+    if ((s = check_kv_heads(cache, batch, q->heads, &G)) != SVDQ_OK) return s;
+    if (q->norm) return fail(SVDQ_ERR_UNSUPPORTED, "q takes no norm here");
+    if ((s = check_rope_heads(q, "q", 1, batch->T, cache->D)) != SVDQ_OK) return s;
+    if (!(scale > 0.0f && scale < __builtin_inff())) return fail(SVDQ_ERR_UNSUPPORTED, "scale must be positive and finite");
+    if (causal != 0 && causal != 1) return fail(SVDQ_ERR_UNSUPPORTED, "causal must be 0 or 1");
+    if (window < 0) return fail(SVDQ_ERR_SHAPE, "window = %d must not be negative", window);
+    const KvBatch b = kv_batch_of(batch);
+    const KvCache c = kv_cache_of(cache);
+    const int64_t need = kv_attend_workspace(b, c, G, kChipCus);
+    if (workspace_bytes < need)
+        return fail(SVDQ_ERR_SHAPE, "workspace of %lld bytes, %lld are needed", (long long)workspace_bytes, (long long)need);
+    if (batch->T == 0) { g_last_error.clear(); return SVDQ_OK; }
+    if ((s = check_kv_pointers(cache, batch)) != SVDQ_OK) return s;
+    if (need && !workspace) return fail(SVDQ_ERR_NULL, "workspace is required");
+    if (need && !aligned(workspace, 16)) return fail(SVDQ_ERR_ALIGN, "workspace needs 16-byte alignment");
+    if ((s = check_rope_overlap(q, nullptr, batch->T)) != SVDQ_OK) return s;
+    if (q->y == cache->data || q->y == cache->scales || (need && (q->y == workspace || q->x == workspace || cache->data == workspace)))
+        return fail(SVDQ_ERR_SHAPE, "the output, the workspace, q and the cache overlap");
+    if ((s = check_current_device()) != SVDQ_OK) return s;
+    KvAttendArgs a = {};
+    a.c = c;
+    a.s = b;
+    a.q = (const uint16_t*)q->x;
+    a.y = (uint16_t*)q->y;
+    a.qts = q->token_stride;
+    a.qhs = q->head_stride;
+    a.yts = q->y_token_stride;
+    a.yhs = q->y_head_stride;
+    a.G = G;
+    a.causal = causal;
+    a.window = window;
+    a.scale2 = scale * 1.4426950408889634f;
+    a.part = (float*)workspace;
+    return launched(launch_kv_attend(a, kChipCus, (hipStream_t)stream), "svdq_kv_attend launch");
 }
 
 }  // extern "C"

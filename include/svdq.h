@@ -664,6 +664,85 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
                                    const double* turns, const int32_t* axis, int32_t pairs, int32_t pairing,
                                    int32_t inverse, float eps, const int32_t* offsets, int32_t groups, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Attention over a paged cache of keys and values in 8 bits, for blocks whose
+ * tokens come in steps or chunks (autoregressive video, text): what stands
+ * between the rotated heads and the output projection.
+ *
+ * The cache: `pages` pages of `page` tokens (a multiple of 64) of every key
+ * head. data [pages][heads][page / 64][2 (keys, values)][4][C][1024] bytes, C =
+ * ceil(D / 64): a block of 16 tokens of one head and side is C runs of 1024 E4M3
+ * codes. Code j of run c is, of the keys, channel 64 c + 16 (j / 256) + j % 16 of
+ * token j / 16 % 16; of the values, channel 64 c + 16 (j / 4 % 4) + j / 16 % 16 of
+ * token 4 (j / 256) + j % 4 (a wave's lanes read either as matrix operands, 16
+ * bytes each). Channels past D are zeros. scales [pages][heads][page / 64][2][4]
+ * bytes: a code stands for code * 2^(byte - 127) (E8M0), one byte a block.
+ *
+ * A batch: `sequences` sequences, sequence b on pages table[b][0 .. width - 1], in
+ * order; lengths[b] tokens of it are in the cache, those of the call among them
+ * (they are the last ones). The call's T tokens are sorted by sequence, offsets[b]
+ * .. offsets[b + 1] - 1 those of b (int32 [sequences + 1]; NULL: T / sequences
+ * each). table, lengths and offsets are int32 DEVICE arrays, read by the kernels,
+ * so a captured graph follows them, and no status reports bad ones: offsets are
+ * clamped into [0, T], one that falls counts as the largest before it; a page
+ * outside [0, pages) is one that is not there (its tokens are neither stored nor
+ * seen; a window's spent pages may be given back like this), and so is what lies
+ * past the table or before token 0. Tokens of no sequence are left as they are.
+ * Sequences may share pages that no call writes; a page written by two
+ * sequences of a call is the caller's mistake.
+ *
+ * svdq_kv_cache_sizes -- bytes of data and scales. New pages need no values.
+ *
+ * svdq_kv_append -- k and v [T][heads][D] into the cache. Keys are normed (RMS,
+ *   norm [D] or NULL) and rotated as svdq_rope_axes does (pairs 0: not), in fp32,
+ *   and rounded once, to their codes. Per block of 16 tokens, head and side: e the
+ *   least exponent with amax <= 448 * 2^e over the call's finite values, at least
+ *   -120, and not below the block's own where the call does not begin it; code =
+ *   e4m3(x * 2^-e), nearest even, infinities saturate, NaN stays. Tokens from
+ *   before are rounded again where e grows. Codes of the last block past
+ *   the last token become zeros. q (NULL: none): queries, normed and rotated into
+ *   q->y in the same launch (y may be x with its strides). k, v: y unused; v: norm
+ *   NULL. Strides multiples of 8, x, y and norm 16-byte aligned, all bf16.
+ *
+ * svdq_kv_attend -- y = softmax(scale q k^T) v for q->x [T][heads][D], heads a
+ *   multiple of the cache's (query head i reads key head i / (heads / key heads)).
+ *   A query at position p (the call's tokens are its sequence's last) sees keys
+ *   [max(0, p - window + 1), causal ? p + 1 : length), window 0: from 0. One that
+ *   sees none gives zeros. Statistics and sums are fp32; probabilities are
+ *   rounded to bf16 for the second product; one rounding of the output. Keys and
+ *   values that a query does not see never reach it, whatever they hold. A query
+ *   with an infinity or a NaN gives NaN. q->y may be q->x with its strides.
+ *   workspace: svdq_kv_attend_workspace_size bytes (may be 0), 16-byte aligned,
+ *   not shared by calls that overlap. scale > 0 and finite.
+ *
+ * D a multiple of 8 in [8, 256]; page in [64, 65536]; width * page < 2^31 - 64; T <
+ * 2^30; sequences in [1, 65536]; window in [0, 2^31). data and workspace 16-byte
+ * aligned, scales 8, the int32 arrays 4.
+ */
+typedef struct {
+    void* data;
+    void* scales;
+    int64_t pages;
+    int32_t heads, D, page;
+} svdq_kv_cache;
+typedef struct {
+    const int32_t* table;
+    const int32_t* lengths;
+    const int32_t* offsets;
+    int64_t T;
+    int32_t sequences, width;
+} svdq_kv_batch;
+svdq_status svdq_kv_cache_sizes(const svdq_kv_cache* cache, int64_t* data_bytes, int64_t* scale_bytes);
+svdq_status svdq_kv_append(const svdq_kv_cache* cache, const svdq_kv_batch* batch, const svdq_rope_heads* q,
+                           const svdq_rope_heads* k, const svdq_rope_heads* v, const void* pos, int32_t pos_dtype,
+                           int32_t axes, const double* turns, const int32_t* axis, int32_t pairs, int32_t pairing,
+                           float eps, void* stream);
+svdq_status svdq_kv_attend_workspace_size(const svdq_kv_cache* cache, const svdq_kv_batch* batch, int32_t heads,
+                                          int64_t* bytes);
+svdq_status svdq_kv_attend(const svdq_kv_cache* cache, const svdq_kv_batch* batch, const svdq_rope_heads* q,
+                           float scale, int32_t causal, int32_t window, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif
