@@ -17,7 +17,8 @@ from ._lib import (SvdqError, awq_gemv_w4a16, check_device, library_path, load_l
                    w4a4_linear_quant_next, svdq_gemm_mxfp4_quant_next, mxfp4_linear_quant_next,
                    svdq_quantize_act_fp8, svdq_quantize_weight_fp8, svdq_gemm_fp8, svdq_gemm_fp8_grouped,
                    svdq_gemm_fp8_variant, svdq_linear_fp8, svdq_linear_fp8_grouped, svdq_linear_fp8_workspace_size, svdq_rope_axes,
-                   svdq_rope_axes_grouped, KvBatchDesc, KvCacheDesc, svdq_kv_append, svdq_kv_attend,
+                   svdq_rope_axes_grouped, svdq_gemm_fp8_residual, svdq_linear_fp8_residual, Fp8Residual,
+                   KvBatchDesc, KvCacheDesc, svdq_kv_append, svdq_kv_attend,
                    svdq_kv_attend_workspace_size, svdq_kv_cache_sizes)
 from .fp8 import Fp8GroupedLinear, Fp8Linear, fp8_grouped_linear, fp8_linear, quantize_act_fp8
 from .offline import quantize_awq, quantize_fp8, quantize_layer
@@ -46,5 +47,5 @@ __all__ = ["SvdqError", "awq_gemv_w4a16", "check_device", "library_path", "load_
            "svdq_linear_fp8", "svdq_linear_fp8_grouped", "svdq_linear_fp8_workspace_size", "svdq_gemm_fp8_variant", "svdq_rope_axes",
            "svdq_rope_axes_grouped", "Fp8GroupedLinear", "Fp8Linear", "fp8_grouped_linear", "fp8_linear",
            "quantize_act_fp8", "quantize_fp8", "RopePlan", "rope_axes", "FusedQKV", "save_fp8_layer", "load_fp8_layer",
-           "KvBatchDesc", "KvCacheDesc", "svdq_kv_append", "svdq_kv_attend", "svdq_kv_attend_workspace_size",
+           "svdq_gemm_fp8_residual", "svdq_linear_fp8_residual", "Fp8Residual", "KvBatchDesc", "KvCacheDesc", "svdq_kv_append", "svdq_kv_attend", "svdq_kv_attend_workspace_size",
            "svdq_kv_cache_sizes", "KVCache"]

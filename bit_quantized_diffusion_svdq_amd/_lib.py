@@ -67,6 +67,8 @@ _SIGS = {
     "svdq_rope_axes": [_P, _P, _I64, _I32, _I32, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P],
     "svdq_rope_axes_grouped": [_P, _P, _I64, _I32, _I32, _P, _I32, _I32, _P, _P, _I32, _I32, _I32, ctypes.c_float, _P,
                                _I32, _P],
+    "svdq_gemm_fp8_residual": [_P, _P, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _P, _P, _I32, _I64, _P],
+    "svdq_linear_fp8_residual": [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _P, _I32, _P, _P, _I32, _I64, _P, _I64, _P],
     "svdq_kv_cache_sizes": [_P, _P, _P],
     "svdq_kv_append": [_P, _P, _P, _P, _P, _P, _I32, _I32, _P, _P, _I32, _I32, ctypes.c_float, _P],
     "svdq_kv_attend_workspace_size": [_P, _P, _I32, _P],
@@ -94,6 +96,11 @@ class RopeHeads(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("heads", ctypes.c_int32), ("norm", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64)]
+
+
+class Fp8Residual(ctypes.Structure):
+    """svdq_fp8_residual: what an 8-bit layer's outputs join."""
+    _fields_ = [("x", ctypes.c_void_p), ("ld", ctypes.c_int64), ("gate", ctypes.c_void_p)]
 
 
 class KvCacheDesc(ctypes.Structure):
@@ -385,6 +392,20 @@ def svdq_rope_axes_grouped(q, k, T, D, dtype, pos, pos_dtype, axes, turns, axis,
 
 def _at(struct):
     return None if struct is None else ctypes.addressof(struct)
+
+
+def svdq_gemm_fp8_residual(qx, sx, M, K, qw, sw, N, offsets, groups, bias, act, residual, y, y_dtype, ldy, stream=None):
+    """residual: Fp8Residual."""
+    _check(load_library().svdq_gemm_fp8_residual(_ptr(qx), _ptr(sx), M, K, _ptr(qw), _ptr(sw), N, _ptr(offsets), groups,
+                                                 _ptr(bias), act, _at(residual), _ptr(y), y_dtype, ldy, _stream(stream)),
+           "svdq_gemm_fp8_residual")
+
+
+def svdq_linear_fp8_residual(x, M, K, ldx, qw, sw, N, offsets, groups, bias, act, residual, y, y_dtype, ldy, workspace,
+                             workspace_bytes, stream=None):
+    _check(load_library().svdq_linear_fp8_residual(_ptr(x), M, K, ldx, _ptr(qw), _ptr(sw), N, _ptr(offsets), groups,
+                                                   _ptr(bias), act, _at(residual), _ptr(y), y_dtype, ldy, _ptr(workspace),
+                                                   workspace_bytes, _stream(stream)), "svdq_linear_fp8_residual")
 
 
 def svdq_kv_cache_sizes(cache):

@@ -10,6 +10,7 @@
 #include <string>
 
 #include "../../include/svdq.h"
+#include "fp8.h"
 #include "kv.h"
 #include "rope.h"
 
@@ -63,10 +64,10 @@ bool gemm_fp8_fits(int64_t M, int64_t N, int E);
 int gemm_fp8_variant(int64_t M, int64_t K, int64_t N, int groups, int y_f32, int cus);
 hipError_t launch_gemm_fp8(const uint8_t* qx, const float* sx, int64_t M, int64_t K, const uint8_t* qw, const float* sw,
                            int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
-                           int64_t ldy, int cus, hipStream_t stream);
+                           int64_t ldy, const Fp8Residual& res, int cus, hipStream_t stream);
 hipError_t launch_linear_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw, const float* sw,
                              int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
-                             int64_t ldy, int cus, hipStream_t stream);
+                             int64_t ldy, const Fp8Residual& res, int cus, hipStream_t stream);
 hipError_t launch_gemm_w4a4_next(const uint8_t* qx, const uint16_t* sx, const uint8_t* qw,
                                  const uint16_t* sw, const float* xl1, const uint16_t* l2t, int rank,
                                  const uint16_t* bias, int act, int64_t M, int64_t N, int64_t K,
@@ -774,14 +775,32 @@ svdq_status check_gemm_fp8_sizes(int64_t M, int64_t K, int64_t N, int32_t groups
     return SVDQ_OK;
 }
 
+// A residual's own checks, before those of pointers. In place (y itself) needs y's rows.
+svdq_status check_residual(const svdq_fp8_residual* r, int64_t M, int64_t N, const void* y, int64_t ldy, int32_t y_dtype) {
+    if (!r) return SVDQ_OK;
+    if (r->ld < N || r->ld >= (int64_t)1 << 31)
+        return fail(SVDQ_ERR_SHAPE, "the residual's row stride %lld must be in [N = %lld, 2^31)", (long long)r->ld, (long long)N);
+    if (M == 0) return SVDQ_OK;
+    if (!r->x) return fail(SVDQ_ERR_NULL, "the residual's x is required");
+    if (!aligned(r->x, y_dtype == SVDQ_DT_F32 ? 4 : 2) || !aligned(r->gate, 2))
+        return fail(SVDQ_ERR_ALIGN, "the residual needs its element's alignment, the gate 2");
+    if (r->x == y && M > 1 && r->ld != ldy) return fail(SVDQ_ERR_SHAPE, "in place needs the residual's row stride to be y's");
+    return SVDQ_OK;
+}
+
+Fp8Residual residual_of(const svdq_fp8_residual* r) {
+    return r ? Fp8Residual{r->x, r->ld, (const uint16_t*)r->gate} : Fp8Residual{};
+}
+
 svdq_status gemm_fp8_impl(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
                           int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act, void* y,
-                          int32_t y_dtype, int64_t ldy, void* stream, const char* what) {
+                          int32_t y_dtype, int64_t ldy, const svdq_fp8_residual* res, void* stream, const char* what) {
     svdq_status s;
     if ((s = check_gemm_fp8_sizes(M, K, N, groups, y_dtype)) != SVDQ_OK) return s;
     if (ldy < N) return fail(SVDQ_ERR_SHAPE, "ldy = %lld < N = %lld", (long long)ldy, (long long)N);
     if (ldy >= (int64_t)1 << 31) return fail(SVDQ_ERR_SHAPE, "ldy = %lld must be below 2^31", (long long)ldy);
     if ((s = check_act(act)) != SVDQ_OK) return s;
+    if ((s = check_residual(res, M, N, y, ldy, y_dtype)) != SVDQ_OK) return s;
     if (M == 0) { g_last_error.clear(); return SVDQ_OK; }
     if (!qx || !sx || !qw || !sw || !y || (groups && !offsets))
         return fail(SVDQ_ERR_NULL, "qx, sx, qw, sw and y%s are required", groups ? ", offsets" : "");
@@ -792,8 +811,8 @@ svdq_status gemm_fp8_impl(const void* qx, const float* sx, int64_t M, int64_t K,
     int cus = 0;
     if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
     return launched(launch_gemm_fp8((const uint8_t*)qx, sx, M, K, (const uint8_t*)qw, sw, N, offsets, groups,
-                                    (const uint16_t*)bias, act, y, y_dtype == SVDQ_DT_F32, ldy, cus,
-                                    (hipStream_t)stream),
+                                    (const uint16_t*)bias, act, y, y_dtype == SVDQ_DT_F32, ldy, residual_of(res),
+                                    cus, (hipStream_t)stream),
                     what);
 }
 
@@ -815,7 +834,8 @@ svdq_status check_linear_fp8_mk(int64_t M, int64_t K) {
 
 svdq_status linear_fp8_impl(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
                             int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act, void* y,
-                            int32_t y_dtype, int64_t ldy, void* ws, int64_t ws_bytes, void* stream, const char* what) {
+                            int32_t y_dtype, int64_t ldy, const svdq_fp8_residual* res, void* ws, int64_t ws_bytes,
+                            void* stream, const char* what) {
     svdq_status s;
     if ((s = check_linear_fp8_mk(M, K)) != SVDQ_OK) return s;
     if (N <= 0 || N >= (int64_t)1 << 23) return fail(SVDQ_ERR_SHAPE, "N = %lld must be in [1, 2^23)", (long long)N);
@@ -833,6 +853,7 @@ svdq_status linear_fp8_impl(const void* x, int64_t M, int64_t K, int64_t ldx, co
         return fail(SVDQ_ERR_SHAPE, "M = %lld x N = %lld needs more tiles than one launch holds", (long long)M, (long long)N);
     if (ws_bytes < need)
         return fail(SVDQ_ERR_SHAPE, "workspace of %lld bytes, %lld are needed", (long long)ws_bytes, (long long)need);
+    if ((s = check_residual(res, M, N, y, ldy, y_dtype)) != SVDQ_OK) return s;
     if (M == 0) { g_last_error.clear(); return SVDQ_OK; }
     if (!x || !qw || !sw || !y || (groups && !offsets) || (need && !ws))
         return fail(SVDQ_ERR_NULL, "x, qw, sw and y%s%s are required", groups ? ", offsets" : "", need ? ", workspace" : "");
@@ -841,19 +862,20 @@ svdq_status linear_fp8_impl(const void* x, int64_t M, int64_t K, int64_t ldx, co
         return fail(SVDQ_ERR_ALIGN, "x, qw, workspace need 16-byte alignment, sw, offsets 4, bias 2, y its element's");
     if (y == qw || (need ? y == ws || x == ws : y == x))
         return fail(SVDQ_ERR_SHAPE, need ? "y, x and the workspace overlap" : "y overlaps x (few rows)");
+    if (res && need && res->x == ws) return fail(SVDQ_ERR_SHAPE, "the residual and the workspace overlap");
     int cus = 0;
     if ((s = check_current_device(&cus)) != SVDQ_OK) return s;
     if (!need)
         return launched(launch_linear_fp8((const uint16_t*)x, M, K, ldx, (const uint8_t*)qw, sw, N, offsets, groups,
-                                          (const uint16_t*)bias, act, y, y_dtype == SVDQ_DT_F32, ldy, cus,
-                                          (hipStream_t)stream),
+                                          (const uint16_t*)bias, act, y, y_dtype == SVDQ_DT_F32, ldy, residual_of(res),
+                                          cus, (hipStream_t)stream),
                         what);
     uint8_t* qx = (uint8_t*)ws;
     float* sx = (float*)(qx + M * K);                    // (K is a multiple of 16)
     if ((s = launched(launch_quant_act_fp8((const uint16_t*)x, M, K, ldx, qx, sx, cus, (hipStream_t)stream), what)) != SVDQ_OK)
         return s;
     return launched(launch_gemm_fp8(qx, sx, M, K, (const uint8_t*)qw, sw, N, offsets, groups, (const uint16_t*)bias, act,
-                                    y, y_dtype == SVDQ_DT_F32, ldy, cus, (hipStream_t)stream),
+                                    y, y_dtype == SVDQ_DT_F32, ldy, residual_of(res), cus, (hipStream_t)stream),
                     what);
 }
 
@@ -997,7 +1019,7 @@ svdq_status svdq_quantize_weight_fp8(const void* w, int64_t K, int64_t N, int64_
 svdq_status svdq_gemm_fp8(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
                           int64_t N, const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
                           void* stream) {
-    return gemm_fp8_impl(qx, sx, M, K, qw, sw, N, nullptr, 0, bias, act, y, y_dtype, ldy, stream,
+    return gemm_fp8_impl(qx, sx, M, K, qw, sw, N, nullptr, 0, bias, act, y, y_dtype, ldy, nullptr, stream,
                          "svdq_gemm_fp8 launch");
 }
 
@@ -1006,7 +1028,7 @@ svdq_status svdq_gemm_fp8_grouped(const void* qx, const float* sx, int64_t M, in
                                   const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
                                   void* stream) {
     if (groups < 1) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
-    return gemm_fp8_impl(qx, sx, M, K, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, stream,
+    return gemm_fp8_impl(qx, sx, M, K, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, nullptr, stream,
                          "svdq_gemm_fp8_grouped launch");
 }
 
@@ -1033,8 +1055,8 @@ svdq_status svdq_linear_fp8_workspace_size(int64_t M, int64_t K, int64_t* bytes)
 svdq_status svdq_linear_fp8(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
                             int64_t N, const void* bias, int32_t act, void* y, int32_t y_dtype, int64_t ldy,
                             void* workspace, int64_t workspace_bytes, void* stream) {
-    return linear_fp8_impl(x, M, K, ldx, qw, sw, N, nullptr, 0, bias, act, y, y_dtype, ldy, workspace, workspace_bytes,
-                           stream, "svdq_linear_fp8 launch");
+    return linear_fp8_impl(x, M, K, ldx, qw, sw, N, nullptr, 0, bias, act, y, y_dtype, ldy, nullptr, workspace,
+                           workspace_bytes, stream, "svdq_linear_fp8 launch");
 }
 
 svdq_status svdq_linear_fp8_grouped(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
@@ -1042,8 +1064,25 @@ svdq_status svdq_linear_fp8_grouped(const void* x, int64_t M, int64_t K, int64_t
                                     void* y, int32_t y_dtype, int64_t ldy, void* workspace, int64_t workspace_bytes,
                                     void* stream) {
     if (groups < 1) return fail(SVDQ_ERR_SHAPE, "groups = %d must be in [1, 65536]", groups);
-    return linear_fp8_impl(x, M, K, ldx, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, workspace,
+    return linear_fp8_impl(x, M, K, ldx, qw, sw, N, offsets, groups, bias, act, y, y_dtype, ldy, nullptr, workspace,
                            workspace_bytes, stream, "svdq_linear_fp8_grouped launch");
+}
+
+svdq_status svdq_gemm_fp8_residual(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
+                                   int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act,
+                                   const svdq_fp8_residual* residual, void* y, int32_t y_dtype, int64_t ldy, void* stream) {
+    if (!residual) return fail(SVDQ_ERR_NULL, "residual is required");
+    return gemm_fp8_impl(qx, sx, M, K, qw, sw, N, groups ? offsets : nullptr, groups, bias, act, y, y_dtype, ldy, residual, stream,
+                         "svdq_gemm_fp8_residual launch");
+}
+
+svdq_status svdq_linear_fp8_residual(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
+                                     int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act,
+                                     const svdq_fp8_residual* residual, void* y, int32_t y_dtype, int64_t ldy,
+                                     void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!residual) return fail(SVDQ_ERR_NULL, "residual is required");
+    return linear_fp8_impl(x, M, K, ldx, qw, sw, N, groups ? offsets : nullptr, groups, bias, act, y, y_dtype, ldy, residual, workspace,
+                           workspace_bytes, stream, "svdq_linear_fp8_residual launch");
 }
 
 svdq_status svdq_rope_axes(const svdq_rope_heads* q, const svdq_rope_heads* k, int64_t T, int32_t D, int32_t dtype,

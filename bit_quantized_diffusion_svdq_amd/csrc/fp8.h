@@ -89,3 +89,10 @@ DEV uint2 block_codes(const uint4& v, float& s) {
     const float r = reciprocal(s);
     return finite ? codes8<true>(w, r) : codes8<false>(w, r);
 }
+
+// what an 8-bit layer's outputs are added to: x + gate * act(...)
+struct Fp8Residual {
+    const void* x;                  // [M][ld] of the output's type, or NULL: no residual
+    int64_t ld;
+    const uint16_t* gate;           // bf16 [groups or 1][N], or NULL: ones
+};

@@ -14,6 +14,8 @@
 //  - Block scales are fp32 with a mantissa, so they cannot ride on the matrix
 //    pipe's E8M0 scales: the FMAs (4 of 64 lanes, 16 cycles of a SIMD) run
 //    beside the MFMAs (32 cycles).
+//  - With a residual (kernels of their own: RES), outputs are residual + gate *
+//    act(...), joined in fp32 before the one rounding.
 #include "fp8.h"
 
 namespace {
@@ -123,6 +125,10 @@ struct Args {
     int act, y_f32, vec;            // vec: rows of y take 16-byte stores
     const uint16_t* x;              // the layer of few rows: bf16 activations (qx, sx NULL), else NULL
     int64_t ldx;
+    const void* res;                // [M][ldr] of y's type, or NULL (it may be y)
+    int64_t ldr;
+    const uint16_t* gate;           // [E or 1][N], or NULL: ones
+    int vecr;                       // four outputs of a residual row in one load
 };
 
 // The rows a workgroup works on: m0 .. m0 + rows - 1 of group g (rows 0: none)
@@ -201,6 +207,37 @@ DEV void store1(const Args& a, int64_t row, int col, float v) {
     else ((uint16_t*)a.y)[row * a.ldy + col] = f32_to_bf16_bits(v);
 }
 
+// four consecutive values of a residual row; past N zeros
+DEV v4f residual4(const Args& a, int64_t row, int col) {
+    v4f r = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.vecr && col + 4 <= a.N) {
+        if (a.y_f32) {
+            r = *(const v4f*)((const float*)a.res + row * a.ldr + col);
+        } else {
+            const uint2 w = *(const uint2*)((const uint16_t*)a.res + row * a.ldr + col);
+            r = v4f{bf16_lo_to_f32(w.x), bf16_hi_to_f32(w.x), bf16_lo_to_f32(w.y), bf16_hi_to_f32(w.y)};
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e < a.N)
+                r[e] = a.y_f32 ? ((const float*)a.res)[row * a.ldr + col + e]
+                               : bf16_lo_to_f32(((const uint16_t*)a.res)[row * a.ldr + col + e]);
+    }
+    return r;
+}
+
+// four consecutive gates of group g; past N ones
+DEV v4f gate4(const Args& a, int g, int col) {
+    v4f r = v4f{1.0f, 1.0f, 1.0f, 1.0f};
+    if (a.gate) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e < a.N) r[e] = bf16_lo_to_f32(a.gate[(int64_t)g * a.N + col + e]);
+    }
+    return r;
+}
+
 // four consecutive outputs of one row
 DEV void store4(const Args& a, int64_t row, int col, const float* v) {
     if (a.vec && col + 4 <= a.N) {
@@ -240,7 +277,7 @@ DEV void dma4(rsrc_t r, char* lds, int voff, int soff) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 4, voff, soff, 0, 0);
 }
 
-template <class C, bool GROUPED>
+template <class C, bool GROUPED, bool RES>
 __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
     constexpr int BM = C::BM, BN = C::BN, TM = C::TM, TN = C::TN, NW = C::NW;
     // S slots of X's rows and row scales and S of W's rows, each a block of K;
@@ -479,6 +516,21 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
     constexpr int PER = 16 / ES, CHUNKS = 16 * CPR / 64;           // outputs of a chunk, chunks of a lane
     static_assert(NW * 16 * RB <= C::XSLOT && 16 * CPR % 64 == 0, "the staged rows fit a slot");
     char* stg = xs0 + wave * (16 * RB);
+    // RES: the gates of the lane's columns, and the residual of its row a block of 16 ahead
+    v4f gate[RES ? TN : 1], res[RES ? TN : 1];
+    auto load_res = [&](int i) __attribute__((always_inline)) {
+        const int row = (wm * TM + i) * 16 + l16;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            res[RES ? j : 0] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            if (row < rr.rows) res[RES ? j : 0] = residual4(a, rr.m0 + row, n0 + (wn * TN + j) * 16 + q4 * 4);
+        }
+    };
+    if constexpr (RES) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) gate[j] = gate4(a, rr.g, n0 + (wn * TN + j) * 16 + q4 * 4);
+        load_res(0);
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -487,11 +539,17 @@ __global__ __launch_bounds__(C::NT, C::WPE) void gemm_fp8_kernel(Args a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][j][e] = gelu_tanh_f32(acc[i][j][e]);
             }
+            if constexpr (RES) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(gate[j][e], acc[i][j][e], res[j][e]);
+            }
             const int at = (j * 16 + q4 * 4) * ES;
             char* d = stg + l16 * RB + ((((at >> 4) ^ l16) & (CPR - 1)) << 4) + (at & 15);
             if constexpr (C::PREC) *(float4*)d = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
             else *(uint2*)d = make_uint2(bf16x2(acc[i][j][0], acc[i][j][1]), bf16x2(acc[i][j][2], acc[i][j][3]));
         }
+        if constexpr (RES)
+            if (i + 1 < TM) load_res(i + 1);
 #pragma unroll
         for (int k = 0; k < CHUNKS; ++k) {
             const int q = k * 64 + lane, r = q / CPR, c = q % CPR;
@@ -537,7 +595,7 @@ struct FewCfg {
 // pass's.
 enum { DENSE, GROUPS, LAYER, LAYER_GROUPS };
 
-template <class C, int KIND>
+template <class C, int KIND, bool RES>
 __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
     constexpr int MT = C::MT, NT = C::NT, NW = C::NW, U = C::U;
     constexpr bool OWN = KIND >= LAYER, RAGGED = KIND == GROUPS || KIND == LAYER_GROUPS;
@@ -674,6 +732,11 @@ __global__ __launch_bounds__(64 * C::NW) void gemm_fp8_few_kernel(Args a) {
         for (int e = 0; e < 4; ++e)
             v[e] = finish(sum[e], a.bias && col + e < a.N ? bf16_lo_to_f32(a.bias[(int64_t)rr.g * a.N + col + e]) : 0.0f,
                           a.act);
+        if constexpr (RES) {
+            const v4f r = row < rr.rows ? residual4(a, rr.m0 + row, col) : v4f{0.0f, 0.0f, 0.0f, 0.0f}, g = gate4(a, rr.g, col);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(g[e], v[e], r[e]);
+        }
         if (row < rr.rows) store4(a, rr.m0 + row, col, v);
     }
 }
@@ -688,14 +751,22 @@ template <class C, bool GROUPED>
 void launch_tiles(const Args& a, hipStream_t stream) {
     const int64_t tm = row_tiles(a, C::BM);
     const int64_t tn = (a.N + C::BN - 1) / C::BN;
-    hipLaunchKernelGGL((gemm_fp8_kernel<C, GROUPED>), dim3((unsigned)(tm * tn)), dim3(C::NT), 0, stream, a);
+    const dim3 grid((unsigned)(tm * tn));
+    if (a.res) hipLaunchKernelGGL((gemm_fp8_kernel<C, GROUPED, true>), grid, dim3(C::NT), 0, stream, a);
+    else hipLaunchKernelGGL((gemm_fp8_kernel<C, GROUPED, false>), grid, dim3(C::NT), 0, stream, a);
+}
+
+template <class C, int KIND>
+void run_few(const Args& a, int64_t grid, size_t lds, hipStream_t stream) {
+    if (a.res) hipLaunchKernelGGL((gemm_fp8_few_kernel<C, KIND, true>), dim3((unsigned)grid), dim3(64 * C::NW), lds, stream, a);
+    else hipLaunchKernelGGL((gemm_fp8_few_kernel<C, KIND, false>), dim3((unsigned)grid), dim3(64 * C::NW), lds, stream, a);
 }
 
 template <class C, bool GROUPED>
 void launch_few(const Args& a, hipStream_t stream) {
     const int64_t tm = row_tiles(a, 16 * C::MT);
     const int64_t tn = (a.N + 16 * C::NT - 1) / (16 * C::NT);
-    hipLaunchKernelGGL((gemm_fp8_few_kernel<C, GROUPED ? GROUPS : DENSE>), dim3((unsigned)(tm * tn)), dim3(64 * C::NW), 0, stream, a);
+    run_few<C, GROUPED ? GROUPS : DENSE>(a, tm * tn, 0, stream);
 }
 
 // 16 outputs a workgroup, or 32 where one trip of its waves' loads still covers
@@ -709,10 +780,10 @@ void launch_layer(const Args& a, int cus, hipStream_t stream) {
     const int64_t tm = row_tiles(a, 16), narrow = tm * ((a.N + 15) / 16);
     if (KB <= 16 && narrow > cus) {
         typedef FewCfg<1, 2, 8, 2, PREC> C;
-        hipLaunchKernelGGL((gemm_fp8_few_kernel<C, KIND>), dim3((unsigned)(tm * ((a.N + 31) / 32))), dim3(64 * C::NW), lds, stream, a);
+        run_few<C, KIND>(a, tm * ((a.N + 31) / 32), lds, stream);
     } else {
         typedef FewCfg<1, 1, 8, 4, PREC> C;
-        hipLaunchKernelGGL((gemm_fp8_few_kernel<C, KIND>), dim3((unsigned)narrow), dim3(64 * C::NW), lds, stream, a);
+        run_few<C, KIND>(a, narrow, lds, stream);
     }
 }
 
@@ -857,11 +928,23 @@ int gemm_fp8_variant(int64_t M, int64_t K, int64_t N, int groups, int y_f32, int
     return pick_variant(a, y_f32 ? 1 : 0, cus);
 }
 
+namespace {
+
+Args with_residual(Args a, const Fp8Residual& r) {
+    a.res = r.x;
+    a.ldr = r.ld;
+    a.gate = r.gate;
+    a.vecr = r.ld % 4 == 0 && (uintptr_t)r.x % (a.y_f32 ? 16 : 8) == 0;
+    return a;
+}
+
+}  // namespace
+
 hipError_t launch_gemm_fp8(const uint8_t* qx, const float* sx, int64_t M, int64_t K, const uint8_t* qw, const float* sw,
                            int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
-                           int64_t ldy, int cus, hipStream_t stream) {
+                           int64_t ldy, const Fp8Residual& res, int cus, hipStream_t stream) {
     const int vec = ldy % (y_f32 ? 4 : 8) == 0 && (uintptr_t)y % 16 == 0;
-    const Args a{qx, sx, qw, sw, bias, y, offs, M, ldy, (int)N, (int)K, E, act, y_f32, vec, nullptr, 0};
+    const Args a = with_residual(Args{qx, sx, qw, sw, bias, y, offs, M, ldy, (int)N, (int)K, E, act, y_f32, vec, nullptr, 0}, res);
     const bool ok = offs ? (y_f32 ? launch_variant<1, true>(a, cus, stream) : launch_variant<0, true>(a, cus, stream))
                          : (y_f32 ? launch_variant<1, false>(a, cus, stream) : launch_variant<0, false>(a, cus, stream));
     return ok ? hipGetLastError() : hipErrorInvalidValue;
@@ -869,9 +952,9 @@ hipError_t launch_gemm_fp8(const uint8_t* qx, const float* sx, int64_t M, int64_
 
 hipError_t launch_linear_fp8(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const uint8_t* qw, const float* sw,
                              int64_t N, const int32_t* offs, int E, const uint16_t* bias, int act, void* y, int y_f32,
-                             int64_t ldy, int cus, hipStream_t stream) {
+                             int64_t ldy, const Fp8Residual& res, int cus, hipStream_t stream) {
     const int vec = ldy % (y_f32 ? 4 : 8) == 0 && (uintptr_t)y % 16 == 0;
-    const Args a{nullptr, nullptr, qw, sw, bias, y, offs, M, ldy, (int)N, (int)K, E, act, y_f32, vec, x, ldx};
+    const Args a = with_residual(Args{nullptr, nullptr, qw, sw, bias, y, offs, M, ldy, (int)N, (int)K, E, act, y_f32, vec, x, ldx}, res);
     if (offs) y_f32 ? launch_layer<1, LAYER_GROUPS>(a, cus, stream) : launch_layer<0, LAYER_GROUPS>(a, cus, stream);
     else y_f32 ? launch_layer<1, LAYER>(a, cus, stream) : launch_layer<0, LAYER>(a, cus, stream);
     return hipGetLastError();

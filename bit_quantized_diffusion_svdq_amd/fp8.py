@@ -16,6 +16,7 @@ allocates what it needs there.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 from dataclasses import dataclass
 
 import torch
@@ -146,11 +147,32 @@ def _output(y, M, N, out_dtype, like):
     return y, y.stride(0) if M > 1 else N
 
 
-def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfloat16, y=None, stream=None):
+def _residual(residual, gate, M, N, dtype, lead, dev):
+    """What the outputs join, or None: checked (``dtype``: the outputs')."""
+    if residual is None:
+        if gate is not None:
+            raise ValueError("gate needs a residual")
+        return None
+    if not (residual.shape == (M, N) and residual.dtype is dtype and (residual.stride(1) == 1 or N == 1)
+            and (residual.stride(0) >= N or M <= 1)):
+        raise ValueError(f"residual must be {dtype} [{M}, {N}] with contiguous columns and rows that do not overlap, got "
+                         f"{tuple(residual.shape)} {residual.dtype}, strides {residual.stride()}")
+    if gate is not None and not (gate.dtype is _BF16 and gate.shape == (*lead, N) and gate.is_contiguous()):
+        raise ValueError(f"gate must be contiguous bf16 {[*lead, N]}, got {tuple(gate.shape)} {gate.dtype}")
+    if residual.device != dev or (gate is not None and gate.device != dev):
+        raise ValueError(f"residual or gate is not on {dev}")
+    return _lib.Fp8Residual(residual.data_ptr(), residual.stride(0) if M > 1 else N, _address(gate))
+
+
+def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfloat16, y=None, stream=None,
+               residual=None, gate=None):
     """act(sum_b sx sw P_b + bias) for already quantised activations: qx E4M3
     [M, K], sx fp32 [ceil(K/128), M] (quantize_act_fp8), qw E4M3 [N, K], sw
     fp32 [ceil(N/128), ceil(K/128)], bias bf16 [N] or None -> y [M, N] (bf16
     or fp32; rows of a given y may be strided; y must not overlap the inputs).
+    residual [M, N] of the outputs' type (rows may be strided; y itself: in
+    place): the outputs are residual + gate * act(...), gate bf16 [N] or None
+    (ones), joined in fp32 before the one rounding.
 
     The output type also chooses the sums. bf16: the E4M3 matrix instructions,
     which drop what falls 13 bits below the largest of each 8 products, 1.4e-5
@@ -159,8 +181,14 @@ def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfl
     fp32: every product and sum in fp32, at half the matrix rate; round its
     result where bf16 outputs of such sums are wanted."""
     M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, 0)
+    res = _residual(residual, gate, M, N, out_dtype, (), qx.device)
     with _on(qx, stream):
         y, ldy = _output(y, M, N, out_dtype, qx)
+        if res is not None:
+            _check(load_library().svdq_gemm_fp8_residual(
+                qx.data_ptr(), sx.data_ptr(), M, K, qw.data_ptr(), sw.data_ptr(), N, None, 0, _address(bias), _lib.ACT[act],
+                ctypes.addressof(res), y.data_ptr(), out_dtype is _F32, ldy, _stream_now()), "svdq_gemm_fp8_residual")
+            return y
         _check(load_library().svdq_gemm_fp8(qx.data_ptr(), sx.data_ptr(), M, K, qw.data_ptr(), sw.data_ptr(), N,
                                             _address(bias), _lib.ACT[act], y.data_ptr(), out_dtype is _F32, ldy,
                                             _stream_now()), "svdq_gemm_fp8")
@@ -175,20 +203,28 @@ def _groups(offsets) -> int:
 
 
 def fp8_grouped_linear(qx, sx, offsets, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfloat16, y=None,
-                       stream=None):
+                       stream=None, residual=None, gate=None):
     """fp8_linear with a weight per group: rows offsets[g] .. offsets[g + 1] - 1
     of qx meet qw[g] [N, K], sw[g], bias[g]. offsets: int32 [groups + 1] on
     the GPU, rising, within [0, M] (read there: no synchronisation, so bad
     values are not reported: they are clamped, and one that falls counts as
     the largest before it). Rows of
     no group (before offsets[0], from offsets[-1] on) are left as they are in
-    a given y and are unspecified in a new one. The sums are fp8_linear's."""
+    a given y and are unspecified in a new one. The sums are fp8_linear's, and
+    so is residual; gate is bf16 [groups, N]."""
     groups = _groups(offsets)
     M, K, N, out_dtype = _check_product(qx, sx, qw, sw, bias, act, out_dtype, y, groups)
     if offsets.device != qx.device:
         raise ValueError(f"offsets is on {offsets.device}, expected {qx.device}")
+    res = _residual(residual, gate, M, N, out_dtype, (groups,), qx.device)
     with _on(qx, stream):
         y, ldy = _output(y, M, N, out_dtype, qx)
+        if res is not None:
+            _check(load_library().svdq_gemm_fp8_residual(
+                qx.data_ptr(), sx.data_ptr(), M, K, qw.data_ptr(), sw.data_ptr(), N, offsets.data_ptr(), groups,
+                _address(bias), _lib.ACT[act], ctypes.addressof(res), y.data_ptr(), out_dtype is _F32, ldy, _stream_now()),
+                "svdq_gemm_fp8_residual")
+            return y
         _check(load_library().svdq_gemm_fp8_grouped(qx.data_ptr(), sx.data_ptr(), M, K, qw.data_ptr(), sw.data_ptr(), N,
                                                     offsets.data_ptr(), groups, _address(bias), _lib.ACT[act],
                                                     y.data_ptr(), out_dtype is _F32, ldy, _stream_now()),
@@ -202,7 +238,7 @@ def _workspace_bytes(M, K) -> int:
     return 0 if M <= 16 and M * kb <= 256 else M * K + 4 * kb * M
 
 
-def _layer(x, qw, sw, bias, act, out_dtype, y, offsets=None):
+def _layer(x, qw, sw, bias, act, out_dtype, y, offsets=None, residual=None, gate=None):
     """The layer in one call, or None for a call that is not the usual one
     (the two passes then do it, or say what is wrong)."""
     M, K = x.shape
@@ -234,8 +270,17 @@ def _layer(x, qw, sw, bias, act, out_dtype, y, offsets=None):
             x, ldx = _aligned_copy(x), K         # in place: y is written while x is read
     if ldx < K or ldx % 8 or x.data_ptr() % 16:
         x, ldx = _aligned_copy(x), K
-    ws = x.new_empty(need, dtype=torch.uint8) if need else None
     f32 = y.dtype is _F32
+    res = None
+    if residual is not None or gate is not None:
+        res = _residual(residual, gate, M, N, y.dtype, lead, dev)
+    ws = x.new_empty(need, dtype=torch.uint8) if need else None
+    if res is not None:
+        _check(load_library().svdq_linear_fp8_residual(
+            x.data_ptr(), M, K, ldx, qw.data_ptr(), sw.data_ptr(), N, _address(offsets), lead[0] if lead else 0, _address(bias),
+            _lib.ACT[act], ctypes.addressof(res), y.data_ptr(), f32, ldy, _address(ws), need, _stream_now()),
+            "svdq_linear_fp8_residual")
+        return y
     if offsets is None:
         _check(load_library().svdq_linear_fp8(x.data_ptr(), M, K, ldx, qw.data_ptr(), sw.data_ptr(), N, _address(bias),
                                               _lib.ACT[act], y.data_ptr(), f32, ldy, _address(ws), need, _stream_now()),
@@ -269,20 +314,21 @@ class Fp8Linear:
         return cls(d["qw"], d["sw"], d.get("bias"))
 
     def __call__(self, x: torch.Tensor, act: str = "none", out_dtype=torch.bfloat16, y=None,
-                 stream=None) -> torch.Tensor:
+                 stream=None, residual=None, gate=None) -> torch.Tensor:
         """Y [M, N] for bf16 activations x [M, K]: the activation pass, then
         the product, in one call on one stream; in one launch for few rows (M
         <= 16 and M * ceil(K / 128) <= 256: single tokens, pooled
         conditioning). bf16 outputs are summed by the E4M3 matrix
-        instructions, fp32 outputs in fp32 (fp8_linear gives the difference)."""
+        instructions, fp32 outputs in fp32 (fp8_linear gives the difference).
+        residual, gate: Y = residual + gate * act(...), as fp8_linear's."""
         if x.dim() != 2 or x.shape[1] != self.K:
             raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
         with _on(x, stream):                     # (the codes are freed on the stream that reads them)
-            out = _layer(x, self.qw, self.sw, self.bias, act, out_dtype, y)
+            out = _layer(x, self.qw, self.sw, self.bias, act, out_dtype, y, None, residual, gate)
             if out is not None:
                 return out
             qx, sx = quantize_act_fp8(x)
-            return fp8_linear(qx, sx, self.qw, self.sw, self.bias, act, out_dtype, y)
+            return fp8_linear(qx, sx, self.qw, self.sw, self.bias, act, out_dtype, y, residual=residual, gate=gate)
 
 
 @dataclass
@@ -310,17 +356,18 @@ class Fp8GroupedLinear:
         return cls(d["qw"], d["sw"], d.get("bias"))
 
     def __call__(self, x: torch.Tensor, offsets: torch.Tensor, act: str = "none", out_dtype=torch.bfloat16, y=None,
-                 stream=None) -> torch.Tensor:
+                 stream=None, residual=None, gate=None) -> torch.Tensor:
         """Y [M, N] for bf16 activations x [M, K] sorted by group
         (fp8_grouped_linear's offsets); one call, one launch for few rows,
-        and the sums, as Fp8Linear."""
+        the sums and the residual, as Fp8Linear (gate [groups, N])."""
         if x.dim() != 2 or x.shape[1] != self.K:
             raise ValueError(f"x must be [M, {self.K}], got {tuple(x.shape)}")
         if _groups(offsets) != self.groups:
             raise ValueError(f"offsets must hold {self.groups + 1} values, got {offsets.numel()}")
         with _on(x, stream):
-            out = _layer(x, self.qw, self.sw, self.bias, act, out_dtype, y, offsets)
+            out = _layer(x, self.qw, self.sw, self.bias, act, out_dtype, y, offsets, residual, gate)
             if out is not None:
                 return out
             qx, sx = quantize_act_fp8(x)
-            return fp8_grouped_linear(qx, sx, offsets, self.qw, self.sw, self.bias, act, out_dtype, y)
+            return fp8_grouped_linear(qx, sx, offsets, self.qw, self.sw, self.bias, act, out_dtype, y, residual=residual,
+                                      gate=gate)

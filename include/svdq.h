@@ -605,6 +605,28 @@ svdq_status svdq_linear_fp8_grouped(const void* x, int64_t M, int64_t K, int64_t
                                     void* y, int32_t y_dtype, int64_t ldy, void* workspace, int64_t workspace_bytes,
                                     void* stream);
 
+/* svdq_gemm_fp8_residual, svdq_linear_fp8_residual -- the product and the layer
+ *   whose outputs join a residual stream,
+ *
+ *     Y[m, n] = x[m, n] + gate[g, n] act( ... + bias[n] )
+ *
+ *   in fp32, before the one rounding. residual: x [M][ld] of y_dtype (ld >= N; x may
+ *   be y with ldy: in place), gate bf16 [groups or 1][N] or NULL (ones). groups 0
+ *   (offsets NULL): the dense form, else the grouped one, whose gate is the row's
+ *   group's. The rest as svdq_gemm_fp8, svdq_linear_fp8 and their grouped forms. */
+typedef struct {
+    const void* x;
+    int64_t ld;
+    const void* gate;
+} svdq_fp8_residual;
+svdq_status svdq_gemm_fp8_residual(const void* qx, const float* sx, int64_t M, int64_t K, const void* qw, const float* sw,
+                                   int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act,
+                                   const svdq_fp8_residual* residual, void* y, int32_t y_dtype, int64_t ldy, void* stream);
+svdq_status svdq_linear_fp8_residual(const void* x, int64_t M, int64_t K, int64_t ldx, const void* qw, const float* sw,
+                                     int64_t N, const int32_t* offsets, int32_t groups, const void* bias, int32_t act,
+                                     const svdq_fp8_residual* residual, void* y, int32_t y_dtype, int64_t ldy,
+                                     void* workspace, int64_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------------
  * svdq_rope_axes -- rotary positions with several axes (time, height, width
  * of images and video) on the query and key heads of an attention block,
