@@ -97,7 +97,7 @@ DEV bool kv_find(const KvBatch& s, int item, BASE base, COUNT count, KvItem& r) 
 // tokens that a row of the table has room for
 DEV int64_t kv_room(const KvBatch& s, const KvCache& c) { return (int64_t)s.width * c.tiles * 64; }
 
-// max and sum over the four lanes that share a column (lane % 16) of a 16 x 16
+// the largest of the four lanes that share a column (lane % 16) of a 16 x 16
 // result: two exchanges of rows of 16 lanes on the vector unit
 DEV float rows4_max(float v) {
     const uint32_t x = __float_as_uint(v);
@@ -107,15 +107,6 @@ DEV float rows4_max(float v) {
     const auto b = __builtin_amdgcn_permlane16_swap(y, y, false, false);
     return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
-DEV float rows4_sum(float v) {
-    const uint32_t x = __float_as_uint(v);
-    const auto a = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const uint32_t y = __float_as_uint(v);
-    const auto b = __builtin_amdgcn_permlane16_swap(y, y, false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
 // least e with amax <= 448 * 2^e, at least kKvExpMin (amax finite, >= 0)
 DEV int kv_exponent(float amax) {
     // 448 = 1.75 * 2^8: by the exponent field, one more where the fraction is past .75

@@ -36,27 +36,19 @@ DEV v4f mfma_scores(const uint4& k0, const uint4& k1, const v8i& q, const v4f& c
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k, q, c, 0, 0, BLK, ks, 0, qs);
 }
 
-// four codes of two blocks, each with its block's scale
-DEV v8bf widen(uint32_t a, float sa, uint32_t b, float sb) {
-    const v2bf v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, sa, false);
-    const v2bf v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)a, sa, true);
-    const v2bf v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, sb, false);
-    const v2bf v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)b, sb, true);
-    return v8bf{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
-}
-
-DEV v8bf bf16x8(const v4f& a, const v4f& b) {
-    return v8bf{(__bf16)a[0], (__bf16)a[1], (__bf16)a[2], (__bf16)a[3],
-                (__bf16)b[0], (__bf16)b[1], (__bf16)b[2], (__bf16)b[3]};
-}
-
 // the bytes of w that hold a NaN code (0x7f, 0xff), 0x80 each
 DEV uint32_t nan_codes(uint32_t w) { return ~(((w & 0x7f7f7f7fu) ^ 0x7f7f7f7fu) + 0x7f7f7f7fu) & 0x80808080u; }
 
-// 0x80 marks to bf16 ones, two at a time
-DEV uint32_t ones2(uint32_t m, int at) {
-    return ((m >> (8 * at + 7)) & 1u) * 0x3f80u | ((m >> (8 * at + 15)) & 1u) * 0x3f800000u;
-}
+// a range of keys, [lo, hi)
+struct Span {
+    int lo, hi;
+};
+
+// A value that all lanes have alike, told to the compiler: quotients come from the
+// vector unit, and what follows from them (branches, addresses, buffer
+// descriptors) would stay there, with a loop around every load.
+DEV int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+DEV Span uni(const Span& s) { return Span{uni(s.lo), uni(s.hi)}; }
 
 // What a workgroup works on: rows row0 .. row0 + rows - 1 (row = token of the
 // sequence * G + head of the group) against the tiles of keys [ta, tb).
@@ -64,10 +56,7 @@ struct Work {
     int b, t0, n, len, room, row0, rows, ta, tb;
 };
 
-// Keys that row `r` of the sequence sees: [lo, hi)
-struct Span {
-    int lo, hi;
-};
+// Keys that row `r` of the sequence sees
 DEV Span span_of(const KvAttendArgs& a, const Work& w, int r) {
     const int pos = w.len - w.n + (int)((uint32_t)r / (uint32_t)a.G);
     Span s;
@@ -84,32 +73,49 @@ DEV bool find_work(const KvAttendArgs& a, int item, int split, Work& w) {
     if (!kv_find(a.s, item, [&](int o, int b) { return (int)((int64_t)o * G / R) + b; },
                  [&](int n) { return (int)(((int64_t)n * G + R - 1) / R); }, it))
         return false;
-    w.b = it.b;
-    w.t0 = it.t0;
-    w.n = it.n;
-    const int len = __builtin_amdgcn_readfirstlane(a.s.lengths[it.b]);
+    w.b = uni(it.b);
+    w.t0 = uni(it.t0);
+    w.n = uni(it.n);
+    const int len = uni(a.s.lengths[w.b]);
     w.len = len < 0 ? 0 : len;
     w.room = (int)kv_room(a.s, a.c);
-    w.row0 = it.part * R;
-    const int left = it.n * G - w.row0;
+    w.row0 = uni(it.part) * R;
+    const int left = w.n * G - w.row0;
     w.rows = left < R ? left : R;
-    const Span first = span_of(a, w, w.row0), last = span_of(a, w, w.row0 + w.rows - 1);
+    const Span first = uni(span_of(a, w, w.row0)), last = uni(span_of(a, w, w.row0 + w.rows - 1));
     const int ta = first.lo / 64, tb = (last.hi + 63) / 64, nt = tb > ta ? tb - ta : 0;
-    int per = (nt + a.S - 1) / a.S;
+    int per = uni((nt + a.S - 1) / a.S);
     if (per < a.least) per = a.least;
     w.ta = ta + split * per < ta + nt ? ta + split * per : ta + nt;
     w.tb = w.ta + per < ta + nt ? w.ta + per : ta + nt;
     return true;
 }
 
-// Up to 64 page numbers of a sequence, one a lane, for the tiles t0, t0 + step, ...
-struct Pages {
-    int mine, left;
-    DEV void load(const KvAttendArgs& a, int b, int t0, int step, int tb) {
-        const int t = t0 + step * (int)(threadIdx.x & 63);
-        mine = t < tb ? a.s.table[(int64_t)b * a.s.width + t / a.c.tiles] : -1;
+// Where the tiles t0, t0 + STEP, ... of a sequence lie, asked for in turn: up to 64
+// page numbers at a time, one a lane.
+template <int STEP>
+struct Tiles {
+    int mine, sub, next, tb;         // the lane's page; place in its page, number, and end of the next tile
+    DEV void start(const KvAttendArgs& a, int t0, int end) {
+        next = 0;
+        tb = end;
+        sub = uni(t0 % a.c.tiles);
     }
-    DEV int at(int i) const { return __builtin_amdgcn_readlane(mine, i); }
+    // the index (of 64 tokens of head h) in the cache, 0 where the tile is past the end or on no page
+    DEV int64_t take(const KvAttendArgs& a, int b, int h, int t0, bool& ok) {
+        const int t = t0 + STEP * next;
+        if ((next & 63) == 0) {
+            const int u = t + STEP * (int)(threadIdx.x & 63);
+            mine = u < tb ? a.s.table[(int64_t)b * a.s.width + u / a.c.tiles] : -1;
+        }
+        const int page = __builtin_amdgcn_readlane(mine, next & 63);
+        ok = t < tb && (uint32_t)page < (uint64_t)a.c.pages;
+        const int64_t at = ok ? ((int64_t)page * a.c.H + h) * a.c.tiles + sub : 0;
+        ++next;
+        sub += STEP;
+        while (sub >= a.c.tiles) sub -= a.c.tiles;
+        return at;
+    }
 };
 
 template <int C, int QT>
@@ -117,14 +123,15 @@ struct Flash {
     v8i qf[QT][C];                   // query operands, in the order of the products
     int qs[QT];                      // their exponents (E8M0)
     Span see[QT];
-    float m[QT], l[QT];              // maximum of the scores, the lane's sum
+    float m[QT];                     // what the scores are taken from before their exponential
+    v4f l[QT];                       // the weights' sum, four times over
     v4f o[QT][4 * C];                // O^T: channels 16 i + 4 (lane / 16) + 0..3 of the lane's query
 
     DEV void clear() {
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             m[t] = kNone;
-            l[t] = 0.0f;
+            l[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 4 * C; ++i) o[t][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         }
@@ -208,82 +215,126 @@ struct Flash {
         }
     }
 
-    // Tile of 64 keys from k0. key(blk, c), value(blk, c): the lane's 16 codes; sc: the blocks'
-    // exponents. masked: some of its keys are not seen by some query; keys outside [zlo, zhi) by none
-    // (what lies there may be anything).
-    template <class KEY, class VALUE>
-    DEV void tile(const KvAttendArgs& a, int k0, uint2 sc, bool masked, int zlo, int zhi, KEY key, VALUE value) {
-        const int g4 = ((threadIdx.x & 63) >> 4) * 4;
-        v4f s[QT][4];
-        scores<0>(s, sc.x, key);
-        scores<1>(s, sc.x, key);
-        scores<2>(s, sc.x, key);
-        scores<3>(s, sc.x, key);
-        if (masked) {
-#pragma unroll
-            for (int t = 0; t < QT; ++t)
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int k = k0 + b * 16 + g4 + r;
-                        s[t][b][r] = k >= see[t].lo && k < see[t].hi ? s[t][b][r] : -__builtin_inff();
-                    }
-        }
-        v8bf p[QT][2];
-        float alpha[QT];
-        bool rises = false;
+    // The scores' reference rises to their maximum, and the sums follow. Only where
+    // some score is more than 8 above it (in powers of two): until then weights of up
+    // to 2^8 are as exact as those of up to 1, and the sums have room. So the usual
+    // tile asks one question of the lanes' own maxima, which need not meet.
+    DEV void raise(const KvAttendArgs& a, const float (&top)[QT]) {
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-            float mx = s[t][0][0];
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) mx = fmaxf(mx, s[t][b][r]);
-            mx = fmaxf(rows4_max(mx), m[t]);
-            alpha[t] = __builtin_amdgcn_exp2f((m[t] - mx) * a.scale2);
-            rises |= mx > m[t];
+            const float mx = fmaxf(rows4_max(top[t]), m[t]);
+            const float alpha = __builtin_amdgcn_exp2f((m[t] - mx) * a.scale2);
             m[t] = mx;
-            const float off = -mx * a.scale2;
-            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) l[t][e] *= alpha;
+#pragma unroll
+            for (int i = 0; i < 4 * C; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][i][e] *= alpha;
+        }
+    }
+
+    // A tile of 64 keys from k0 goes through these in turn. key(blk, c), value(blk, c): the lane's 16
+    // codes; ks, vs: the exponents of its four blocks.
+    template <class KEY>
+    DEV void score_tile(v4f (&s)[QT][4], uint32_t ks, KEY key) const {
+        scores<0>(s, ks, key);
+        scores<1>(s, ks, key);
+        scores<2>(s, ks, key);
+        scores<3>(s, ks, key);
+    }
+
+    // some of the tile's keys are not seen by some query
+    DEV void mask(v4f (&s)[QT][4], int k0) const {
+        const int g4 = ((threadIdx.x & 63) >> 4) * 4;
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
 #pragma unroll
             for (int b = 0; b < 4; ++b)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    s[t][b][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][b][r], a.scale2, off));
-                    sum += s[t][b][r];
+                    const int k = k0 + b * 16 + g4 + r;
+                    s[t][b][r] = k >= see[t].lo && k < see[t].hi ? s[t][b][r] : -__builtin_inff();
                 }
-            l[t] = __builtin_fmaf(l[t], alpha[t], sum);
-            p[t][0] = bf16x8(s[t][0], s[t][1]);
-            p[t][1] = bf16x8(s[t][2], s[t][3]);
+    }
+
+    DEV void settle(const KvAttendArgs& a, const v4f (&s)[QT][4]) {
+        float top[QT];
+        bool rises = false;
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            top[t] = s[t][0][0];
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) top[t] = fmaxf(top[t], s[t][b][r]);
+            rises |= (top[t] - m[t]) * a.scale2 > 8.0f;
         }
-        if (__ballot(rises)) {
+        if (__ballot(rises)) raise(a, top);
+    }
+
+    // weights of two of the lane's four keys of block b, t / 2-th query
+    DEV void weight2(const KvAttendArgs& a, const v4f (&s)[QT][4], uint32_t (&p)[QT][8], int b, int i) const {
+        const int t = i >> 1, r = 2 * (i & 1);
+        const float off = -m[t] * a.scale2;
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][b][r], a.scale2, off));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][b][r + 1], a.scale2, off));
+        p[t][2 * b + (i & 1)] = bf16x2(e0, e1);
+    }
+    DEV static v8bf weight_operand(const uint32_t (&p)[8], int h) {
+        return __builtin_bit_cast(v8bf, make_uint4(p[4 * h], p[4 * h + 1], p[4 * h + 2], p[4 * h + 3]));
+    }
+
+    DEV void weights(const KvAttendArgs& a, const v4f (&s)[QT][4], uint32_t (&p)[QT][8]) const {
 #pragma unroll
-            for (int t = 0; t < QT; ++t)
+        for (int b = 0; b < 4; ++b)
 #pragma unroll
-                for (int i = 0; i < 4 * C; ++i)
+            for (int i = 0; i < 2 * QT; ++i) weight2(a, s, p, b, i);
+    }
+
+    // The next tile's scores of block BLK in the place of this one's, whose weights are formed, and
+    // beside them the weights of the next block.
+    template <int BLK, class KEY>
+    DEV void exchange(const KvAttendArgs& a, v4f (&s)[QT][4], uint32_t (&p)[QT][8], uint32_t ks, KEY key) const {
+        uint4 k[C];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[t][i][e] *= alpha[t];
-        }
-        float vs[4];
+        for (int c = 0; c < C; ++c) k[c] = key(BLK, c);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) vs[b] = __uint_as_float(((sc.y >> (8 * b)) & 0xffu) << 23);
-        uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};         // the bytes of keys that some query sees
-        if (masked) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int first = k0 + b * 16 + g4;
-                int lo = zlo - first, hi = zhi - first;
-                lo = lo < 0 ? 0 : lo > 4 ? 4 : lo;
-                hi = hi < 0 ? 0 : hi > 4 ? 4 : hi;
-                const uint32_t below_hi = hi > 3 ? ~0u : (1u << (8 * hi)) - 1u;
-                const uint32_t below_lo = lo > 3 ? ~0u : (1u << (8 * lo)) - 1u;
-                keep[b] = below_hi & ~below_lo;
+        for (int j = 0; j < QT * (C > 2 ? C : 2); ++j) {
+            const int i = C - 1 - j / QT, t = j % QT;
+            if (i >= 0) {
+                const bool pair = i + 1 < C || C % 2 == 0;
+                const v4f x = i == C - 1 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : s[t][BLK];
+                s[t][BLK] = mfma_scores<BLK>(k[pair ? i & ~1 : i], k[pair ? i | 1 : i], qf[t][i], x, (int)ks, qs[t]);
             }
+            if (BLK < 3 && j < 2 * QT) weight2(a, s, p, BLK + 1, j);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    }
+
+    // Weights of a tile from its scores, the next tile's scores in their place, block by block: one
+    // matrix instruction and a few of the vector unit in turn, which run side by side (a bf16 product
+    // of 16 cycles leaves its SIMD 8 for others, the keys' of 32 leaves 16).
+    template <class KEY>
+    DEV void exchange_tile(const KvAttendArgs& a, v4f (&s)[QT][4], uint32_t (&p)[QT][8], uint32_t ks, KEY key) const {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            uint32_t v[4][4];
+        for (int i = 0; i < 2 * QT; ++i) weight2(a, s, p, 0, i);
+        __builtin_amdgcn_sched_barrier(0);
+        exchange<0>(a, s, p, ks, key);
+        exchange<1>(a, s, p, ks, key);
+        exchange<2>(a, s, p, ks, key);
+        exchange<3>(a, s, p, ks, key);
+    }
+
+    template <class VALUE>
+    DEV void sums(uint32_t ve, const uint32_t (&p)[QT][8], VALUE value) {
+        float vs[4];
+        const uint32_t e4 = __builtin_amdgcn_readfirstlane(ve);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) vs[b] = __uint_as_float(((e4 >> (8 * b)) & 0xffu) << 23);
+        // values of 64 channels, four words of 16 rows of the operand each
+        uint32_t v[4][4];
+        auto read = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const uint4 w = value(b, c);
@@ -292,75 +343,96 @@ struct Flash {
                 v[b][2] = w.z;
                 v[b][3] = w.w;
             }
-            if (masked) {
-                uint32_t any = 0;
+        };
+        // two values of the operand of rows u: 8 make it (blocks 0 and 1, then 2 and 3)
+        auto widen2 = [&](uint32_t (&f)[8], int u, int j) __attribute__((always_inline)) {
+            const int b = j / 2;
+            f[j] = __builtin_bit_cast(uint32_t, j % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v[b][u], vs[b], true)
+                                                      : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v[b][u], vs[b], false));
+        };
+        read(0);
+        uint32_t f[2][8];
+        const uint32_t one2 = 0x3f803f80u;
+        const v8bf ones = __builtin_bit_cast(v8bf, make_uint4(one2, one2, one2, one2));
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+        for (int j = 0; j < 2 * QT; ++j) {
+            l[j % QT] = mfma_bf16_16x16x32(ones, weight_operand(p[j % QT], j / QT), l[j % QT]);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        v[b][u] &= keep[b];
-                        any |= nan_codes(v[b][u]);
-                    }
-                if (__ballot(any != 0)) nans(a, k0, c, v);
-            }
+            for (int x = 0; x < 4 / QT; ++x) widen2(f[0], 0, j * 4 / QT + x);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const v8bf v01 = widen(v[0][u], vs[0], v[1][u], vs[1]);
-                const v8bf v23 = widen(v[2][u], vs[2], v[3][u], vs[3]);
+                if (u == 3 && c + 1 < C) read(c + 1);
+                const uint32_t(&now)[8] = f[u & 1];
 #pragma unroll
-                for (int t = 0; t < QT; ++t) {
-                    o[t][c * 4 + u] = mfma_bf16_16x16x32(v01, p[t][0], o[t][c * 4 + u]);
-                    o[t][c * 4 + u] = mfma_bf16_16x16x32(v23, p[t][1], o[t][c * 4 + u]);
+                for (int j = 0; j < 2 * QT; ++j) {
+                    const int t = j % QT, h = j / QT;
+                    o[t][c * 4 + u] = mfma_bf16_16x16x32(weight_operand(now, h), weight_operand(p[t], h), o[t][c * 4 + u]);
+                    if (u < 3 || c + 1 < C) {
+#pragma unroll
+                        for (int x = 0; x < 4 / QT; ++x) widen2(f[(u + 1) & 1], (u + 1) & 3, j * 4 / QT + x);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
-        }
     }
 
-    // A tile that not every query sees whole holds NaN values: they would reach the queries that do not
-    // see them too (0 * NaN). Counted by a product of ones, they go to those that do, and leave v.
-    DEV void nans(const KvAttendArgs& a, int k0, int c, uint32_t (&v)[4][4]) {
+    // NaN values among 64 channels of a tile that not every query sees whole: a product would take them
+    // to the queries that do not see them as well (0 * NaN), so they are taken out, and the sums of those
+    // that do see them become NaN here: bf16's largest number, squared, makes them infinite, and o * 0 + o
+    // leaves what is finite.
+    DEV void nan_values(int k0, int c, const uint32_t (&v)[4][4]) {
         const int g4 = ((threadIdx.x & 63) >> 4) * 4;
-#pragma unroll 1
-        for (int u = 0; u < 4; ++u) {
-            uint32_t mark[4];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const uint32_t w = u == 0 ? v[b][0] : u == 1 ? v[b][1] : u == 2 ? v[b][2] : v[b][3];
-                mark[b] = nan_codes(w);
+        for (int t = 0; t < QT; ++t) {
+            uint32_t sees[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int k = k0 + (x >> 1) * 16 + g4 + 2 * (x & 1);
+                sees[x] = (k >= see[t].lo && k < see[t].hi ? 0x7f7fu : 0u) |
+                          (k + 1 >= see[t].lo && k + 1 < see[t].hi ? 0x7f7f0000u : 0u);
             }
-#pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                v4f n = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t wa[4], wb[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int b = 2 * h + x / 2, at = 2 * (x & 1), k = k0 + b * 16 + g4 + at;
-                        wa[x] = ones2(mark[b], at);
-                        wb[x] = (k >= see[t].lo && k < see[t].hi ? 0x3f80u : 0u) |
-                                (k + 1 >= see[t].lo && k + 1 < see[t].hi ? 0x3f800000u : 0u);
-                    }
-                    n = mfma_bf16_16x16x32(__builtin_bit_cast(v8bf, make_uint4(wa[0], wa[1], wa[2], wa[3])),
-                                           __builtin_bit_cast(v8bf, make_uint4(wb[0], wb[1], wb[2], wb[3])), n);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i == u)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[t][c * 4 + i][e] = n[e] > 0.0f ? __builtin_nanf("") : o[t][c * 4 + i][e];
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const uint32_t x = nan_codes(v[b][u]) >> 7;
-                v[b][u] &= ~(x * 0xffu);
+                uint32_t mark[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t n = nan_codes(v[x >> 1][u]) >> (16 * (x & 1));
+                    mark[x] = (n >> 7 & 1u) * 0x7f7fu | (n >> 15 & 1u) * 0x7f7f0000u;
+                }
+#pragma unroll
+                for (int i = 0; i < 4 * C; ++i) {
+                    if (i != c * 4 + u) continue;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) o[t][i] = mfma_bf16_16x16x32(weight_operand(mark, h), weight_operand(sees, h), o[t][i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[t][i][e] = __builtin_fmaf(o[t][i][e], 0.0f, o[t][i][e]);
+                }
             }
+        }
     }
 };
+
+// The bytes of a word of block b's values (tokens 4 g .. 4 g + 3 of it) whose keys lie in [lo, hi)
+DEV uint32_t kept_bytes(int k0, int b, int lo, int hi) {
+    const int first = k0 + b * 16 + ((threadIdx.x & 63) >> 4) * 4;
+    lo -= first;
+    hi -= first;
+    lo = lo < 0 ? 0 : lo > 4 ? 4 : lo;
+    hi = hi < 0 ? 0 : hi > 4 ? 4 : hi;
+    const uint32_t below_hi = hi > 3 ? ~0u : (1u << (8 * hi)) - 1u, below_lo = lo > 3 ? ~0u : (1u << (8 * lo)) - 1u;
+    return below_hi & ~below_lo;
+}
+
+DEV uint4 and4(const uint4& v, uint32_t m) { return make_uint4(v.x & m, v.y & m, v.z & m, v.w & m); }
+DEV uint32_t nan_codes4(const uint4& v) { return nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w); }
+DEV uint32_t without_nan(uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xffu); }
+DEV uint4 without_nan(const uint4& v) {
+    return make_uint4(without_nan(v.x), without_nan(v.y), without_nan(v.z), without_nan(v.w));
+}
 
 // row r of the sequence: its token and query head
 struct Row {
@@ -391,7 +463,7 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
     __shared__ float stat[4][R][2];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int split = blockIdx.x % a.S, rest = blockIdx.x / a.S, h = rest % a.c.H, item = rest / a.c.H;
+    const int rest = uni(blockIdx.x / a.S), split = blockIdx.x - rest * a.S, item = uni(rest / a.c.H), h = rest - item * a.c.H;
     Work w;
     if (!find_work<R>(a, item, split, w)) return;
     Flash<C, QT> f;
@@ -403,18 +475,14 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
         f.load_query(t, a.q + x.t * a.qts + x.h * a.qhs, a.c.D);
         f.see[t] = span_of(a, w, r);
     }
-    const Span first = span_of(a, w, w.row0), last = span_of(a, w, w.row0 + w.rows - 1);
+    const Span first = uni(span_of(a, w, w.row0)), last = uni(span_of(a, w, w.row0 + w.rows - 1));
     const int64_t tile_bytes = 8 * C * 1024;
     uint4 kr[4][C], vr[4][C];
     uint2 sc, nsc;
-    Pages pages;
     const int t0 = w.ta + wave;
     const int mine = w.tb > t0 ? (w.tb - t0 + 3) / 4 : 0;
-    auto where = [&](int i, bool& ok) __attribute__((always_inline)) {       // the wave's i-th tile
-        const int page = pages.at(i & 63), t = t0 + 4 * i;
-        ok = (uint32_t)page < (uint64_t)a.c.pages;
-        return ((int64_t)(ok ? page : 0) * a.c.H + h) * a.c.tiles + t % a.c.tiles;
-    };
+    Tiles<4> tiles;
+    tiles.start(a, t0, w.tb);
     auto load_k = [&](int64_t at) __attribute__((always_inline)) {
         const uint8_t* p = a.c.data + at * tile_bytes;
 #pragma unroll
@@ -433,8 +501,7 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
     bool ok = false;
     int64_t at = 0;
     if (mine > 0) {
-        pages.load(a, w.b, t0, 4, w.tb);
-        at = where(0, ok);
+        at = tiles.take(a, w.b, h, t0, ok);
         load_k(at);
         load_v(at);
     }
@@ -443,14 +510,43 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
         const bool masked = k0 < last.lo || k0 + 64 > first.hi;
         const bool seen = ok;
         sc = nsc;
-        // the next tile's page; past the last one, this tile again
-        if (((i + 1) & 63) == 0 && i + 1 < mine) pages.load(a, w.b, t0 + 4 * (i + 1), 4, w.tb);
-        int64_t next = at;
-        if (i + 1 < mine) next = where(i + 1, ok);
-        if (seen)
-            f.tile(a, k0, sc, masked, first.lo, last.hi, [&](int b, int c) __attribute__((always_inline)) { return kr[b][c]; },
-                   [&](int b, int c) __attribute__((always_inline)) { return vr[b][c]; });
-        at = next;
+        if (i + 1 < mine) at = tiles.take(a, w.b, h, t0, ok);
+        const auto key = [&](int b, int c) __attribute__((always_inline)) { return kr[b][c]; };
+        const auto value = [&](int b, int c) __attribute__((always_inline)) { return vr[b][c]; };
+        if (seen) {
+            v4f s[QT][4];
+            uint32_t p[QT][8];
+            f.score_tile(s, sc.x, key);
+            if (masked) {
+                f.mask(s, k0);
+                uint32_t any = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        vr[b][c] = and4(vr[b][c], kept_bytes(k0, b, first.lo, last.hi));
+                        any |= nan_codes4(vr[b][c]);
+                    }
+                if (__ballot(any != 0)) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        uint32_t v[4][4];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            v[b][0] = vr[b][c].x;
+                            v[b][1] = vr[b][c].y;
+                            v[b][2] = vr[b][c].z;
+                            v[b][3] = vr[b][c].w;
+                            vr[b][c] = without_nan(vr[b][c]);
+                        }
+                        f.nan_values(k0, c, v);
+                    }
+                }
+            }
+            f.settle(a, s);
+            f.weights(a, s, p);
+            f.sums(sc.y, p, value);
+        }
         if (i + 1 < mine) {
             load_k(at);
             load_v(at);
@@ -459,7 +555,7 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
     // the waves' maxima and sums, then their outputs 64 channels at a time
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-        const float l = rows4_sum(f.l[t]);
+        const float l = f.l[t][0];
         if (g == 0) {
             stat[wave][t * 16 + l16][0] = f.m[t];
             stat[wave][t * 16 + l16][1] = l;
@@ -508,13 +604,14 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
 
 // ---------------------------------------------------------------- many rows
 
-// 128 rows a workgroup, 32 a wave; the tiles of keys come through LDS (two
-// slots, loaded straight from memory: the cache's order is the operands'), one
-// meeting of the waves a tile.
+// 128 rows a workgroup, 32 a wave; the tiles of keys come through LDS, loaded
+// straight from memory (the cache's order is the operands'), keys a tile before
+// their values: the scores of a tile are formed beside the weights of the one
+// before, matrix work beside vector work. One meeting of the waves a tile.
 template <int C>
 __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAttendArgs a) {
-    constexpr int QT = 2, R = 128, W = 64 * C, TILE = 8 * C * 1024;
-    __shared__ __attribute__((aligned(16))) char slot0[TILE + 256], slot1[TILE + 256];
+    constexpr int QT = 2, R = 128, W = 64 * C, HALF = 4 * C * 1024;
+    __shared__ __attribute__((aligned(16))) char key0[HALF], key1[HALF], value0[HALF], value1[HALF];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // Workgroup b runs on XCD b % 8: each takes a contiguous run of the row
@@ -522,7 +619,7 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
     // later row tiles, which see more keys where order counts, go first.
     const int all = gridDim.x, x8 = blockIdx.x & 7, q8 = all >> 3, r8 = all & 7;
     const int t8 = x8 * q8 + (x8 < r8 ? x8 : r8) + (blockIdx.x >> 3);
-    const int split = t8 % a.S, rest = t8 / a.S, h = rest / a.items, item = a.items - 1 - rest % a.items;
+    const int rest = uni(t8 / a.S), split = t8 - rest * a.S, h = uni(rest / a.items), item = a.items - 1 - (rest - h * a.items);
     Work w;
     if (!find_work<R>(a, item, split, w)) return;
     Flash<C, QT> f;
@@ -536,49 +633,118 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
         f.see[t] = span_of(a, w, r);
     }
     const int rl = wr + 31 < w.rows ? wr + 31 : w.rows - 1;
-    const Span first = span_of(a, w, w.row0 + (wr < w.rows ? wr : w.rows - 1)), last = span_of(a, w, w.row0 + rl);
-    Pages pages;
+    const Span first = uni(span_of(a, w, w.row0 + (wr < w.rows ? wr : w.rows - 1))), last = uni(span_of(a, w, w.row0 + rl));
+    const Span wfirst = uni(span_of(a, w, w.row0)), wlast = uni(span_of(a, w, w.row0 + w.rows - 1));
     const int nt = w.tb - w.ta;
-    auto fetch = [&](char* s, int i) __attribute__((always_inline)) {
-        if ((i & 63) == 0) pages.load(a, w.b, w.ta + i, 1, w.tb);
-        const int page = pages.at(i & 63);
-        const bool ok = (uint32_t)page < (uint64_t)a.c.pages;
-        const int64_t at = ((int64_t)(ok ? page : 0) * a.c.H + h) * a.c.tiles + (w.ta + i) % a.c.tiles;
-        const rsrc_t rt = make_rsrc(a.c.data + at * TILE, TILE), rs = make_rsrc(a.c.scales + at * 8, 8);
+
+    Tiles<1> tiles;
+    tiles.start(a, w.ta, w.tb);
+    auto find = [&](bool& ok) __attribute__((always_inline)) { return tiles.take(a, w.b, h, w.ta, ok); };
+    // one side of a tile into LDS, a quarter a wave (zeros if it is not there)
+    auto fetch = [&](char* s, int64_t at, int side, bool ok) __attribute__((always_inline)) {
+        const rsrc_t r = make_rsrc(a.c.data + (2 * at + side) * HALF, ok ? HALF : 0);
 #pragma unroll
-        for (int k = 0; k < 2 * C; ++k) {
+        for (int k = 0; k < C; ++k) {
             const int p = (k * 4 + wave) * 1024;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rt, (lds_void*)(s + p), 16, lane * 16, p, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(s + p), 16, lane * 16, p, 0, 0);
         }
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(s + TILE), 4, lane * 4, 0, 0, 0);
-        return ok;
     };
-    bool ok = false, next = false;
-    auto step = [&](const char* s, char* other, int i) __attribute__((always_inline)) {
-        // this tile has landed, and nobody reads the other slot any more
+    auto landed = [&]() __attribute__((always_inline)) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         lds_barrier();
-        next = false;
-        if (i + 1 < nt) next = fetch(other, i + 1);
-        const int k0 = (w.ta + i) * 64;
-        if (ok && wr < w.rows && k0 < last.hi && k0 + 64 > first.lo) {
-            const bool masked = k0 < last.lo || k0 + 64 > first.hi;
-            f.tile(a, k0, *(const uint2*)(s + TILE), masked, first.lo, last.hi,
-                   [&](int b, int c) __attribute__((always_inline)) { return *(const uint4*)(s + (b * C + c) * 1024 + lane * 16); },
-                   [&](int b, int c) __attribute__((always_inline)) {
-                       return *(const uint4*)(s + TILE / 2 + (b * C + c) * 1024 + lane * 16);
-                   });
-        }
-        ok = next;
     };
-    if (nt > 0) ok = fetch(slot0, 0);
-    for (int i = 0; i < nt; i += 2) {
-        step(slot0, slot1, i);
-        if (i + 1 < nt) step(slot1, slot0, i + 1);
+    bool ok0, ok1, ok2;                                  // of tiles i, i + 1, i + 2
+    v4f s[QT][4];
+    uint2 sc0, sc1;                                      // exponents of tiles i, i + 1
+    auto codes = [&](const char* k) __attribute__((always_inline)) {
+        return [=](int b, int c) __attribute__((always_inline)) { return *(const uint4*)(k + (b * C + c) * 1024 + lane * 16); };
+    };
+    auto is_masked = [&](int i, bool ok) __attribute__((always_inline)) {
+        const int k0 = (w.ta + i) * 64;
+        return !ok || k0 < last.lo || k0 + 64 > first.hi;
+    };
+    auto hide = [&](int i, bool ok) __attribute__((always_inline)) {
+        if (is_masked(i, ok)) f.mask(s, ok ? (w.ta + i) * 64 : INT32_MIN / 2);
+        f.settle(a, s);
+    };
+    // Values of a tile that not all rows of the workgroup see whole: keys that none of them sees may
+    // hold anything, and become zeros in LDS, as do NaN values once the sums have them.
+    auto clean = [&](char* v, int k0) __attribute__((always_inline)) {
+        uint32_t any = 0;
+#pragma unroll 1
+        for (int q = 0; q < 4 * C; ++q)
+            any |= nan_codes4(and4(*(const uint4*)(v + q * 1024 + lane * 16), kept_bytes(k0, q / C, wfirst.lo, wlast.hi)));
+        if (__ballot(any != 0)) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                uint32_t x[4][4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const uint4 y = and4(codes(v)(b, c), kept_bytes(k0, b, wfirst.lo, wlast.hi));
+                    x[b][0] = y.x;
+                    x[b][1] = y.y;
+                    x[b][2] = y.z;
+                    x[b][3] = y.w;
+                }
+                f.nan_values(k0, c, x);
+            }
+        }
+        lds_barrier();
+#pragma unroll 1
+        for (int q = wave; q < 4 * C; q += 4) {
+            uint4* x = (uint4*)(v + q * 1024 + lane * 16);
+            *x = without_nan(and4(*x, kept_bytes(k0, q / C, wfirst.lo, wlast.hi)));
+        }
+        lds_barrier();
+    };
+    // Tile i, whose scores are in s: its weights, beside them the next tile's scores; then its sums.
+    int64_t at1 = 0;                                     // tile i + 1
+    auto step = [&](char* knext, char* kfree, char* v, char* vfree, int i) __attribute__((always_inline)) {
+        landed();                                        // keys of i + 1, values of i; nobody reads the others
+        const int k0 = (w.ta + i) * 64;
+        if (ok0 && (k0 < wlast.lo || k0 + 64 > wfirst.hi)) clean(v, k0);
+        const int64_t at2 = find(ok2);
+        fetch(kfree, at2, 0, ok2);
+        fetch(vfree, at1, 1, ok1);
+        const uint2 sc2 = *(const uint2*)(a.c.scales + at2 * 8);
+        if (wr < w.rows) {
+            uint32_t p[QT][8];
+            f.exchange_tile(a, s, p, sc1.x, codes(knext));
+            f.sums(sc0.y, p, codes(v));
+#pragma unroll
+            for (int t = 0; t < QT; ++t)                 // (or the compiler moves the scores behind the branch)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) order_point(s[t][b]);
+            hide(i + 1, ok1);
+        }
+        ok0 = ok1;
+        ok1 = ok2;
+        sc0 = sc1;
+        sc1 = sc2;
+        at1 = at2;
+    };
+    if (nt > 0) {
+        const int64_t at0 = find(ok0);
+        at1 = find(ok1);
+        fetch(key0, at0, 0, ok0);
+        sc0 = *(const uint2*)(a.c.scales + at0 * 8);
+        sc1 = *(const uint2*)(a.c.scales + at1 * 8);
+        landed();
+        fetch(value0, at0, 1, ok0);
+        fetch(key1, at1, 0, ok1);
+        if (wr < w.rows) {
+            f.score_tile(s, sc0.x, codes(key0));
+            hide(0, ok0);
+        }
+        for (int i = 0; i < nt; i += 2) {
+            step(key1, key0, value0, value1, i);
+            if (i + 1 < nt) step(key0, key1, value1, value0, i + 1);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); // (loads into LDS end before the workgroup does)
     }
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-        const float l = rows4_sum(f.l[t]);
+        const float l = f.l[t][0];
         const int i = wr + t * 16 + l16;
         if (i < w.rows) {
             const Row x = row_of(a, w, h, w.row0 + i);
