@@ -141,8 +141,9 @@ struct KvAttendArgs {
     int G;                           // query heads of a key head
     int causal, window;              // window 0: none
     float scale2;                    // scale * log2(e)
-    int items, S, least;             // row tiles; splits of the keys; least tiles of 64 keys a split
-    float* part;                     // S > 1: [T * heads][S][64 C] sums, then [T * heads][S][2] maximum and sum
+    int rows, items, whole;          // rows of a row tile; row tiles of a key head; those of all heads that are not split
+    int S, least;                    // splits of the others' keys; least tiles of 64 keys a split
+    float* part;                     // S > 1: [split tiles][rows][S][64 C] sums, then [..][2] references and weights' sums
 };
 
 hipError_t launch_kv_append(KvAppendArgs a, RopeArgs q, int half, int cus, hipStream_t stream);

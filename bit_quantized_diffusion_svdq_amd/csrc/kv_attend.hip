@@ -67,7 +67,7 @@ DEV Span span_of(const KvAttendArgs& a, const Work& w, int r) {
 }
 
 template <int R>
-DEV bool find_work(const KvAttendArgs& a, int item, int split, Work& w) {
+DEV bool find_work(const KvAttendArgs& a, int item, int split, int splits, Work& w) {
     KvItem it;
     const int G = a.G;
     if (!kv_find(a.s, item, [&](int o, int b) { return (int)((int64_t)o * G / R) + b; },
@@ -84,7 +84,7 @@ DEV bool find_work(const KvAttendArgs& a, int item, int split, Work& w) {
     w.rows = left < R ? left : R;
     const Span first = uni(span_of(a, w, w.row0)), last = uni(span_of(a, w, w.row0 + w.rows - 1));
     const int ta = first.lo / 64, tb = (last.hi + 63) / 64, nt = tb > ta ? tb - ta : 0;
-    int per = uni((nt + a.S - 1) / a.S);
+    int per = uni((nt + splits - 1) / splits);
     if (per < a.least) per = a.least;
     w.ta = ta + split * per < ta + nt ? ta + split * per : ta + nt;
     w.tb = w.ta + per < ta + nt ? w.ta + per : ta + nt;
@@ -295,10 +295,11 @@ struct Flash {
     // The next tile's scores of block BLK in the place of this one's, whose weights are formed, and
     // beside them the weights of the next block.
     template <int BLK, class KEY>
-    DEV void exchange(const KvAttendArgs& a, v4f (&s)[QT][4], uint32_t (&p)[QT][8], uint32_t ks, KEY key) const {
-        uint4 k[C];
+    DEV void exchange(const KvAttendArgs& a, v4f (&s)[QT][4], uint32_t (&p)[QT][8], uint32_t ks, uint4 (&k)[C], KEY key) const {
+        uint4 next[C];                                   // the next block's, on their way
 #pragma unroll
-        for (int c = 0; c < C; ++c) k[c] = key(BLK, c);
+        for (int c = 0; c < C; ++c)
+            if (BLK < 3) next[c] = key(BLK + 1, c);
 #pragma unroll
         for (int j = 0; j < QT * (C > 2 ? C : 2); ++j) {
             const int i = C - 1 - j / QT, t = j % QT;
@@ -310,47 +311,57 @@ struct Flash {
             if (BLK < 3 && j < 2 * QT) weight2(a, s, p, BLK + 1, j);
             __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (BLK < 3) k[c] = next[c];
     }
 
     // Weights of a tile from its scores, the next tile's scores in their place, block by block: one
     // matrix instruction and a few of the vector unit in turn, which run side by side (a bf16 product
     // of 16 cycles leaves its SIMD 8 for others, the keys' of 32 leaves 16).
-    template <class KEY>
-    DEV void exchange_tile(const KvAttendArgs& a, v4f (&s)[QT][4], uint32_t (&p)[QT][8], uint32_t ks, KEY key) const {
+    template <class KEY, class VALUE>
+    DEV void exchange_tile(const KvAttendArgs& a, v4f (&s)[QT][4], uint32_t (&p)[QT][8], uint32_t ks, KEY key, VALUE value,
+                           uint32_t (&v)[4][4]) const {
+        uint4 k[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) k[c] = key(0, c);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 2 * QT; ++i) weight2(a, s, p, 0, i);
         __builtin_amdgcn_sched_barrier(0);
-        exchange<0>(a, s, p, ks, key);
-        exchange<1>(a, s, p, ks, key);
-        exchange<2>(a, s, p, ks, key);
-        exchange<3>(a, s, p, ks, key);
+        exchange<0>(a, s, p, ks, k, key);
+        exchange<1>(a, s, p, ks, k, key);
+        exchange<2>(a, s, p, ks, k, key);
+        read_values(v, 0, value);                        // (on their way for sums())
+        exchange<3>(a, s, p, ks, k, key);
     }
 
+    // the lane's values of 64 channels: of four rows of the operand each, a word a block
     template <class VALUE>
-    DEV void sums(uint32_t ve, const uint32_t (&p)[QT][8], VALUE value) {
+    DEV static void read_values(uint32_t (&v)[4][4], int c, VALUE value) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint4 w = value(b, c);
+            v[b][0] = w.x;
+            v[b][1] = w.y;
+            v[b][2] = w.z;
+            v[b][3] = w.w;
+        }
+    }
+
+    // The weights' and the weighted values' sums; v: read_values(0).
+    template <class VALUE>
+    DEV void sums(uint32_t ve, const uint32_t (&p)[QT][8], VALUE value, uint32_t (&v)[4][4]) {
         float vs[4];
         const uint32_t e4 = __builtin_amdgcn_readfirstlane(ve);
 #pragma unroll
         for (int b = 0; b < 4; ++b) vs[b] = __uint_as_float(((e4 >> (8 * b)) & 0xffu) << 23);
-        // values of 64 channels, four words of 16 rows of the operand each
-        uint32_t v[4][4];
-        auto read = [&](int c) __attribute__((always_inline)) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const uint4 w = value(b, c);
-                v[b][0] = w.x;
-                v[b][1] = w.y;
-                v[b][2] = w.z;
-                v[b][3] = w.w;
-            }
-        };
         // two values of the operand of rows u: 8 make it (blocks 0 and 1, then 2 and 3)
         auto widen2 = [&](uint32_t (&f)[8], int u, int j) __attribute__((always_inline)) {
             const int b = j / 2;
             f[j] = __builtin_bit_cast(uint32_t, j % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v[b][u], vs[b], true)
                                                       : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v[b][u], vs[b], false));
         };
-        read(0);
         uint32_t f[2][8];
         const uint32_t one2 = 0x3f803f80u;
         const v8bf ones = __builtin_bit_cast(v8bf, make_uint4(one2, one2, one2, one2));
@@ -365,7 +376,7 @@ struct Flash {
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (u == 3 && c + 1 < C) read(c + 1);
+                if (u == 3 && c + 1 < C) read_values(v, c + 1, value);
                 const uint32_t(&now)[8] = f[u & 1];
 #pragma unroll
                 for (int j = 0; j < 2 * QT; ++j) {
@@ -444,11 +455,13 @@ DEV Row row_of(const KvAttendArgs& a, const Work& w, int h, int r) {
     return Row{(int64_t)w.t0 + i, h * a.G + (r - i * a.G)};
 }
 
-DEV float* part_sums(const KvAttendArgs& a, const Row& r, int split, int W) {
-    return a.part + ((r.t * (a.G * a.c.H) + r.h) * a.S + split) * W;
+// Sums and (reference, weights' sum) of row i of the n-th split row tile of R rows, by one split
+DEV float* part_sums(const KvAttendArgs& a, int n, int R, int i, int split, int W) {
+    return a.part + (((int64_t)n * R + i) * a.S + split) * W;
 }
-DEV float* part_stats(const KvAttendArgs& a, const Row& r, int split, int W) {
-    return a.part + a.s.T * (a.G * a.c.H) * (int64_t)a.S * W + ((r.t * (a.G * a.c.H) + r.h) * a.S + split) * 2;
+DEV float* part_stats(const KvAttendArgs& a, int n, int R, int i, int split, int W) {
+    const int64_t rows = ((int64_t)a.items * a.c.H - a.whole) * R;
+    return a.part + rows * a.S * W + (((int64_t)n * R + i) * a.S + split) * 2;
 }
 
 // ---------------------------------------------------------------- few rows
@@ -465,7 +478,7 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int rest = uni(blockIdx.x / a.S), split = blockIdx.x - rest * a.S, item = uni(rest / a.c.H), h = rest - item * a.c.H;
     Work w;
-    if (!find_work<R>(a, item, split, w)) return;
+    if (!find_work<R>(a, item, split, a.S, w)) return;
     Flash<C, QT> f;
     f.clear();
 #pragma unroll
@@ -545,7 +558,9 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
             }
             f.settle(a, s);
             f.weights(a, s, p);
-            f.sums(sc.y, p, value);
+            uint32_t v[4][4];
+            f.read_values(v, 0, value);
+            f.sums(sc.y, p, value, v);
         }
         if (i + 1 < mine) {
             load_k(at);
@@ -590,8 +605,8 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
                 const Row x = row_of(a, w, h, w.row0 + r);
                 const int d = c * 64 + c4;
                 if (a.S > 1) {
-                    *(v4f*)(part_sums(a, x, split, W) + d) = y;
-                    if (c == 0 && c4 == 0) *(float2*)part_stats(a, x, split, W) = make_float2(m, sum);
+                    *(v4f*)(part_sums(a, rest, R, r, split, W) + d) = y;
+                    if (c == 0 && c4 == 0) *(float2*)part_stats(a, rest, R, r, split, W) = make_float2(m, sum);
                 } else if (d < a.c.D) {
                     const float n = sum != 0.0f ? 1.0f / sum : 0.0f;
                     *(uint2*)(a.y + x.t * a.yts + x.h * a.yhs + d) =
@@ -614,14 +629,17 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
     __shared__ __attribute__((aligned(16))) char key0[HALF], key1[HALF], value0[HALF], value1[HALF];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // Workgroup b runs on XCD b % 8: each takes a contiguous run of the row
-    // tiles, key head by key head, so that those in flight share keys in its L2;
-    // later row tiles, which see more keys where order counts, go first.
-    const int all = gridDim.x, x8 = blockIdx.x & 7, q8 = all >> 3, r8 = all & 7;
-    const int t8 = x8 * q8 + (x8 < r8 ? x8 : r8) + (blockIdx.x >> 3);
-    const int rest = uni(t8 / a.S), split = t8 - rest * a.S, h = uni(rest / a.items), item = a.items - 1 - (rest - h * a.items);
+    // Row tiles in the order of the key heads, later ones, which see more keys where order counts, first.
+    // The first a.whole of them are a workgroup's each, the rest a.S workgroups'. Workgroup b runs on XCD b %
+    // 8: of either part an XCD takes a contiguous run, so that those in flight share keys in its L2.
+    const bool whole = (int)blockIdx.x < a.whole;
+    const int all = whole ? a.whole : gridDim.x - a.whole, b8 = whole ? blockIdx.x : blockIdx.x - a.whole;
+    const int x8 = b8 & 7, q8 = all >> 3, r8 = all & 7, splits = whole ? 1 : a.S;
+    const int t8 = x8 * q8 + (x8 < r8 ? x8 : r8) + (b8 >> 3);
+    const int of = uni(t8 / splits), split = t8 - of * splits, rest = whole ? of : a.whole + of;
+    const int h = uni(rest / a.items), item = a.items - 1 - (rest - h * a.items);
     Work w;
-    if (!find_work<R>(a, item, split, w)) return;
+    if (!find_work<R>(a, item, split, splits, w)) return;
     Flash<C, QT> f;
     f.clear();
     const int wr = wave * 32;                            // the wave's first row; past the end it has none
@@ -709,8 +727,9 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
         const uint2 sc2 = *(const uint2*)(a.c.scales + at2 * 8);
         if (wr < w.rows) {
             uint32_t p[QT][8];
-            f.exchange_tile(a, s, p, sc1.x, codes(knext));
-            f.sums(sc0.y, p, codes(v));
+            uint32_t v0[4][4];
+            f.exchange_tile(a, s, p, sc1.x, codes(knext), codes(v), v0);
+            f.sums(sc0.y, p, codes(v), v0);
 #pragma unroll
             for (int t = 0; t < QT; ++t)                 // (or the compiler moves the scores behind the branch)
 #pragma unroll
@@ -748,11 +767,11 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
         const int i = wr + t * 16 + l16;
         if (i < w.rows) {
             const Row x = row_of(a, w, h, w.row0 + i);
-            if (a.S > 1) {
-                float* p = part_sums(a, x, split, W);
+            if (splits > 1) {
+                float* p = part_sums(a, rest - a.whole, R, i, split, W);
 #pragma unroll
                 for (int k = 0; k < 4 * C; ++k) *(v4f*)(p + k * 16 + g * 4) = f.o[t][k];
-                if (g == 0) *(float2*)part_stats(a, x, split, W) = make_float2(f.m[t], l);
+                if (g == 0) *(float2*)part_stats(a, rest - a.whole, R, i, split, W) = make_float2(f.m[t], l);
             } else {
                 const float n = l != 0.0f ? 1.0f / l : 0.0f;
                 uint16_t* p = a.y + x.t * a.yts + x.h * a.yhs;
@@ -778,13 +797,14 @@ __global__ __launch_bounds__(256) void attend_join_kernel(KvAttendArgs a) {
     if (row >= a.s.T * heads) return;
     const int64_t t = row / heads;
     const int h = (int)(row - t * heads);
-    if (a.s.offs) {                                      // tokens of no sequence are left as they are
-        KvItem it;
-        if (!kv_find(a.s, (int)t, [](int o, int) { return o; }, [](int n) { return n; }, it)) return;
-    }
-    const Row x{t, h};
-    const float* p = part_sums(a, x, 0, W);
-    const float2 st = lane < a.S ? *(const float2*)part_stats(a, x, lane, W) : make_float2(kNone, 0.0f);
+    KvItem it;                                           // tokens of no sequence are left as they are
+    if (!kv_find(a.s, (int)t, [](int o, int) { return o; }, [](int n) { return n; }, it)) return;
+    const int kh = h / a.G, r = ((int)t - it.t0) * a.G + h - kh * a.G, of = r / a.rows, i = r - of * a.rows;
+    const int item = of + (a.s.offs ? (int)((int64_t)it.t0 * a.G / a.rows) + it.b : it.b * ((a.s.n * a.G + a.rows - 1) / a.rows));
+    const int tile = a.rows == 128 ? kh * a.items + a.items - 1 - item - a.whole : item * a.c.H + kh;     // the kernels' orders
+    if (tile < 0) return;                                   // not split
+    const float* p = part_sums(a, tile, a.rows, i, 0, W);
+    const float2 st = lane < a.S ? *(const float2*)part_stats(a, tile, a.rows, i, lane, W) : make_float2(kNone, 0.0f);
     float m = st.x;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
@@ -812,33 +832,51 @@ __global__ __launch_bounds__(256) void attend_join_kernel(KvAttendArgs a) {
 // ---------------------------------------------------------------- which kernel, how many splits
 
 struct Plan {
-    int many, qt, items, S, least;
+    int many, rows, items, whole, S, least;
 };
 
+// Few rows a sequence (up to 32, on the average): keys are split until there
+// are four workgroups a CU, at least 4 tiles each. More rows: workgroups come in
+// rounds of the CUs' places, and the row tiles of a last round that is not full are
+// split where that takes less time: a tile of 64 keys takes 1.75 us with the
+// places taken, a row tile's sums 26 ns a split and 128 channels to write and
+// read, the launch that joins them 5 us (4608 queries over 23040 keys of 24 heads:
+// 864 row tiles on 512 places).
 Plan plan_of(const KvBatch& s, const KvCache& c, int G, int cus) {
     Plan p{};
     const int64_t rows = s.T * G;
     const int64_t most = s.offs ? (rows + s.B - 1) / s.B : (int64_t)s.n * G;      // of a sequence, on the average
     p.many = most > 32;
-    p.qt = most > 16 ? 2 : 1;
-    const int R = p.many ? 128 : 16 * p.qt;
+    const int R = p.rows = p.many ? 128 : most > 16 ? 32 : 16;
     p.items = (int)(s.offs ? rows / R + s.B : s.B * (((int64_t)s.n * G + R - 1) / R));
     const int64_t groups = (int64_t)p.items * c.H, tiles = (int64_t)s.width * c.tiles;
     p.least = p.many ? 8 : 4;
-    const int64_t want = (int64_t)cus * (p.many ? 2 : 4);
-    int64_t S = groups > 0 ? (want + groups - 1) / groups : 1;
-    const int64_t top = (tiles + p.least - 1) / p.least;
-    if (S > top) S = top;
-    if (S > 64) S = 64;
-    p.S = S < 1 ? 1 : (int)S;
+    p.S = 1;
+    const int64_t top = (tiles + p.least - 1) / p.least < 64 ? (tiles + p.least - 1) / p.least : 64;
+    if (!p.many) {
+        const int64_t S = groups > 0 ? ((int64_t)cus * 4 + groups - 1) / groups : 1;
+        p.S = (int)(S < top ? S : top);
+        if (p.S < 1) p.S = 1;
+        return p;
+    }
+    const int C = (c.D + 63) / 64;
+    const int64_t places = (int64_t)cus * (C <= 2 ? 2 : 1), rest = groups % places;
+    const double tile = 1.75 * (C <= 2 ? C / 2.0 : C / 4.0), io = 0.026 * C / 2.0;
+    double least = (double)tiles * tile;                 // of the last round
+    for (int S = 2; S <= top && rest; ++S) {
+        const double t = (double)((rest * S + places - 1) / places) / S * (double)tiles * tile + (double)(rest * S) * io + 5.0;
+        if (t < least) least = t, p.S = S;
+    }
+    p.whole = (int)(p.S > 1 ? groups - rest : groups);
     return p;
 }
 
 template <int C>
 hipError_t launch(const KvAttendArgs& a, const Plan& p, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)p.items * a.c.H * p.S));
+    const int64_t groups = (int64_t)p.items * a.c.H;
+    const dim3 grid((unsigned)(p.whole + (groups - p.whole) * p.S));
     if (p.many) hipLaunchKernelGGL((attend_many_kernel<C>), grid, dim3(256), 0, stream, a);
-    else if (p.qt == 2) hipLaunchKernelGGL((attend_few_kernel<C, 2>), grid, dim3(256), 0, stream, a);
+    else if (p.rows == 32) hipLaunchKernelGGL((attend_few_kernel<C, 2>), grid, dim3(256), 0, stream, a);
     else hipLaunchKernelGGL((attend_few_kernel<C, 1>), grid, dim3(256), 0, stream, a);
     if (p.S > 1) {
         const int64_t rows = a.s.T * a.G * a.c.H;
@@ -851,12 +889,14 @@ hipError_t launch(const KvAttendArgs& a, const Plan& p, hipStream_t stream) {
 
 int64_t kv_attend_workspace(const KvBatch& s, const KvCache& c, int G, int cus) {
     const Plan p = plan_of(s, c, G, cus);
-    return p.S > 1 ? s.T * G * c.H * (int64_t)p.S * ((c.D + 63) / 64 * 64 + 2) * 4 : 0;
+    return p.S > 1 ? ((int64_t)p.items * c.H - p.whole) * p.rows * p.S * ((c.D + 63) / 64 * 64 + 2) * 4 : 0;
 }
 
 hipError_t launch_kv_attend(KvAttendArgs a, int cus, hipStream_t stream) {
     const Plan p = plan_of(a.s, a.c, a.G, cus);
     a.items = p.items;
+    a.whole = p.whole;
+    a.rows = p.rows;
     a.S = p.S;
     a.least = p.least;
     switch ((a.c.D + 63) / 64) {
