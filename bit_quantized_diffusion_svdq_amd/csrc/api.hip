@@ -1124,7 +1124,7 @@ svdq_status check_kv_cache(const svdq_kv_cache* c) {
 
 svdq_status check_kv_batch(const svdq_kv_cache* c, const svdq_kv_batch* b) {
     if (!b) return fail(SVDQ_ERR_NULL, "batch is required");
-    if (b->T < 0 || b->T >= (int64_t)1 << 30) return fail(SVDQ_ERR_SHAPE, "T = %lld must be in [0, 2^30)", (long long)b->T);
+    if (b->T < 0 || b->T >= (int64_t)1 << 24) return fail(SVDQ_ERR_SHAPE, "T = %lld must be in [0, 2^24)", (long long)b->T);
     if (b->sequences < 1 || b->sequences > 65536)
         return fail(SVDQ_ERR_SHAPE, "sequences = %d must be in [1, 65536]", b->sequences);
     if (b->width < 0 || (int64_t)b->width * c->page >= ((int64_t)1 << 31) - 64)
@@ -1161,10 +1161,15 @@ KvBatch kv_batch_of(const svdq_kv_batch* b) {
     return KvBatch{b->table, b->lengths, b->offsets, b->T, b->sequences, b->width, b->offsets ? 0 : (int)(b->T / b->sequences)};
 }
 
+int64_t kv_attend_workspace(const KvBatch& b, const KvCache& c, int G) {
+    const int rows = kv_attend_rows(b, G);
+    return rows ? kv_attend_few_workspace(b, c, G, rows, kChipCus) : kv_attend_many_workspace(b, c, G, kChipCus);
+}
+
 // query heads of a key head, or a refusal
 svdq_status check_kv_heads(const svdq_kv_cache* c, const svdq_kv_batch* b, int32_t heads, int* G) {
-    if (heads < 1 || heads > 65536 || heads % c->heads)
-        return fail(SVDQ_ERR_SHAPE, "%d query heads must be a multiple of %d key heads, at most 65536", heads, c->heads);
+    if (heads < 1 || heads > 65535 || heads % c->heads)
+        return fail(SVDQ_ERR_SHAPE, "%d query heads must be a multiple of %d key heads, at most 65535", heads, c->heads);
     *G = heads / c->heads;
     // a row tile's workgroup has at least one row, or is one more of a sequence; lanes of a launch stay below 2^32
     if (b->T * heads >= (int64_t)1 << 30 || (b->T * *G / 16 + b->sequences) * c->heads >= (int64_t)1 << 24)
@@ -1278,7 +1283,7 @@ svdq_status svdq_kv_attend_workspace_size(const svdq_kv_cache* cache, const svdq
     if ((s = check_kv_batch(cache, batch)) != SVDQ_OK) return s;
     if ((s = check_kv_heads(cache, batch, heads, &G)) != SVDQ_OK) return s;
     if (!bytes) return fail(SVDQ_ERR_NULL, "bytes is required");
-    *bytes = kv_attend_workspace(kv_batch_of(batch), kv_cache_of(cache), G, kChipCus);
+    *bytes = kv_attend_workspace(kv_batch_of(batch), kv_cache_of(cache), G);
     g_last_error.clear();
     return SVDQ_OK;
 }
@@ -1299,7 +1304,7 @@ svdq_status svdq_kv_attend(const svdq_kv_cache* cache, const svdq_kv_batch* batc
     if (window < 0) return fail(SVDQ_ERR_SHAPE, "window = %d must not be negative", window);
     const KvBatch b = kv_batch_of(batch);
     const KvCache c = kv_cache_of(cache);
-    const int64_t need = kv_attend_workspace(b, c, G, kChipCus);
+    const int64_t need = kv_attend_workspace(b, c, G);
     if (workspace_bytes < need)
         return fail(SVDQ_ERR_SHAPE, "workspace of %lld bytes, %lld are needed", (long long)workspace_bytes, (long long)need);
     if (batch->T == 0) { g_last_error.clear(); return SVDQ_OK; }
@@ -1324,7 +1329,10 @@ svdq_status svdq_kv_attend(const svdq_kv_cache* cache, const svdq_kv_batch* batc
     a.window = window;
     a.scale2 = scale * 1.4426950408889634f;
     a.part = (float*)workspace;
-    return launched(launch_kv_attend(a, kChipCus, (hipStream_t)stream), "svdq_kv_attend launch");
+    const int rows = kv_attend_rows(b, G);
+    return launched(rows ? launch_kv_attend_few(a, rows, kChipCus, (hipStream_t)stream)
+                         : launch_kv_attend_many(a, kChipCus, (hipStream_t)stream),
+                    "svdq_kv_attend launch");
 }
 
 }  // extern "C"

@@ -1,6 +1,6 @@
 // A paged cache of keys and values in 8 bits: its layout, and the sequences of
 // a call. Filled by the C ABI's host side; shared by kv_append.hip (which
-// writes the cache) and kv_attend.hip (which reads it).
+// writes the cache) and kv_attend_few.hip, kv_attend_many.hip (which read it).
 //
 // A page holds 64 `tiles` tokens of every key head; a tile (64 tokens of one
 // head) is contiguous: 4 blocks of 16 tokens of keys, then 4 of values, C =
@@ -43,11 +43,37 @@ struct KvItem {
     int b, t0, n, part;
 };
 
+// The lane's tokens of 64 sequences from b0 on: n from lo. Offsets are clamped into [0, T], and one
+// that falls counts as the largest before it (`done`, carried along), so no token belongs to two
+// sequences.
+DEV void kv_offsets(const KvBatch& s, int b0, int& done, int& lo, int& n) {
+    const int lane = threadIdx.x & 63, T = (int)s.T, b = b0 + lane;
+    int hi = 0;
+    lo = 0;
+    if (b < s.B) {
+        lo = s.offs[b];
+        hi = s.offs[b + 1];
+        lo = lo < 0 ? 0 : lo > T ? T : lo;
+        hi = hi < 0 ? 0 : hi > T ? T : hi;
+    }
+    if (__builtin_amdgcn_readfirstlane(lo) < done || __ballot(b < s.B && hi < lo)) {
+        int top = lo > done ? lo : done;                 // somewhere they fall: each becomes the largest up to it
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(top, d);
+            if (lane >= d && o > top) top = o;
+        }
+        lo = top;
+        hi = hi < lo ? lo : hi;
+    }
+    done = __builtin_amdgcn_readlane(hi, s.B - b0 < 64 ? s.B - b0 - 1 : 63);
+    n = b < s.B ? hi - lo : 0;
+}
+
 // The sequence of item `item`, found by every wave on its own, 64 sequences at
 // a time. base(o, b): the first item of sequence b whose tokens start at o;
 // count(n): items of n tokens; base(o + n, b + 1) - base(o, b) >= count(n).
-// Offsets are clamped into [0, T], and one that falls counts as the largest
-// before it, so no token belongs to two sequences. False: no such item.
+// False: no such item.
 template <class BASE, class COUNT>
 DEV bool kv_find(const KvBatch& s, int item, BASE base, COUNT count, KvItem& r) {
     if (!s.offs) {
@@ -58,35 +84,18 @@ DEV bool kv_find(const KvBatch& s, int item, BASE base, COUNT count, KvItem& r) 
         r.n = s.n;
         return r.b < s.B;
     }
-    const int lane = threadIdx.x & 63, T = (int)s.T;
     int done = 0;                                        // the largest offset so far
     for (int b0 = 0; b0 < s.B; b0 += 64) {
-        const int b = b0 + lane;
-        int lo = 0, hi = 0;
-        if (b < s.B) {
-            lo = s.offs[b];
-            hi = s.offs[b + 1];
-            lo = lo < 0 ? 0 : lo > T ? T : lo;
-            hi = hi < 0 ? 0 : hi > T ? T : hi;
-        }
-        if (__builtin_amdgcn_readfirstlane(lo) < done || __ballot(b < s.B && hi < lo)) {
-            int top = lo > done ? lo : done;             // somewhere they fall: each becomes the largest up to it
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(top, d);
-                if (lane >= d && o > top) top = o;
-            }
-            lo = top;
-            hi = hi < lo ? lo : hi;
-        }
-        done = __builtin_amdgcn_readlane(hi, s.B - b0 < 64 ? s.B - b0 - 1 : 63);
+        const int b = b0 + (threadIdx.x & 63);
+        int lo, n;
+        kv_offsets(s, b0, done, lo, n);
         const int first = base(lo, b);
-        const unsigned long long hit = __ballot(b < s.B && item >= first && item < first + count(hi - lo));
+        const unsigned long long hit = __ballot(b < s.B && item >= first && item < first + count(n));
         if (hit) {
             const int src = __builtin_ctzll(hit);
             r.b = b0 + src;
             r.t0 = __builtin_amdgcn_readlane(lo, src);
-            r.n = __builtin_amdgcn_readlane(hi, src) - r.t0;
+            r.n = __builtin_amdgcn_readlane(n, src);
             r.part = item - __builtin_amdgcn_readlane(first, src);
             return true;
         }
@@ -141,11 +150,20 @@ struct KvAttendArgs {
     int G;                           // query heads of a key head
     int causal, window;              // window 0: none
     float scale2;                    // scale * log2(e)
-    int rows, items, whole;          // rows of a row tile; row tiles of a key head; those of all heads that are not split
-    int S, least;                    // splits of the others' keys; least tiles of 64 keys a split
-    float* part;                     // S > 1: [split tiles][rows][S][64 C] sums, then [..][2] references and weights' sums
+    float* part;                     // pieces of rows: weighted sums, then references and weights' sums
+    int S;                           // splits of a split row tile; workgroups (few rows)
+    int items, whole;                // many rows: row tiles of a key head; those of all heads that are not split
 };
 
 hipError_t launch_kv_append(KvAppendArgs a, RopeArgs q, int half, int cus, hipStream_t stream);
-int64_t kv_attend_workspace(const KvBatch& s, const KvCache& c, int G, int cus);
-hipError_t launch_kv_attend(KvAttendArgs a, int cus, hipStream_t stream);
+int64_t kv_attend_few_workspace(const KvBatch& s, const KvCache& c, int G, int rows, int cus);
+int64_t kv_attend_many_workspace(const KvBatch& s, const KvCache& c, int G, int cus);
+hipError_t launch_kv_attend_few(KvAttendArgs a, int rows, int cus, hipStream_t stream);
+hipError_t launch_kv_attend_many(KvAttendArgs a, int cus, hipStream_t stream);
+
+// Query rows of a sequence (tokens * query heads of a key head), on the average, decide: up to 16
+// and 32 go to the few-rows kernel in row tiles of as many, more (0) to the other.
+static inline int kv_attend_rows(const KvBatch& s, int G) {
+    const int64_t most = s.offs ? (s.T * G + s.B - 1) / s.B : (int64_t)s.n * G;
+    return most > 32 ? 0 : most > 16 ? 32 : 16;
+}

@@ -1,0 +1,376 @@
+// svdq_kv_attend for sequences of few query rows (kv_flash.h has the mathematics):
+// the cache's bytes count. Every key is used once, straight from memory into the
+// operands; the tiles of all sequences and key heads are dealt out evenly.
+//
+// The tiles of 64 keys of one key head of a row tile are padded to a multiple of four
+// (one for each wave of a workgroup), those of all row tiles and key heads form one
+// line, and workgroup w takes the `share` tiles from w * share on, of one row tile after
+// the other. Lengths are known on the GPU only, so every workgroup adds them up for
+// itself. A row tile that crosses a border leaves sums of its pieces, joined by a second
+// launch: the first piece of a workgroup (which goes on what the one before began)
+// in slot 2 w, the last in 2 w + 1.
+#include "kv_flash.h"
+
+namespace {
+
+// a load that leaves no line behind for others (5.9 -> 6.8 TB/s over 690 MB)
+DEV uint4 load_once(const uint8_t* p) {
+    typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+    const v4u v = __builtin_nontemporal_load((const v4u*)p);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// 64 sequences at a time, one a lane, and where their tiles lie on a key head's line
+template <int R>
+struct Line {
+    int b0, done;                    // the first lane's sequence; the largest offset before it
+    int64_t before, sum;             // tiles before it, of the 64
+    int lo, n, len, ta, nt, pad;     // the lane's: first token, tokens, length, first tile of keys, tiles, padded
+    int64_t units, start;            // row tiles * pad, and where they start
+
+    DEV void restart() {
+        b0 = -64;
+        done = 0;
+        before = sum = 0;
+    }
+    DEV void next(const KvAttendArgs& a) {
+        const int lane = threadIdx.x & 63;
+        b0 += 64;
+        before += sum;
+        const int b = b0 + lane;
+        const bool in = b < a.s.B;
+        lo = n = len = 0;
+        if (in) len = a.s.lengths[b];
+        if (a.s.offs) {
+            kv_offsets(a.s, b0, done, lo, n);
+        } else if (in) {
+            lo = b * a.s.n;
+            n = a.s.n;
+        }
+        const int room = (int)kv_room(a.s, a.c);
+        len = len < 0 ? 0 : len;
+        const int hi = len < room ? len : room, from = a.window && len - n - a.window + 1 > 0 ? len - n - a.window + 1 : 0;
+        ta = from / 64;
+        nt = (hi + 63) / 64 - ta;
+        nt = nt < 0 ? 0 : nt;
+        pad = nt < 4 ? 4 : (nt + 3) & ~3;
+        units = in ? (int64_t)(((int64_t)n * a.G + R - 1) / R) * pad : 0;
+        int64_t inc = units;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = __shfl_up(inc, d);
+            if (lane >= d) inc += o;
+        }
+        start = before + inc - units;
+        sum = uni64(__shfl(inc, 63));
+    }
+    // tiles of a key head
+    DEV int64_t total(const KvAttendArgs& a) {
+        restart();
+        while (b0 + 64 < a.s.B) next(a);
+        return before + sum;
+    }
+};
+
+// A workgroup's tiles: a multiple of four
+DEV int64_t share_of(const KvAttendArgs& a, int64_t total) {
+    const int64_t all = total * a.c.H, per = (all + a.S - 1) / a.S;
+    return uni64(per <= 4 ? 4 : (per + 3) & ~(int64_t)3);
+}
+
+// Sums and (reference, weights' sum) of row i of a piece
+template <int R>
+DEV float* part_sums(const KvAttendArgs& a, int64_t slot, int i, int W) { return a.part + (slot * R + i) * W; }
+template <int R>
+DEV float* part_stats(const KvAttendArgs& a, int64_t slot, int i, int W) {
+    return a.part + 2 * (int64_t)a.S * R * W + (slot * R + i) * 2;
+}
+
+// One piece of a row tile: tiles [w.ta, w.tb) of it. slot: where its sums go; -1: it is whole.
+template <int C, int QT>
+DEV void piece(const KvAttendArgs& a, const Work& w, int h, int64_t slot, float (&red)[4][16 * QT][68], float (&stat)[4][16 * QT][2]) {
+    constexpr int R = 16 * QT, W = 64 * C;
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    Flash<C, QT> f;
+    f.clear();
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int i = t * 16 + l16, r = w.row0 + (i < w.rows ? i : w.rows - 1);
+        const Row x = row_of(a, w, h, r);
+        f.load_query(t, a.q + x.t * a.qts + x.h * a.qhs, a.c.D);
+        f.see[t] = span_of(a, w, r);
+    }
+    const Span first = uni(span_of(a, w, w.row0)), last = uni(span_of(a, w, w.row0 + w.rows - 1));
+    const int64_t tile_bytes = 8 * C * 1024;
+    uint4 kr[4][C], vr[4][C];
+    uint2 sc, nsc;
+    const int t0 = w.ta + wave;
+    const int mine = w.tb > t0 ? (w.tb - t0 + 3) / 4 : 0;
+    Tiles<4> tiles;
+    auto load_k = [&](int64_t at) __attribute__((always_inline)) {
+        const uint8_t* p = a.c.data + at * tile_bytes;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int c = 0; c < C; ++c) kr[b][c] = load_once(p + (b * C + c) * 1024 + lane * 16);
+        nsc = *(const uint2*)(a.c.scales + at * 8);
+    };
+    auto load_v = [&](int64_t at) __attribute__((always_inline)) {
+        const uint8_t* p = a.c.data + at * tile_bytes + tile_bytes / 2;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int c = 0; c < C; ++c) vr[b][c] = load_once(p + (b * C + c) * 1024 + lane * 16);
+    };
+    bool ok = false, next = false;
+    int64_t at = 0;
+    if (mine > 0) {
+        tiles.start(a, w.b, t0, w.tb);
+        at = tiles.take(a, h, ok);
+        load_k(at);
+        load_v(at);
+    }
+    const auto key = [&](int b, int c) __attribute__((always_inline)) { return kr[b][c]; };
+    const auto value = [&](int b, int c) __attribute__((always_inline)) { return vr[b][c]; };
+    for (int i = 0; i < mine; ++i) {
+        const int k0 = (t0 + 4 * i) * 64;
+        const bool masked = !ok || k0 < last.lo || k0 + 64 > first.hi;
+        sc = nsc;
+        at = tiles.take(a, h, next);            // the next tile (past the last one: any)
+        v4f s[QT][4];
+        uint32_t p[QT][8];
+        f.score_tile(s, sc.x, key);
+        __builtin_amdgcn_sched_barrier(0);
+        load_k(at);                                      // in flight while this tile is worked on
+        __builtin_amdgcn_sched_barrier(0);
+        if (masked) {
+            f.mask(s, ok ? k0 : kNowhere);
+            uint32_t any = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    vr[b][c] = and4(vr[b][c], ok ? kept_bytes(k0, b, first.lo, last.hi) : 0u);
+                    any |= nan_codes4(vr[b][c]);
+                }
+            if (__ballot(any != 0)) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    uint32_t v[4][4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        v[b][0] = vr[b][c].x;
+                        v[b][1] = vr[b][c].y;
+                        v[b][2] = vr[b][c].z;
+                        v[b][3] = vr[b][c].w;
+                        vr[b][c] = without_nan(vr[b][c]);
+                    }
+                    f.nan_values(k0, c, v);
+                }
+            }
+        }
+        f.settle(a, s);
+        f.weights(a, s, p);
+        uint32_t v[4][4];
+        f.read_values(v, 0, value);
+        f.sums(sc.y, p, value, v);
+        __builtin_amdgcn_sched_barrier(0);
+        load_v(at);
+        ok = next;
+    }
+    // the waves' maxima and sums, then their outputs 64 channels at a time
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const float l = f.l[t][0];
+        if (g == 0) {
+            stat[wave][t * 16 + l16][0] = f.m[t];
+            stat[wave][t * 16 + l16][1] = l;
+        }
+    }
+    const int row = tid >> 4, c4 = (tid & 15) * 4;       // of the joined outputs
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        if (c) __syncthreads();
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) *(v4f*)&red[wave][t * 16 + l16][u * 16 + g * 4] = f.o[t][c * 4 + u];
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            const int r = t * 16 + row;
+            float m = stat[0][r][0];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) m = fmaxf(m, stat[k][r][0]);
+            float sum = 0.0f;
+            v4f y = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float s = __builtin_amdgcn_exp2f((stat[k][r][0] - m) * a.scale2);
+                sum = __builtin_fmaf(s, stat[k][r][1], sum);
+                const v4f v = *(const v4f*)&red[k][r][c4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(s, v[e], y[e]);
+            }
+            if (r < w.rows) {
+                const Row x = row_of(a, w, h, w.row0 + r);
+                const int d = c * 64 + c4;
+                if (slot >= 0) {
+                    *(v4f*)(part_sums<R>(a, slot, r, W) + d) = y;
+                    if (c == 0 && c4 == 0) *(float2*)part_stats<R>(a, slot, r, W) = make_float2(m, sum);
+                } else if (d < a.c.D) {
+                    const float n = sum != 0.0f ? 1.0f / sum : 0.0f;
+                    *(uint2*)(a.y + x.t * a.yts + x.h * a.yhs + d) =
+                        make_uint2(bf16x2(y[0] * n, y[1] * n), bf16x2(y[2] * n, y[3] * n));
+                }
+            }
+        }
+    }
+}
+
+template <int C, int QT>
+__global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_kernel(KvAttendArgs a) {
+    constexpr int R = 16 * QT;
+    __shared__ __attribute__((aligned(16))) float red[4][R][68];
+    __shared__ float stat[4][R][2];
+    Line<R> line;
+    const int64_t total = line.total(a);
+    if (total == 0) return;
+    const int64_t share = share_of(a, total), all = total * a.c.H;
+    int64_t x = (int64_t)blockIdx.x * share;
+    const int64_t end = x + share < all ? x + share : all;
+    if (x >= end) return;
+    int h = (int)(x / total);
+    h = uni(h);
+    int64_t at = x - h * total;                          // on head h's line
+    if (a.s.B > 64) line.restart();
+    for (bool again = false; x < end; again = true) {
+        if (again) __syncthreads();                      // (the last piece's sums are read)
+        if (at >= total) {
+            at -= total;
+            ++h;
+            if (a.s.B > 64) line.restart();
+        }
+        while (at >= line.before + line.sum) line.next(a);
+        const unsigned long long hit = __ballot(at >= line.start && at < line.start + line.units);
+        const int src = __builtin_ctzll(hit);
+        const int pad = __builtin_amdgcn_readlane(line.pad, src);
+        const int64_t into = at - uni64(__shfl(line.start, src));
+        const int part = uni((int)(into / pad)), from = uni((int)(into - (int64_t)part * pad));
+        const int to = end - x < pad - from ? from + (int)(end - x) : pad;
+        Work w;
+        w.b = line.b0 + src;
+        w.t0 = __builtin_amdgcn_readlane(line.lo, src);
+        w.n = __builtin_amdgcn_readlane(line.n, src);
+        w.len = __builtin_amdgcn_readlane(line.len, src);
+        w.room = (int)kv_room(a.s, a.c);
+        w.row0 = part * R;
+        const int left = w.n * a.G - w.row0;
+        w.rows = left < R ? left : R;
+        const int ta = __builtin_amdgcn_readlane(line.ta, src), tb = ta + __builtin_amdgcn_readlane(line.nt, src);
+        w.ta = ta + from;
+        w.tb = ta + to < tb ? ta + to : tb;
+        const int64_t slot = from == 0 && to == pad ? -1 : 2 * (int64_t)blockIdx.x + (from == 0);
+        piece<C, QT>(a, w, h, slot, red, stat);
+        x += to - from;
+        at += to - from;
+    }
+}
+
+// ---------------------------------------------------------------- pieces joined
+
+// A workgroup per (token, query head): its pieces' sums, weighted by their references,
+// dealt to four waves and joined in LDS.
+template <int C, int QT>
+__global__ __launch_bounds__(256) void attend_few_join_kernel(KvAttendArgs a) {
+    constexpr int R = 16 * QT, W = 64 * C;
+    __shared__ float red[4][W], stat[4][2];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = blockIdx.x, h = blockIdx.y, kh = uni(h / a.G);
+    Line<R> line;
+    const int64_t total = line.total(a), share = share_of(a, total);
+    unsigned long long hit = 0;
+    if (a.s.B > 64) line.restart();
+    else hit = __ballot(t >= line.lo && t < line.lo + line.n);
+    while (!hit) {
+        if (line.b0 + 64 >= a.s.B) return;               // of no sequence: left as it is
+        line.next(a);
+        hit = __ballot(t >= line.lo && t < line.lo + line.n);
+    }
+    const int src = __builtin_ctzll(hit);
+    const int r = (t - __builtin_amdgcn_readlane(line.lo, src)) * a.G + h - kh * a.G, i = r % R;
+    const int pad = __builtin_amdgcn_readlane(line.pad, src);
+    const int64_t from = kh * total + uni64(__shfl(line.start, src)) + (int64_t)(r / R) * pad;
+    const int64_t w0 = uni64(from / share), w1 = uni64((from + pad - 1) / share);
+    if (w0 == w1) return;                                // one piece: written already
+    // piece 0 is the last of workgroup w0, piece j > 0 the first of w0 + j
+    const int pieces = (int)(w1 - w0) + 1;
+    auto slot = [&](int j) __attribute__((always_inline)) { return j ? 2 * (w0 + j) : 2 * w0 + 1; };
+    float m = kNone;
+    for (int j = lane; j < pieces; j += 64) m = fmaxf(m, part_stats<R>(a, slot(j), i, W)[0]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    float y[C], sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) y[c] = 0.0f;
+#pragma unroll 4
+    for (int j = wave; j < pieces; j += 4) {
+        const float2 st = *(const float2*)part_stats<R>(a, slot(j), i, W);
+        const float wgt = __builtin_amdgcn_exp2f((st.x - m) * a.scale2);
+        const float* p = part_sums<R>(a, slot(j), i, W);
+        sum = __builtin_fmaf(wgt, st.y, sum);
+#pragma unroll
+        for (int c = 0; c < C; ++c) y[c] = __builtin_fmaf(wgt, p[c * 64 + lane], y[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) red[wave][c * 64 + lane] = y[c];
+    if (lane == 0) stat[wave][0] = sum;
+    __syncthreads();
+    const float all = stat[0][0] + stat[1][0] + stat[2][0] + stat[3][0], n = all != 0.0f ? 1.0f / all : 0.0f;
+    uint16_t* out = a.y + t * a.yts + h * a.yhs;
+    for (int d = threadIdx.x; d < a.c.D; d += 256) out[d] = f32_to_bf16_bits((red[0][d] + red[1][d] + red[2][d] + red[3][d]) * n);
+}
+
+// workgroups: as many as stay on the chip at a time, or one for each four tiles if those are fewer
+int64_t shares(const KvBatch& s, const KvCache& c, int G, int rows, int cus) {
+    const int64_t pad = (((int64_t)s.width * c.tiles + 3) & ~(int64_t)3) < 4 ? 4 : ((int64_t)s.width * c.tiles + 3) & ~(int64_t)3;
+    const int64_t tiles = s.offs ? s.T * G / rows + s.B : s.B * (((int64_t)s.n * G + rows - 1) / rows);
+    const int64_t places = (int64_t)cus * ((c.D <= 128 && rows == 16) ? 2 : 1);
+    const double most = (double)tiles * c.H * (double)pad / 4.0;
+    return most < (double)places ? (int64_t)most : places;
+}
+
+template <int C, int QT>
+void launch(const KvAttendArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL((attend_few_kernel<C, QT>), dim3((unsigned)a.S), dim3(256), 0, stream, a);
+    if (a.part) hipLaunchKernelGGL((attend_few_join_kernel<C, QT>), dim3((unsigned)a.s.T, (unsigned)(a.G * a.c.H)), dim3(256), 0, stream, a);
+}
+
+template <int C>
+void launch(const KvAttendArgs& a, int rows, hipStream_t stream) {
+    if (rows == 32) launch<C, 2>(a, stream);
+    else launch<C, 1>(a, stream);
+}
+
+}  // namespace
+
+// A cache of four tiles a sequence at the most whose workgroups take four each: no piece.
+int64_t kv_attend_few_workspace(const KvBatch& s, const KvCache& c, int G, int rows, int cus) {
+    const int64_t S = shares(s, c, G, rows, cus), items = s.offs ? s.T * G / rows + s.B : s.B * (((int64_t)s.n * G + rows - 1) / rows);
+    if ((int64_t)s.width * c.tiles <= 4 && items * c.H <= S) return 0;
+    return 2 * S * rows * ((c.D + 63) / 64 * 64 + 2) * 4;
+}
+
+hipError_t launch_kv_attend_few(KvAttendArgs a, int rows, int cus, hipStream_t stream) {
+    a.S = (int)shares(a.s, a.c, a.G, rows, cus);
+    if (!kv_attend_few_workspace(a.s, a.c, a.G, rows, cus)) a.part = nullptr;
+    switch ((a.c.D + 63) / 64) {
+        case 1: launch<1>(a, rows, stream); break;
+        case 2: launch<2>(a, rows, stream); break;
+        case 3: launch<3>(a, rows, stream); break;
+        default: launch<4>(a, rows, stream);
+    }
+    return hipGetLastError();
+}

@@ -738,7 +738,7 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
  *   not shared by calls that overlap. scale > 0 and finite.
  *
  * D a multiple of 8 in [8, 256]; page in [64, 65536]; width * page < 2^31 - 64; T <
- * 2^30; sequences in [1, 65536]; window in [0, 2^31). data and workspace 16-byte
+ * 2^24; sequences in [1, 65536]; window in [0, 2^31). data and workspace 16-byte
  * aligned, scales 8, the int32 arrays 4.
  */
 typedef struct {
