@@ -1162,7 +1162,7 @@ KvBatch kv_batch_of(const svdq_kv_batch* b) {
 }
 
 int64_t kv_attend_workspace(const KvBatch& b, const KvCache& c, int G) {
-    const int rows = kv_attend_rows(b, G);
+    const int rows = kv_attend_rows(b, c.D, G);
     return rows ? kv_attend_few_workspace(b, c, G, rows, kChipCus) : kv_attend_many_workspace(b, c, G, kChipCus);
 }
 
@@ -1174,6 +1174,10 @@ svdq_status check_kv_heads(const svdq_kv_cache* c, const svdq_kv_batch* b, int32
     // a row tile's workgroup has at least one row, or is one more of a sequence; lanes of a launch stay below 2^32
     if (b->T * heads >= (int64_t)1 << 30 || (b->T * *G / 16 + b->sequences) * c->heads >= (int64_t)1 << 24)
         return fail(SVDQ_ERR_SHAPE, "T = %lld with %d heads needs more workgroups than one launch holds", (long long)b->T, heads);
+    const int rows = kv_attend_rows(kv_batch_of(b), c->D, *G);
+    if (rows && !kv_attend_few_fits(kv_batch_of(b), kv_cache_of(c), *G, rows))
+        return fail(SVDQ_ERR_SHAPE, "%d sequences of up to %lld tokens need more than 2^31 tiles of 64 keys", b->sequences,
+                    (long long)b->width * c->page);
     return SVDQ_OK;
 }
 
@@ -1329,7 +1333,7 @@ svdq_status svdq_kv_attend(const svdq_kv_cache* cache, const svdq_kv_batch* batc
     a.window = window;
     a.scale2 = scale * 1.4426950408889634f;
     a.part = (float*)workspace;
-    const int rows = kv_attend_rows(b, G);
+    const int rows = kv_attend_rows(b, c.D, G);
     return launched(rows ? launch_kv_attend_few(a, rows, kChipCus, (hipStream_t)stream)
                          : launch_kv_attend_many(a, kChipCus, (hipStream_t)stream),
                     "svdq_kv_attend launch");

@@ -156,14 +156,16 @@ struct KvAttendArgs {
 };
 
 hipError_t launch_kv_append(KvAppendArgs a, RopeArgs q, int half, int cus, hipStream_t stream);
+bool kv_attend_few_fits(const KvBatch& s, const KvCache& c, int G, int rows);
 int64_t kv_attend_few_workspace(const KvBatch& s, const KvCache& c, int G, int rows, int cus);
 int64_t kv_attend_many_workspace(const KvBatch& s, const KvCache& c, int G, int cus);
 hipError_t launch_kv_attend_few(KvAttendArgs a, int rows, int cus, hipStream_t stream);
 hipError_t launch_kv_attend_many(KvAttendArgs a, int cus, hipStream_t stream);
 
-// Query rows of a sequence (tokens * query heads of a key head), on the average, decide: up to 16
-// and 32 go to the few-rows kernel in row tiles of as many, more (0) to the other.
-static inline int kv_attend_rows(const KvBatch& s, int G) {
+// Query rows of a sequence (tokens * query heads of a key head), on the average, decide: up to 32 go to
+// the few-rows kernel, in row tiles of 16 or 32 (wide heads: 16, whose sums and operands fit the
+// registers), more (0) to the other.
+static inline int kv_attend_rows(const KvBatch& s, int D, int G) {
     const int64_t most = s.offs ? (s.T * G + s.B - 1) / s.B : (int64_t)s.n * G;
-    return most > 32 ? 0 : most > 16 ? 32 : 16;
+    return most > 32 ? 0 : most > 16 && D <= 128 ? 32 : 16;
 }

@@ -11,11 +11,12 @@
 // of the block past the last token become zeros.
 //
 // A workgroup takes one block of one sequence and some of its key heads, a
-// wave one head at a time. It works the block's cosines and sines out once, in
-// LDS. Keys: a lane holds 16 channels of one token in each 64, which is 16
+// wave the keys or the values of one head at a time. The keys' two waves work the
+// block's cosines and sines out once, in LDS, while their first head is on its
+// way. Keys: a lane holds 16 channels of one token in each 64, which is 16
 // bytes of the cache. Values: a lane holds 4 channels of 4 tokens, which is four
 // words of it; the words meet in LDS and leave 16 bytes a lane. A block is
-// written by one wave, so nothing is atomic.
+// written by its two waves, so nothing is atomic.
 #include "fp8.h"
 #include "kv.h"
 #include "rope_body.h"
@@ -40,7 +41,7 @@ DEV float fit(float x, float r) {
     return v == v ? c : v;
 }
 
-// the largest of a wave's values, in all lanes
+// the largest of a wave's values (>= 0), in all lanes
 DEV float wave_max(float v) {
     v = fmaxf(v, lane16_other<0>(v));
     v = fmaxf(v, lane16_other<1>(v));
@@ -49,12 +50,148 @@ DEV float wave_max(float v) {
     return rows4_max(v);
 }
 
+template <bool F>
+struct Finite {
+    static constexpr bool value = F;
+};
+
+// bits of a magnitude that is no infinity and no NaN in any lane of the wave
+DEV bool all_finite(uint32_t m) { return __ballot(m >= 0x7f800000u) == 0; }
+
+// four values times r to four codes. FINITE: none is an infinity or a NaN, and so none passes 448 (r is
+// the power of two that their largest allows)
+template <bool FINITE>
+DEV uint32_t codes4(float a, float b, float c, float d, float r) {
+    if constexpr (FINITE) return e4m3_x4(a * r, b * r, c * r, d * r);
+    else return e4m3_x4(fit(a, r), fit(b, r), fit(c, r), fit(d, r));
+}
+
 DEV float bf16_at(const uint32_t* w, int e) { return (e & 1) ? bf16_hi_to_f32(w[e >> 1]) : bf16_lo_to_f32(w[e >> 1]); }
+
+// Cosines and sines of the block's tokens, slots [s0, s1): a wave takes every fourth slot, a lane a
+// pair; the positions of its four slots are read at once.
+DEV void block_angles(const KvAppendArgs& a, float2* cs, int pitch, int s0, int s1, int64_t t_at0, int wave) {
+    const int lane = threadIdx.x & 63;
+    for (int p = lane; p < a.pairs; p += 64) {
+        int ax = a.axis[p];
+        const double turns = a.turns[p];
+        ax = ax < 0 ? 0 : ax >= a.axes ? a.axes - 1 : ax;
+        int bits[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + wave + 4 * i;
+            bits[i] = 0;
+            if (s < s1) bits[i] = ((const int*)a.pos)[(t_at0 + s) * a.axes + ax];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + wave + 4 * i;
+            if (s < s1) cs[s * pitch + p] = turn_of(a.pos_f32 ? (double)__int_as_float(bits[i]) : (double)bits[i], turns);
+        }
+    }
+}
+
+// The values of heads hn, hn + 2, ... of a block, by one wave: a lane has 4 channels of each 64 of its
+// four tokens, and of the cache's order a row of four words of 4 tokens.
+template <int C, class MEANWHILE>
+DEV void append_values(const KvAppendArgs& a, int page, int tile, int blk, int s0, int s1, int64_t t_at0, int hn, int hend,
+                       uint8_t (&turn)[C][4 * 272], MEANWHILE meanwhile) {
+    const int lane = threadIdx.x & 63, quad = lane >> 4, j = lane & 15, D = a.c.D;
+    uint32_t isnew = 0, isold = 0;                       // bytes of the quad's words from the call, from before
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int slot = quad * 4 + s;
+        isnew |= slot >= s0 && slot < s1 ? 0xffu << (8 * s) : 0u;
+        isold |= slot < s0 ? 0xffu << (8 * s) : 0u;
+    }
+    uint2 w[C][4];
+    uint4 old[C];
+    int e0 = kKvExpMin;
+    uint8_t *vd = a.c.data, *sc = a.c.scales;
+    auto fetch = [&](int h) __attribute__((always_inline)) {
+        const int64_t at = ((int64_t)page * a.c.H + h) * a.c.tiles + tile;
+        vd = a.c.data + at * (8 * C * 1024) + (4 + blk) * C * 1024 + lane * 16;
+        sc = a.c.scales + at * 8 + 4 + blk;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int slot = quad * 4 + s, d = c * 64 + j * 4;
+                w[c][s] = make_uint2(0u, 0u);
+                if (slot >= s0 && slot < s1 && d < D) w[c][s] = *(const uint2*)(a.v + (t_at0 + slot) * a.vts + h * a.vhs + d);
+            }
+            old[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (isold) old[c] = *(const uint4*)(vd + c * 1024);
+        }
+        if (s0 > 0) e0 = (int)sc[0] - 127;
+    };
+    if (hn < hend) fetch(hn);
+    meanwhile();
+    for (int h = hn; h < hend; h += 2) {
+        uint32_t m2 = 0;                                 // magnitudes of bf16 pairs, ordered as integers
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) m2 = max_u16x2(m2, max_u16x2(w[c][s].x & 0x7fff7fffu, w[c][s].y & 0x7fff7fffu));
+        const uint32_t m = (m2 >> 16 > (m2 & 0xffffu) ? m2 >> 16 : m2 & 0xffffu) << 16;
+        const bool finite = all_finite(m);
+        float amax = __uint_as_float(m);
+        if (!finite) {
+            amax = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint32_t x[2] = {w[c][s].x, w[c][s].y};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) amax = fmaxf(amax, finite_abs(bf16_at(x, i)));
+                }
+        }
+        int e = kv_exponent(wave_max(amax));
+        e = e < e0 ? e0 : e;
+        if (lane == 0) sc[0] = (uint8_t)(e + 127);
+        const float rv = exp2i(-e);
+        auto turned = [&](auto fin) __attribute__((always_inline)) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float t[4];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const uint32_t x[2] = {w[c][s].x, w[c][s].y};
+                        t[s] = bf16_at(x, i);
+                    }
+                    // channel 64 c + 4 j + i: row 4 (j % 4) + i of the run, word j / 4
+                    *(uint32_t*)&turn[c][quad * 272 + ((j & 3) * 4 + i) * 16 + (j >> 2) * 4] =
+                        codes4<decltype(fin)::value>(t[0], t[1], t[2], t[3], rv);
+                }
+        };
+        if (finite) turned(Finite<true>{});
+        else turned(Finite<false>{});
+        __builtin_amdgcn_wave_barrier();
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (isold == ~0u && e == e0) continue;       // four tokens from before, as they are
+            uint4 x = *(const uint4*)&turn[c][quad * 272 + j * 16];
+            x = make_uint4(x.x & isnew, x.y & isnew, x.z & isnew, x.w & isnew);
+            if (isold) {
+                uint4 o = old[c];
+                if (e != e0) o = rescale16(o, exp2i(e0 - e < -126 ? -126 : e0 - e));
+                x = make_uint4(x.x | (o.x & isold), x.y | (o.y & isold), x.z | (o.z & isold), x.w | (o.w & isold));
+            }
+            *(uint4*)(vd + c * 1024) = x;
+        }
+        __builtin_amdgcn_wave_barrier();
+        if (h + 2 < hend) fetch(h + 2);
+    }
+}
 
 template <int C, int HALF, int U>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs q) {
     __shared__ float2 cs[16 * (kPairs + 2)];             // a token's pairs, rows apart by two more
-    __shared__ __attribute__((aligned(16))) uint8_t turn[4][C][4 * 272];
+    __shared__ __attribute__((aligned(16))) uint8_t turn[2][C][4 * 272];
     static_assert(sizeof cs >= sizeof(float2) * 4 * kMaxPairs, "the queries' angles fit");
     const int blocks = a.items * a.groups;
     if ((int)blockIdx.x >= blocks) {
@@ -81,65 +218,65 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
     const int tile = (int)(first / 64 % a.c.tiles), blk = (int)(first / 16 % 4);
 
     const int P = a.pairs, pitch = P + 2;
-    for (int i = tid; i < (s1 - s0) * P; i += 256) {
-        const int s = s0 + i / P, p = i - (s - s0) * P;
-        int ax = a.axis[p];
-        ax = ax < 0 ? 0 : ax >= a.axes ? a.axes - 1 : ax;
-        const int bits = ((const int*)a.pos)[(t_at0 + s) * a.axes + ax];
-        cs[s * pitch + p] = turn_of(a.pos_f32 ? (double)__int_as_float(bits) : (double)bits, a.turns[p]);
-    }
-    __syncthreads();
-
-    const int key = lane >> 2, part = lane & 3;          // keys: the lane's token, its 16 channels of each 64
-    const int quad = lane >> 4, j = lane & 15;           // values: its 4 tokens, its 4 channels of each 64
-    const bool knew = key >= s0 && key < s1;
-    uint32_t vnew = 0, vold = 0;                         // bytes of the quad's words from the call, from before
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        const int slot = quad * 4 + s;
-        vnew |= slot >= s0 && slot < s1 ? 0xffu << (8 * s) : 0u;
-        vold |= slot < s0 ? 0xffu << (8 * s) : 0u;
-    }
     const int D = a.c.D;
     const int hend = h0 + a.per < a.c.H ? h0 + a.per : a.c.H;
-    for (int h = h0 + wave; h < hend; h += 4) {
+    const int hn = h0 + (wave >> 1);                     // the wave's heads: hn, hn + 2, ...; waves 0 and 2 their keys
+    if (wave & 1) {
+        append_values<C>(a, page, tile, blk, s0, s1, t_at0, hn, hend, turn[wave >> 1], [&]() __attribute__((always_inline)) {
+            block_angles(a, cs, pitch, s0, s1, t_at0, wave);
+            __syncthreads();                             // (with the keys' waves)
+        });
+        return;
+    }
+
+    // ---- keys
+    const int key = lane >> 2, part = lane & 3;          // the lane's token, its 16 channels of each 64
+    const bool knew = key >= s0 && key < s1;
+    uint4 kw[C][2], pw[HALF ? C : 1][2];
+    int e0 = kKvExpMin;
+    uint8_t *kd = a.c.data, *sc = a.c.scales;
+    auto fetch = [&](int h) __attribute__((always_inline)) {
         const int64_t at = ((int64_t)page * a.c.H + h) * a.c.tiles + tile;
-        uint8_t* kd = a.c.data + at * (8 * C * 1024) + blk * C * 1024 + (part * 16 + key) * 16;
-        uint8_t* vd = a.c.data + at * (8 * C * 1024) + (4 + blk) * C * 1024 + lane * 16;
-        uint8_t* sc = a.c.scales + at * 8 + blk;
-        // everything that the head needs, on its way
-        uint4 kw[C][2], pw[C][2];
-        uint2 vw[C][4];
+        kd = a.c.data + at * (8 * C * 1024) + blk * C * 1024 + (part * 16 + key) * 16;
+        sc = a.c.scales + at * 8 + blk;
         const uint16_t* kp = a.k + (t_at0 + key) * a.kts + h * a.khs;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
+        for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int d = c * 64 + part * 16 + e * 8;
-                kw[c][e] = pw[c][e] = make_uint4(0u, 0u, 0u, 0u);
+                kw[c][e] = make_uint4(0u, 0u, 0u, 0u);
                 if (knew && d < D) kw[c][e] = *(const uint4*)(kp + d);
-                if (HALF && knew) {                      // the other channels of their pairs, 4 at a time
+                if constexpr (HALF) {                    // the other channels of their pairs, 4 at a time
                     const int o0 = d < P ? d + P : d - P, o1 = d + 4 < P ? d + 4 + P : d + 4 - P;
                     uint2 x = make_uint2(0u, 0u), y = x;
-                    if (d < 2 * P) x = *(const uint2*)(kp + o0);
-                    if (d + 4 < 2 * P) y = *(const uint2*)(kp + o1);
+                    if (knew && d < 2 * P) x = *(const uint2*)(kp + o0);
+                    if (knew && d + 4 < 2 * P) y = *(const uint2*)(kp + o1);
                     pw[c][e] = make_uint4(x.x, x.y, y.x, y.y);
                 }
             }
+        if (s0 > 0) e0 = (int)sc[0] - 127;
+    };
+    if (hn < hend) fetch(hn);                            // on its way while the angles are worked out
+    block_angles(a, cs, pitch, s0, s1, t_at0, wave);
+    // the norm's weights of the lane's channels and of the others of their pairs
+    uint4 nw[C][2], mw[HALF ? C : 1][2];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int slot = quad * 4 + s, d = c * 64 + j * 4;
-                vw[c][s] = make_uint2(0u, 0u);
-                if (slot >= s0 && slot < s1 && d < D) vw[c][s] = *(const uint2*)(a.v + (t_at0 + slot) * a.vts + h * a.vhs + d);
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int d = c * 64 + part * 16 + e * 8;
+            nw[c][e] = make_uint4(0u, 0u, 0u, 0u);
+            if (a.norm && d < D) nw[c][e] = *(const uint4*)(a.norm + d);
+            if constexpr (HALF) {
+                uint2 x = make_uint2(0u, 0u), y = x;
+                if (a.norm && d < 2 * P) x = *(const uint2*)(a.norm + (d < P ? d + P : d - P));
+                if (a.norm && d + 4 < 2 * P) y = *(const uint2*)(a.norm + (d + 4 < P ? d + 4 + P : d + 4 - P));
+                mw[c][e] = make_uint4(x.x, x.y, y.x, y.y);
             }
         }
-        int ek0 = kKvExpMin, ev0 = kKvExpMin;
-        if (s0 > 0) {
-            ek0 = (int)sc[0] - 127;
-            ev0 = (int)sc[4] - 127;
-        }
-
-        // ---- keys
+    __syncthreads();
+    for (int h = hn; h < hend; h += 2) {
         float r = 1.0f;
         if (a.norm) {
             float ss = 0.0f;
@@ -153,15 +290,16 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
                 }
             ss += lane16_other<0>(ss);
             ss += lane16_other<1>(ss);
-            r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, 1.0f / (float)D, a.eps));
+            r = knew ? __builtin_amdgcn_rsqf(__builtin_fmaf(ss, 1.0f / (float)D, a.eps)) : 0.0f;
         }
-        float x[C][16], amax = 0.0f;
+        float x[C][16];
+        uint32_t m = 0;                                  // magnitudes, ordered as integers
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int f = 0; f < 4; ++f) {                // 4 channels from d
                 const int d = c * 64 + part * 16 + f * 4;
-                const uint4 ow = kw[c][f >> 1], tw = pw[c][f >> 1];
+                const uint4 ow = kw[c][f >> 1], tw = pw[HALF ? c : 0][HALF ? f >> 1 : 0];
                 const uint32_t o[2] = {f & 1 ? ow.z : ow.x, f & 1 ? ow.w : ow.y};
                 const uint32_t p[2] = {f & 1 ? tw.z : tw.x, f & 1 ? tw.w : tw.y};
                 float own[4], other[4];
@@ -171,16 +309,14 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
                     other[i] = HALF ? bf16_at(p, i) : 0.0f;
                 }
                 const bool first_half = d < P, turned = d < 2 * P;
-                if (a.norm && knew && d < D) {
-                    const uint2 nw = *(const uint2*)(a.norm + d);
-                    const uint32_t n[2] = {nw.x, nw.y};
+                if (a.norm) {                            // (zeros where there is no token or channel)
+                    const uint4 ww = nw[c][f >> 1], vw = mw[HALF ? c : 0][HALF ? f >> 1 : 0];
+                    const uint32_t n[2] = {f & 1 ? ww.z : ww.x, f & 1 ? ww.w : ww.y};
+                    const uint32_t o2[2] = {f & 1 ? vw.z : vw.x, f & 1 ? vw.w : vw.y};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) own[i] *= r * bf16_at(n, i);
-                    if (HALF && turned) {
-                        const uint2 mw = *(const uint2*)(a.norm + (first_half ? d + P : d - P));
-                        const uint32_t m[2] = {mw.x, mw.y};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) other[i] *= r * bf16_at(m, i);
+                    for (int i = 0; i < 4; ++i) {
+                        own[i] *= r * bf16_at(n, i);
+                        if (HALF) other[i] *= r * bf16_at(o2, i);
                     }
                 }
                 if (turned && knew) {
@@ -204,71 +340,37 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     x[c][f * 4 + i] = own[i];
-                    amax = fmaxf(amax, finite_abs(own[i]));
+                    const uint32_t b = __float_as_uint(own[i]) & 0x7fffffffu;
+                    m = m > b ? m : b;
                 }
             }
+        const bool finite = all_finite(m);
+        float amax = __uint_as_float(m);
+        if (!finite) {
+            amax = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(x[c][i]));
+        }
         int e = kv_exponent(wave_max(amax));
-        e = e < ek0 ? ek0 : e;
+        e = e < e0 ? e0 : e;
         if (lane == 0) sc[0] = (uint8_t)(e + 127);
         const float rk = exp2i(-e);
-        const float fk = exp2i(ek0 - e < -126 ? -126 : ek0 - e);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if (key >= s0) {                             // the call's tokens; zeros past them
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    w[i] = e4m3_x4(fit(x[c][4 * i], rk), fit(x[c][4 * i + 1], rk), fit(x[c][4 * i + 2], rk), fit(x[c][4 * i + 3], rk));
+                    w[i] = finite ? codes4<true>(x[c][4 * i], x[c][4 * i + 1], x[c][4 * i + 2], x[c][4 * i + 3], rk)
+                                  : codes4<false>(x[c][4 * i], x[c][4 * i + 1], x[c][4 * i + 2], x[c][4 * i + 3], rk);
                 *(uint4*)(kd + c * 1024) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else if (e != ek0) {
-                *(uint4*)(kd + c * 1024) = rescale16(*(const uint4*)(kd + c * 1024), fk);
+            } else if (e != e0) {
+                *(uint4*)(kd + c * 1024) = rescale16(*(const uint4*)(kd + c * 1024), exp2i(e0 - e < -126 ? -126 : e0 - e));
             }
         }
-
-        // ---- values
-        amax = 0.0f;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const uint32_t w[2] = {vw[c][s].x, vw[c][s].y};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) amax = fmaxf(amax, finite_abs(bf16_at(w, i)));
-            }
-        e = kv_exponent(wave_max(amax));
-        e = e < ev0 ? ev0 : e;
-        if (lane == 0) sc[4] = (uint8_t)(e + 127);
-        const float rv = exp2i(-e);
-        const float fv = exp2i(ev0 - e < -126 ? -126 : ev0 - e);
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float t[4];
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint32_t w[2] = {vw[c][s].x, vw[c][s].y};
-                    t[s] = fit(bf16_at(w, i), rv);
-                }
-                // channel 64 c + 4 j + i: row 4 (j % 4) + i of the run, word j / 4
-                *(uint32_t*)&turn[wave][c][quad * 272 + ((j & 3) * 4 + i) * 16 + (j >> 2) * 4] = e4m3_x4(t[0], t[1], t[2], t[3]);
-            }
-        __builtin_amdgcn_wave_barrier();
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (vold == ~0u && e == ev0) continue;       // four tokens from before, as they are
-            uint4 w = *(const uint4*)&turn[wave][c][quad * 272 + j * 16];
-            w = make_uint4(w.x & vnew, w.y & vnew, w.z & vnew, w.w & vnew);
-            if (vold) {
-                uint4 o = *(const uint4*)(vd + c * 1024);
-                if (e != ev0) o = rescale16(o, fv);
-                w = make_uint4(w.x | (o.x & vold), w.y | (o.y & vold), w.z | (o.z & vold), w.w | (o.w & vold));
-            }
-            *(uint4*)(vd + c * 1024) = w;
-        }
-        __builtin_amdgcn_wave_barrier();
+        if (h + 2 < hend) fetch(h + 2);
     }
 }
 
@@ -294,10 +396,11 @@ hipError_t launch(KvAppendArgs a, RopeArgs q, int half, int cus, hipStream_t str
 
 hipError_t launch_kv_append(KvAppendArgs a, RopeArgs q, int half, int cus, hipStream_t stream) {
     a.items = (int)(a.s.offs ? a.s.T / 16 + 2 * (int64_t)a.s.B : a.s.n > 0 ? (int64_t)a.s.B * ((a.s.n + 14) / 16 + 1) : 0);
-    // Four heads a workgroup, one a wave; more, which share the angles, once there are four
-    // workgroups a CU without.
-    a.per = 4;
-    while (a.per < a.c.H && (int64_t)a.items * ((a.c.H + 2 * a.per - 1) / (2 * a.per)) >= 4 * (int64_t)cus) a.per *= 2;
+    // Two heads a workgroup; more, which share the angles, while that leaves two workgroups a CU (8003
+    // tokens of 4 heads of 64: 14.1 us with four heads a workgroup, 16.3 with two; 4608 of 24 of 128:
+    // 31.8 with four, 32.6 with sixteen, 38.8 with two).
+    a.per = 2;
+    while (a.per < a.c.H && (int64_t)a.items * ((a.c.H + 2 * a.per - 1) / (2 * a.per)) >= 2 * (int64_t)cus) a.per *= 2;
     a.groups = (a.c.H + a.per - 1) / a.per;
     switch ((a.c.D + 63) / 64) {
         case 1: return launch<1>(a, q, half, cus, stream);

@@ -20,13 +20,24 @@ DEV uint4 load_once(const uint8_t* p) {
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// sums over the lanes up to each
+DEV int lanes_sum(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);       // one lane before, of the 16
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);       // two
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, true);       // the last of the 16 before, to rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, true);       // lane 31, to rows 2 and 3
+    return v;
+}
+
 // 64 sequences at a time, one a lane, and where their tiles lie on a key head's line
 template <int R>
 struct Line {
     int b0, done;                    // the first lane's sequence; the largest offset before it
-    int64_t before, sum;             // tiles before it, of the 64
+    int before, sum;                 // tiles before it, of the 64 (the host has seen that all of them stay below 2^31)
     int lo, n, len, ta, nt, pad;     // the lane's: first token, tokens, length, first tile of keys, tiles, padded
-    int64_t units, start;            // row tiles * pad, and where they start
+    int units, start;                // row tiles * pad, and where they start
 
     DEV void restart() {
         b0 = -64;
@@ -54,18 +65,13 @@ struct Line {
         nt = (hi + 63) / 64 - ta;
         nt = nt < 0 ? 0 : nt;
         pad = nt < 4 ? 4 : (nt + 3) & ~3;
-        units = in ? (int64_t)(((int64_t)n * a.G + R - 1) / R) * pad : 0;
-        int64_t inc = units;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t o = __shfl_up(inc, d);
-            if (lane >= d) inc += o;
-        }
+        units = in ? (n * a.G + R - 1) / R * pad : 0;
+        const int inc = lanes_sum(units);
         start = before + inc - units;
-        sum = uni64(__shfl(inc, 63));
+        sum = __builtin_amdgcn_readlane(inc, 63);
     }
     // tiles of a key head
-    DEV int64_t total(const KvAttendArgs& a) {
+    DEV int total(const KvAttendArgs& a) {
         restart();
         while (b0 + 64 < a.s.B) next(a);
         return before + sum;
@@ -73,9 +79,9 @@ struct Line {
 };
 
 // A workgroup's tiles: a multiple of four
-DEV int64_t share_of(const KvAttendArgs& a, int64_t total) {
-    const int64_t all = total * a.c.H, per = (all + a.S - 1) / a.S;
-    return uni64(per <= 4 ? 4 : (per + 3) & ~(int64_t)3);
+DEV int share_of(const KvAttendArgs& a, int total) {
+    const uint32_t per = ((uint32_t)(total * a.c.H) + a.S - 1) / (uint32_t)a.S;
+    return uni(per <= 4 ? 4 : (int)((per + 3) & ~3u));
 }
 
 // Sums and (reference, weights' sum) of row i of a piece
@@ -92,22 +98,23 @@ DEV void piece(const KvAttendArgs& a, const Work& w, int h, int64_t slot, float 
     constexpr int R = 16 * QT, W = 64 * C;
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int t0 = w.ta + wave;
+    const int mine = w.tb > t0 ? (w.tb - t0 + 3) / 4 : 0;
+    Tiles<4> tiles;
+    if (mine > 0) tiles.start(a, w.b, t0, w.tb);
     Flash<C, QT> f;
-    f.clear();
+    uint4 q[QT][2 * C];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         const int i = t * 16 + l16, r = w.row0 + (i < w.rows ? i : w.rows - 1);
         const Row x = row_of(a, w, h, r);
-        f.load_query(t, a.q + x.t * a.qts + x.h * a.qhs, a.c.D);
+        f.fetch_query(q[t], a.q + x.t * a.qts + x.h * a.qhs, a.c.D);
         f.see[t] = span_of(a, w, r);
     }
     const Span first = uni(span_of(a, w, w.row0)), last = uni(span_of(a, w, w.row0 + w.rows - 1));
     const int64_t tile_bytes = 8 * C * 1024;
     uint4 kr[4][C], vr[4][C];
     uint2 sc, nsc;
-    const int t0 = w.ta + wave;
-    const int mine = w.tb > t0 ? (w.tb - t0 + 3) / 4 : 0;
-    Tiles<4> tiles;
     auto load_k = [&](int64_t at) __attribute__((always_inline)) {
         const uint8_t* p = a.c.data + at * tile_bytes;
 #pragma unroll
@@ -126,11 +133,13 @@ DEV void piece(const KvAttendArgs& a, const Work& w, int h, int64_t slot, float 
     bool ok = false, next = false;
     int64_t at = 0;
     if (mine > 0) {
-        tiles.start(a, w.b, t0, w.tb);
         at = tiles.take(a, h, ok);
         load_k(at);
         load_v(at);
     }
+    f.clear();
+#pragma unroll
+    for (int t = 0; t < QT; ++t) f.take_query(t, q[t]);
     const auto key = [&](int b, int c) __attribute__((always_inline)) { return kr[b][c]; };
     const auto value = [&](int b, int c) __attribute__((always_inline)) { return vr[b][c]; };
     for (int i = 0; i < mine; ++i) {
@@ -235,15 +244,14 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
     __shared__ __attribute__((aligned(16))) float red[4][R][68];
     __shared__ float stat[4][R][2];
     Line<R> line;
-    const int64_t total = line.total(a);
+    const int total = line.total(a);
     if (total == 0) return;
-    const int64_t share = share_of(a, total), all = total * a.c.H;
-    int64_t x = (int64_t)blockIdx.x * share;
-    const int64_t end = x + share < all ? x + share : all;
-    if (x >= end) return;
-    int h = (int)(x / total);
-    h = uni(h);
-    int64_t at = x - h * total;                          // on head h's line
+    const int share = share_of(a, total), all = total * a.c.H;
+    if ((int64_t)blockIdx.x * share >= all) return;
+    int x = blockIdx.x * share;
+    const int end = all - x < share ? all : x + share;
+    int h = uni((uint32_t)x / (uint32_t)total);
+    int at = x - h * total;                              // on head h's line
     if (a.s.B > 64) line.restart();
     for (bool again = false; x < end; again = true) {
         if (again) __syncthreads();                      // (the last piece's sums are read)
@@ -256,9 +264,9 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
         const unsigned long long hit = __ballot(at >= line.start && at < line.start + line.units);
         const int src = __builtin_ctzll(hit);
         const int pad = __builtin_amdgcn_readlane(line.pad, src);
-        const int64_t into = at - uni64(__shfl(line.start, src));
-        const int part = uni((int)(into / pad)), from = uni((int)(into - (int64_t)part * pad));
-        const int to = end - x < pad - from ? from + (int)(end - x) : pad;
+        const int into = at - __builtin_amdgcn_readlane(line.start, src);
+        const int part = uni((uint32_t)into / (uint32_t)pad), from = into - part * pad;
+        const int to = end - x < pad - from ? from + end - x : pad;
         Work w;
         w.b = line.b0 + src;
         w.t0 = __builtin_amdgcn_readlane(line.lo, src);
@@ -290,7 +298,7 @@ __global__ __launch_bounds__(256) void attend_few_join_kernel(KvAttendArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = blockIdx.x, h = blockIdx.y, kh = uni(h / a.G);
     Line<R> line;
-    const int64_t total = line.total(a), share = share_of(a, total);
+    const int total = line.total(a), share = share_of(a, total);
     unsigned long long hit = 0;
     if (a.s.B > 64) line.restart();
     else hit = __ballot(t >= line.lo && t < line.lo + line.n);
@@ -302,12 +310,12 @@ __global__ __launch_bounds__(256) void attend_few_join_kernel(KvAttendArgs a) {
     const int src = __builtin_ctzll(hit);
     const int r = (t - __builtin_amdgcn_readlane(line.lo, src)) * a.G + h - kh * a.G, i = r % R;
     const int pad = __builtin_amdgcn_readlane(line.pad, src);
-    const int64_t from = kh * total + uni64(__shfl(line.start, src)) + (int64_t)(r / R) * pad;
-    const int64_t w0 = uni64(from / share), w1 = uni64((from + pad - 1) / share);
+    const uint32_t from = kh * total + __builtin_amdgcn_readlane(line.start, src) + r / R * pad;
+    const int w0 = uni(from / (uint32_t)share), w1 = uni((from + pad - 1) / (uint32_t)share);
     if (w0 == w1) return;                                // one piece: written already
     // piece 0 is the last of workgroup w0, piece j > 0 the first of w0 + j
-    const int pieces = (int)(w1 - w0) + 1;
-    auto slot = [&](int j) __attribute__((always_inline)) { return j ? 2 * (w0 + j) : 2 * w0 + 1; };
+    const int pieces = w1 - w0 + 1;
+    auto slot = [&](int j) __attribute__((always_inline)) { return (int64_t)(j ? 2 * (w0 + j) : 2 * w0 + 1); };
     float m = kNone;
     for (int j = lane; j < pieces; j += 64) m = fmaxf(m, part_stats<R>(a, slot(j), i, W)[0]);
 #pragma unroll
@@ -333,6 +341,14 @@ __global__ __launch_bounds__(256) void attend_few_join_kernel(KvAttendArgs a) {
     for (int d = threadIdx.x; d < a.c.D; d += 256) out[d] = f32_to_bf16_bits((red[0][d] + red[1][d] + red[2][d] + red[3][d]) * n);
 }
 
+// whether the tiles of all row tiles and key heads can be numbered
+}  // namespace
+bool kv_attend_few_fits(const KvBatch& s, const KvCache& c, int G, int rows) {
+    const int64_t tiles = s.offs ? s.T * G / rows + s.B : s.B * (((int64_t)s.n * G + rows - 1) / rows);
+    return (double)tiles * c.H * ((double)s.width * c.tiles + 4.0) < 2147483648.0;
+}
+namespace {
+
 // workgroups: as many as stay on the chip at a time, or one for each four tiles if those are fewer
 int64_t shares(const KvBatch& s, const KvCache& c, int G, int rows, int cus) {
     const int64_t pad = (((int64_t)s.width * c.tiles + 3) & ~(int64_t)3) < 4 ? 4 : ((int64_t)s.width * c.tiles + 3) & ~(int64_t)3;
@@ -350,8 +366,9 @@ void launch(const KvAttendArgs& a, hipStream_t stream) {
 
 template <int C>
 void launch(const KvAttendArgs& a, int rows, hipStream_t stream) {
-    if (rows == 32) launch<C, 2>(a, stream);
-    else launch<C, 1>(a, stream);
+    if constexpr (C <= 2)
+        if (rows == 32) return launch<C, 2>(a, stream);
+    launch<C, 1>(a, stream);
 }
 
 }  // namespace

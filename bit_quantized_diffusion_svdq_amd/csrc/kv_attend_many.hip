@@ -73,7 +73,9 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
     for (int t = 0; t < QT; ++t) {
         const int i = wr + t * 16 + l16, r = w.row0 + (i < w.rows ? i : w.rows - 1);
         const Row x = row_of(a, w, h, r);
-        f.load_query(t, a.q + x.t * a.qts + x.h * a.qhs, a.c.D);
+        uint4 q[2 * C];
+        f.fetch_query(q, a.q + x.t * a.qts + x.h * a.qhs, a.c.D);
+        f.take_query(t, q);
         f.see[t] = span_of(a, w, r);
     }
     const int rl = wr + 31 < w.rows ? wr + 31 : w.rows - 1;

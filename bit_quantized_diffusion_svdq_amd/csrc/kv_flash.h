@@ -51,9 +51,6 @@ struct Span {
 // vector unit, and what follows from them (branches, addresses, buffer
 // descriptors) would stay there, with a loop around every load.
 DEV int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
-DEV int64_t uni64(int64_t x) {
-    return ((int64_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x);
-}
 DEV Span uni(const Span& s) { return Span{uni(s.lo), uni(s.hi)}; }
 
 // What a workgroup works on: rows row0 .. row0 + rows - 1 (row = token of the
@@ -126,29 +123,35 @@ struct Flash {
         }
     }
 
-    // The lane's 16 C channels of a query (16 (lane / 16) + 0..15 of each 64; p NULL: zeros) as two
-    // E4M3 numbers each. A query with an infinity or a NaN becomes NaN.
-    DEV void load_query(int t, const uint16_t* p, int D) {
+    // The lane's 16 C channels of a query: 16 (lane / 16) + 0..15 of each 64
+    DEV static void fetch_query(uint4 (&q)[2 * C], const uint16_t* p, int D) {
         const int g = (threadIdx.x & 63) >> 4;
-        float v[16 * C];
-        float amax = 0.0f, odd = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int d = c * 64 + g * 16 + h * 8;
-                uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                if (p && d < D) w = *(const uint4*)(p + d);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float x = (e & 1) ? bf16_hi_to_f32(u[e >> 1]) : bf16_lo_to_f32(u[e >> 1]);
-                    const float ax = fabsf(x);
-                    v[c * 16 + h * 8 + e] = x;
-                    if (ax < __builtin_inff()) amax = fmaxf(amax, ax);
-                    else odd = 1.0f;
-                }
+                q[2 * c + h] = make_uint4(0u, 0u, 0u, 0u);
+                if (d < D) q[2 * c + h] = *(const uint4*)(p + d);
             }
+    }
+
+    // as two E4M3 numbers each. A query with an infinity or a NaN becomes NaN.
+    DEV void take_query(int t, const uint4 (&q)[2 * C]) {
+        float v[16 * C];
+        float amax = 0.0f, odd = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 2 * C; ++c) {
+            const uint32_t u[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = (e & 1) ? bf16_hi_to_f32(u[e >> 1]) : bf16_lo_to_f32(u[e >> 1]);
+                const float ax = fabsf(x);
+                v[c * 8 + e] = x;
+                if (ax < __builtin_inff()) amax = fmaxf(amax, ax);
+                else odd = 1.0f;
+            }
+        }
         amax = rows4_max(amax);
         odd = rows4_max(odd);
         const int e = kv_exponent(amax);

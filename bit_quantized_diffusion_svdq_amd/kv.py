@@ -20,19 +20,33 @@ import torch
 from . import _lib
 from ._lib import KvBatchDesc, KvCacheDesc, RopeHeads, _check, _require, load_library
 from .fp8 import _on, _stream_now
-from .rope import PAIRING, RopePlan, _strides
+from .rope import PAIRING, RopePlan
 
 _BF16, _I32 = torch.bfloat16, torch.int32
+_NO_TURN = (None, 0, 1, None, None, 0, 0)
 
 
 def _heads_of(x, name, T, D):
-    """(heads, token stride, head stride) of a source or an output [T, heads, D]."""
-    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or x.dtype is not _BF16:
-        raise ValueError(f"{name} must be bf16 [{T}, heads, {D}], got {tuple(x.shape)} {x.dtype}")
-    if x.stride(2) != 1:
+    """(heads, token stride, head stride) of a source or an output [T, heads, D]; an axis of one
+    element has no stride of its own."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or x.dtype is not _BF16:
+        raise ValueError(f"{name} must be bf16 [{T}, heads, {D}], got {tuple(shape)} {x.dtype}")
+    ts, hs, es = x.stride()
+    if es != 1:
         raise ValueError(f"{name} must have contiguous heads (stride(2) == 1)")
-    H = x.shape[1]
-    return (H, *_strides(x, T, H, D))
+    H = shape[1]
+    if H == 1:
+        hs = D
+    return H, (ts if T > 1 else H * hs), hs
+
+
+def _norm_at(name, w, D, dev):
+    if not (w.dtype is _BF16 and w.shape == (D,) and w.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous bf16 vector of {D} values")
+    if w.device != dev:
+        raise ValueError(f"{name} is on {w.device}, the cache on {dev}")
+    return w.data_ptr()
 
 
 class KVCache:
@@ -72,8 +86,7 @@ class KVCache:
                                  self.page_size)
         self._at = ctypes.addressof(self._desc)
 
-    def _batch(self, T, table, lengths, offsets):
-        dev = self.data.device
+    def _batch(self, T, table, lengths, offsets, dev):
         if not (table.dtype is _I32 and table.dim() == 2 and table.shape[0] >= 1 and table.is_contiguous()):
             raise ValueError(f"table must be contiguous int32 [sequences, width], got {tuple(table.shape)} {table.dtype}")
         B, width = table.shape
@@ -105,55 +118,57 @@ class KVCache:
         if k.dim() != 3:
             raise ValueError(f"k must be [T, {self.kv_heads}, {D}], got {tuple(k.shape)}")
         T = k.shape[0]
-        if torch.is_grad_enabled() and (k.requires_grad or v.requires_grad or (q is not None and q.requires_grad)):
+        if (k.requires_grad or v.requires_grad or (q is not None and q.requires_grad)) and torch.is_grad_enabled():
             raise ValueError("k, v or q requires a gradient, which this call does not record: call it under torch.no_grad() "
                              "or on detached tensors")
-        sides = []
-        for name, x in (("k", k), ("v", v)):
-            H, ts, hs = _heads_of(x, name, T, D)
-            if H != self.kv_heads:
-                raise ValueError(f"{name} has {H} heads, the cache {self.kv_heads}")
-            sides.append((ts, hs))
-        if (pos is None) != (plan is None):
-            raise ValueError("pos and plan belong together")
-        f32_pos = False
-        if plan is not None:
+        kh, kts, khs = _heads_of(k, "k", T, D)
+        vh, vts, vhs = _heads_of(v, "v", T, D)
+        if kh != self.kv_heads or vh != kh:
+            raise ValueError(f"k has {kh} heads and v {vh}, the cache {self.kv_heads}")
+        if plan is None:
+            if pos is not None:
+                raise ValueError("pos and plan belong together")
+            turn = _NO_TURN
+        else:
+            if pos is None:
+                raise ValueError("pos and plan belong together")
             if plan.head_dim != D:
                 raise ValueError(f"the plan turns heads of {plan.head_dim}, the cache holds {D}")
             f32_pos = pos.dtype is torch.float32
             if not ((f32_pos or pos.dtype is _I32) and pos.shape == (T, plan.axes) and pos.is_contiguous()):
                 raise ValueError(f"pos must be contiguous int32 or fp32 [{T}, {plan.axes}], got {tuple(pos.shape)} {pos.dtype}")
-        if q is None and (q_norm is not None or q_out is not None):
-            raise ValueError("q_norm and q_out need q")
-        for name, w in (("k_norm", k_norm), ("q_norm", q_norm)):
-            if w is not None and not (w.dtype is _BF16 and w.shape == (D,) and w.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous bf16 vector of {D} values")
-        batch = self._batch(T, table, lengths, offsets)
-        for t in (k, v, q, pos, k_norm, q_norm, q_out, None if plan is None else plan.turns):
-            if t is not None and t.device != dev:
-                raise ValueError(f"a tensor of the call is on {t.device}, the cache on {dev}")
+            if pos.device != dev or plan.turns.device != dev:
+                raise ValueError(f"pos is on {pos.device}, the plan on {plan.turns.device}, the cache on {dev}")
+            turn = (pos.data_ptr(), f32_pos, plan.axes, plan.turns.data_ptr(), plan.axis.data_ptr(), plan.pairs,
+                    PAIRING[plan.pairing])
+        batch = self._batch(T, table, lengths, offsets, dev)
+        if k.device != dev or v.device != dev:
+            raise ValueError(f"k is on {k.device}, v on {v.device}, the cache on {dev}")
+        k_norm = None if k_norm is None else _norm_at("k_norm", k_norm, D, dev)
+        qs = q_at = None
         if q is not None:
             qh, qts, qhs = _heads_of(q, "q", T, D)
             if qh < 1:
                 raise ValueError("q must have at least one head")
+            yts, yhs = qh * D, D
             if q_out is not None:
                 yh, yts, yhs = _heads_of(q_out, "q_out", T, D)
                 if yh != qh:
                     raise ValueError(f"q_out must have {qh} heads, got {yh}")
+            if q.device != dev or (q_out is not None and q_out.device != dev):
+                raise ValueError(f"q or q_out is not on {dev}")
+            q_norm = None if q_norm is None else _norm_at("q_norm", q_norm, D, dev)
+        elif q_norm is not None or q_out is not None:
+            raise ValueError("q_norm and q_out need q")
         with _on(k, stream):
-            qs = None
             if q is not None:
                 if q_out is None:
-                    q_out, yts, yhs = q.new_empty(T, qh, D), qh * D, D
-                qs = RopeHeads(q.data_ptr(), qts, qhs, qh, None if q_norm is None else q_norm.data_ptr(), q_out.data_ptr(),
-                               yts, yhs)
-            ks = RopeHeads(k.data_ptr(), *sides[0], self.kv_heads, None if k_norm is None else k_norm.data_ptr())
-            vs = RopeHeads(v.data_ptr(), *sides[1], self.kv_heads)
-            turn = (None, 0, 1, None, None, 0, 0) if plan is None else (
-                pos.data_ptr(), f32_pos, plan.axes, plan.turns.data_ptr(), plan.axis.data_ptr(), plan.pairs,
-                PAIRING[plan.pairing])
-            _check(load_library().svdq_kv_append(self._at, ctypes.addressof(batch),
-                                                 None if qs is None else ctypes.addressof(qs), ctypes.addressof(ks),
+                    q_out = q.new_empty(T, qh, D)
+                qs = RopeHeads(q.data_ptr(), qts, qhs, qh, q_norm, q_out.data_ptr(), yts, yhs)
+                q_at = ctypes.addressof(qs)
+            ks = RopeHeads(k.data_ptr(), kts, khs, kh, k_norm)
+            vs = RopeHeads(v.data_ptr(), vts, vhs, vh)
+            _check(load_library().svdq_kv_append(self._at, ctypes.addressof(batch), q_at, ctypes.addressof(ks),
                                                  ctypes.addressof(vs), *turn, eps, _stream_now()), "svdq_kv_append")
         return q_out
 
@@ -184,7 +199,7 @@ class KVCache:
             raise ValueError(f"scale must be positive and finite, got {scale}")
         if not 0 <= window < 1 << 31:
             raise ValueError(f"window must be in [0, 2^31), got {window}")
-        batch = self._batch(T, table, lengths, offsets)
+        batch = self._batch(T, table, lengths, offsets, dev)
         yts, yhs = H * D, D
         if out is not None:
             yh, yts, yhs = _heads_of(out, "out", T, D)

@@ -738,7 +738,9 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
  *   not shared by calls that overlap. scale > 0 and finite.
  *
  * D a multiple of 8 in [8, 256]; page in [64, 65536]; width * page < 2^31 - 64; T <
- * 2^24; sequences in [1, 65536]; window in [0, 2^31). data and workspace 16-byte
+ * 2^24; sequences in [1, 65536]; window in [0, 2^31); for svdq_kv_attend T * heads <
+ * 2^30, and the row tiles of 16 or 32 query rows of all sequences and key heads times
+ * width * page / 64 below 2^31 where a sequence has 32 rows at the most. data and workspace 16-byte
  * aligned, scales 8, the int32 arrays 4.
  */
 typedef struct {
