@@ -132,6 +132,7 @@ DEV void piece(const KvAttendArgs& a, const Work& w, int h, int64_t slot, float 
     };
     bool ok = false, next = false;
     int64_t at = 0;
+    uint32_t nans = 0;
     if (mine > 0) {
         at = tiles.take(a, h, ok);
         load_k(at);
@@ -155,29 +156,14 @@ DEV void piece(const KvAttendArgs& a, const Work& w, int h, int64_t slot, float 
         __builtin_amdgcn_sched_barrier(0);
         if (masked) {
             f.mask(s, ok ? k0 : kNowhere);
-            uint32_t any = 0;
 #pragma unroll
             for (int b = 0; b < 4; ++b)
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
+                for (int c = 0; c < C; ++c) {            // (NaN values are seen to in the end)
                     vr[b][c] = and4(vr[b][c], ok ? kept_bytes(k0, b, first.lo, last.hi) : 0u);
-                    any |= nan_codes4(vr[b][c]);
+                    nans |= nan_codes4(vr[b][c]);
+                    vr[b][c] = without_nan(vr[b][c]);
                 }
-            if (__ballot(any != 0)) {
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    uint32_t v[4][4];
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        v[b][0] = vr[b][c].x;
-                        v[b][1] = vr[b][c].y;
-                        v[b][2] = vr[b][c].z;
-                        v[b][3] = vr[b][c].w;
-                        vr[b][c] = without_nan(vr[b][c]);
-                    }
-                    f.nan_values(k0, c, v);
-                }
-            }
         }
         f.settle(a, s);
         f.weights(a, s, p);
@@ -187,6 +173,16 @@ DEV void piece(const KvAttendArgs& a, const Work& w, int h, int64_t slot, float 
         __builtin_amdgcn_sched_barrier(0);
         load_v(at);
         ok = next;
+    }
+    if (__ballot(nans != 0)) {
+#pragma unroll 1
+        for (int i = 0; i < mine; ++i) {
+            const int t = t0 + 4 * i, k0 = t * 64, pg = uni(t / a.c.tiles);
+            const int page = a.s.table[(int64_t)w.b * a.s.width + pg];
+            if ((k0 >= last.lo && k0 + 64 <= first.hi) || (uint32_t)page >= (uint64_t)a.c.pages) continue;
+            const int64_t u = ((int64_t)page * a.c.H + h) * a.c.tiles + t - pg * a.c.tiles;
+            nan_tile(f, a.c.data + u * tile_bytes + tile_bytes / 2, k0, first.lo, last.hi);
+        }
     }
     // the waves' maxima and sums, then their outputs 64 channels at a time
 #pragma unroll

@@ -52,7 +52,8 @@ DEV float* part_stats(const KvAttendArgs& a, int n, int i, int split, int W) {
 template <int C>
 __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAttendArgs a) {
     constexpr int QT = 2, R = kRows, W = 64 * C, HALF = 4 * C * 1024;
-    __shared__ __attribute__((aligned(16))) char key0[HALF], key1[HALF], value0[HALF], value1[HALF];
+    __shared__ __attribute__((aligned(16))) char key0[HALF], key1[HALF], raw0[HALF], raw1[HALF];
+    __shared__ __attribute__((aligned(16))) char value0[2 * HALF], value1[2 * HALF];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // Row tiles in the order of the key heads, later ones, which see more keys where order counts, first.
@@ -98,9 +99,9 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         lds_barrier();
     };
-    bool ok0, ok1, ok2;                                  // of tiles i, i + 1, i + 2
+    bool ok0, ok1, ok2;                                  // whether tiles 0, i + 1, i + 2 are there
     v4f s[QT][4];
-    uint2 sc0, sc1;                                      // exponents of tiles i, i + 1
+    uint2 sc1;                                           // exponents of tile i + 1
     auto codes = [&](const char* k) __attribute__((always_inline)) {
         return [=](int b, int c) __attribute__((always_inline)) { return *(const uint4*)(k + (b * C + c) * 1024 + lane * 16); };
     };
@@ -113,81 +114,107 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
         f.settle(a, s);
     };
     // Values of a tile that not all rows of the workgroup see whole: keys that none of them sees may
-    // hold anything, and become zeros in LDS, as do NaN values once the sums have them.
+    // hold anything, and become zeros in LDS, as do NaN values (which are seen to in the end).
+    auto partly = [&](int k0) __attribute__((always_inline)) { return k0 < wlast.lo || k0 + 64 > wfirst.hi; };
+    uint32_t nans = 0;
     auto clean = [&](char* v, int k0) __attribute__((always_inline)) {
-        uint32_t any = 0;
-#pragma unroll 1
-        for (int q = 0; q < 4 * C; ++q)
-            any |= nan_codes4(and4(*(const uint4*)(v + q * 1024 + lane * 16), kept_bytes(k0, q / C, wfirst.lo, wlast.hi)));
-        if (__ballot(any != 0)) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                uint32_t x[4][4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const uint4 y = and4(codes(v)(b, c), kept_bytes(k0, b, wfirst.lo, wlast.hi));
-                    x[b][0] = y.x;
-                    x[b][1] = y.y;
-                    x[b][2] = y.z;
-                    x[b][3] = y.w;
-                }
-                f.nan_values(k0, c, x);
-            }
-        }
-        lds_barrier();
 #pragma unroll 1
         for (int q = wave; q < 4 * C; q += 4) {
             uint4* x = (uint4*)(v + q * 1024 + lane * 16);
-            *x = without_nan(and4(*x, kept_bytes(k0, q / C, wfirst.lo, wlast.hi)));
+            const uint4 y = and4(*x, kept_bytes(k0, q / C, wfirst.lo, wlast.hi));
+            nans |= nan_codes4(y);
+            *x = without_nan(y);
         }
         lds_barrier();
     };
-    // Tile i, whose scores are in s: its weights, beside them the next tile's scores; then its sums.
-    int64_t at1 = 0;                                     // tile i + 1
-    auto step = [&](char* knext, char* kfree, char* v, char* vfree, int i) __attribute__((always_inline)) {
-        landed();                                        // keys of i + 1, values of i; nobody reads the others
-        const int k0 = (w.ta + i) * 64;
-        if (ok0 && (k0 < wlast.lo || k0 + 64 > wfirst.hi)) clean(v, k0);
+    // The values of a tile as operands in bf16, a share of the workgroup's waves each: 64 channels (c) of
+    // two blocks of keys (h) at a time, in eight steps.
+    constexpr int SHARES = (2 * C + 3) / 4;
+    uint4 rw[2];
+    uint32_t half[8];
+    auto widen = [&](const char* raw, char* out, uint32_t ve, int x) __attribute__((always_inline)) {
+        const int q = wave + x / 8 * 4, hh = q / C, c = q - hh * C, u = x % 8 / 2, b = x % 2;
+        if (2 * C % 4 && q >= 2 * C) return;
+        if (x % 8 == 0) {
+            rw[0] = *(const uint4*)(raw + (2 * hh * C + c) * 1024 + lane * 16);
+            rw[1] = *(const uint4*)(raw + ((2 * hh + 1) * C + c) * 1024 + lane * 16);
+        }
+        const float vs = __uint_as_float(((ve >> (16 * hh + 8 * b)) & 0xffu) << 23);
+        const uint4 r = rw[b];
+        const uint32_t word = u == 0 ? r.x : u == 1 ? r.y : u == 2 ? r.z : r.w;
+        half[2 * b] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)word, vs, false));
+        half[2 * b + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)word, vs, true));
+        if (b) *(uint4*)(out + ((c * 4 + u) * 2 + hh) * 1024 + lane * 16) = make_uint4(half[0], half[1], half[2], half[3]);
+    };
+    // Tile i, whose scores are in s: its weights, beside them the next tile's scores; then its sums,
+    // beside them the next tile's values.
+    auto step = [&](char* knext, char* kfree, char* rnext, char* rfree, char* v, char* vnext, int i) __attribute__((always_inline)) {
+        landed();                                        // tile i + 1, and tile i's values; nobody reads the others
+        const int k1 = (w.ta + i + 1) * 64;
+        if (ok1 && partly(k1)) clean(rnext, k1);
         const int64_t at2 = find(ok2);
         fetch(kfree, at2, 0, ok2);
-        fetch(vfree, at1, 1, ok1);
+        fetch(rfree, at2, 1, ok2);
         const uint2 sc2 = *(const uint2*)(a.c.scales + at2 * 8);
+        const uint32_t ve = uni(sc1.y);
+        auto meanwhile = [&](int x) __attribute__((always_inline)) {
+            constexpr int PER = (8 * SHARES + 4 * C - 1) / (4 * C);
+#pragma unroll
+            for (int y = 0; y < PER; ++y)
+                if (x * PER + y < 8 * SHARES) widen(rnext, vnext, ve, x * PER + y);
+        };
         if (wr < w.rows) {
             uint32_t p[QT][8];
-            uint32_t v0[4][4];
-            f.exchange_tile(a, s, p, sc1.x, codes(knext), codes(v), v0);
-            f.sums(sc0.y, p, codes(v), v0);
+            f.exchange_tile(a, s, p, sc1.x, codes(knext));
+            __builtin_amdgcn_s_setprio(1);               // (the other wave's vector work waits for a product, not the reverse)
+            f.ready_sums(p, [&](int x, int hh) __attribute__((always_inline)) {
+                return *(const uint4*)(v + (x * 2 + hh) * 1024 + lane * 16);
+            }, meanwhile);
+            __builtin_amdgcn_s_setprio(0);
 #pragma unroll
             for (int t = 0; t < QT; ++t)                 // (or the compiler moves the scores behind the branch)
 #pragma unroll
                 for (int b = 0; b < 4; ++b) order_point(s[t][b]);
             hide(i + 1, ok1);
+        } else {
+#pragma unroll
+            for (int x = 0; x < 4 * C; ++x) meanwhile(x);
         }
-        ok0 = ok1;
         ok1 = ok2;
-        sc0 = sc1;
         sc1 = sc2;
-        at1 = at2;
     };
     if (nt > 0) {
         tiles.start(a, w.b, w.ta, w.tb);
-        const int64_t at0 = find(ok0);
-        at1 = find(ok1);
+        const int64_t at0 = find(ok0), at1 = find(ok1);
         fetch(key0, at0, 0, ok0);
-        sc0 = *(const uint2*)(a.c.scales + at0 * 8);
+        fetch(raw0, at0, 1, ok0);
+        const uint2 sc0 = *(const uint2*)(a.c.scales + at0 * 8);
         sc1 = *(const uint2*)(a.c.scales + at1 * 8);
         landed();
-        fetch(value0, at0, 1, ok0);
+        const int k0 = w.ta * 64;
+        if (ok0 && partly(k0)) clean(raw0, k0);
         fetch(key1, at1, 0, ok1);
+        fetch(raw1, at1, 1, ok1);
+#pragma unroll
+        for (int x = 0; x < 8 * SHARES; ++x) widen(raw0, value0, uni(sc0.y), x);
         if (wr < w.rows) {
             f.score_tile(s, sc0.x, codes(key0));
             hide(0, ok0);
         }
         for (int i = 0; i < nt; i += 2) {
-            step(key1, key0, value0, value1, i);
-            if (i + 1 < nt) step(key0, key1, value1, value0, i + 1);
+            step(key1, key0, raw1, raw0, value0, value1, i);
+            if (i + 1 < nt) step(key0, key1, raw0, raw1, value1, value0, i + 1);
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); // (loads into LDS end before the workgroup does)
+        if (__syncthreads_or(nans != 0)) {
+#pragma unroll 1
+            for (int i = 0; i < nt; ++i) {
+                const int t = w.ta + i, pg = uni(t / a.c.tiles), page = a.s.table[(int64_t)w.b * a.s.width + pg];
+                if (!partly(t * 64) || (uint32_t)page >= (uint64_t)a.c.pages) continue;
+                const int64_t at = ((int64_t)page * a.c.H + h) * a.c.tiles + t - pg * a.c.tiles;
+                nan_tile(f, a.c.data + (2 * at + 1) * HALF, t * 64, wfirst.lo, wlast.hi);
+            }
+        }
     }
 #pragma unroll
     for (int t = 0; t < QT; ++t) {

@@ -307,9 +307,8 @@ struct Flash {
     // Weights of a tile from its scores, the next tile's scores in their place, block by block: one
     // matrix instruction and a few of the vector unit in turn, which run side by side (a bf16 product
     // of 16 cycles leaves its SIMD 8 for others, the keys' of 32 leaves 16).
-    template <class KEY, class VALUE>
-    DEV void exchange_tile(const KvAttendArgs& a, v4f (&s)[QT][4], uint32_t (&p)[QT][8], uint32_t ks, KEY key, VALUE value,
-                           uint32_t (&v)[4][4]) const {
+    template <class KEY>
+    DEV void exchange_tile(const KvAttendArgs& a, v4f (&s)[QT][4], uint32_t (&p)[QT][8], uint32_t ks, KEY key) const {
         uint4 k[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) k[c] = key(0, c);
@@ -320,7 +319,6 @@ struct Flash {
         exchange<0>(a, s, p, ks, k, key);
         exchange<1>(a, s, p, ks, k, key);
         exchange<2>(a, s, p, ks, k, key);
-        read_values(v, 0, value);                        // (on their way for sums())
         exchange<3>(a, s, p, ks, k, key);
     }
 
@@ -379,10 +377,39 @@ struct Flash {
             }
     }
 
-    // NaN values among 64 channels of a tile that not every query sees whole: a product would take them
-    // to the queries that do not see them as well (0 * NaN), so they are taken out, and the sums of those
-    // that do see them become NaN here: bf16's largest number, squared, makes them infinite, and o * 0 + o
-    // leaves what is finite.
+    // The same from operands that are ready: ready(i, h) of 16 channels (rows of the operand) and two
+    // blocks of keys. meanwhile(i): other work of the wave, beside the products of channels 16 i.
+    template <class READY, class MEANWHILE>
+    DEV void ready_sums(const uint32_t (&p)[QT][8], READY ready, MEANWHILE meanwhile) {
+        uint4 v[3][2];                                   // two on their way
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[i][h] = ready(i, h);
+        const uint32_t one2 = 0x3f803f80u;
+        const v8bf ones = __builtin_bit_cast(v8bf, make_uint4(one2, one2, one2, one2));
+#pragma unroll
+        for (int j = 0; j < 2 * QT; ++j) l[j % QT] = mfma_bf16_16x16x32(ones, weight_operand(p[j % QT], j / QT), l[j % QT]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 4 * C; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (i + 2 < 4 * C) v[(i + 2) % 3][h] = ready(i + 2, h);
+#pragma unroll
+            for (int j = 0; j < 2 * QT; ++j) {
+                const int t = j % QT, h = j / QT;
+                o[t][i] = mfma_bf16_16x16x32(__builtin_bit_cast(v8bf, v[i % 3][h]), weight_operand(p[t], h), o[t][i]);
+                if (j == 0) meanwhile(i);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // NaN values of a tile that not every query sees whole: a product would take them to the queries that
+    // do not see them as well (0 * NaN), so they are taken out of it, and in the end, where there were any,
+    // the sums of those that do see them become NaN here: bf16's largest number, squared, makes them
+    // infinite, and o * 0 + o leaves what is finite.
     DEV void nan_values(int k0, int c, const uint32_t (&v)[4][4]) {
         const int g4 = ((threadIdx.x & 63) >> 4) * 4;
 #pragma unroll
@@ -431,6 +458,25 @@ DEV uint32_t nan_codes4(const uint4& v) { return nan_codes(v.x) | nan_codes(v.y)
 DEV uint32_t without_nan(uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xffu); }
 DEV uint4 without_nan(const uint4& v) {
     return make_uint4(without_nan(v.x), without_nan(v.y), without_nan(v.z), without_nan(v.w));
+}
+
+// nan_values() of the tile whose values lie at p, keys [lo, hi) of it
+template <int C, int QT>
+DEV void nan_tile(Flash<C, QT>& f, const uint8_t* p, int k0, int lo, int hi) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        uint32_t v[4][4], any = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint4 w = and4(*(const uint4*)(p + (b * C + c) * 1024 + (threadIdx.x & 63) * 16), kept_bytes(k0, b, lo, hi));
+            v[b][0] = w.x;
+            v[b][1] = w.y;
+            v[b][2] = w.z;
+            v[b][3] = w.w;
+            any |= nan_codes4(w);
+        }
+        if (__ballot(any != 0)) f.nan_values(k0, c, v);
+    }
 }
 
 // row r of the sequence: its token and query head

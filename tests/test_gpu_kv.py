@@ -190,3 +190,61 @@ def test_append(case):
         qr, qerr = turned(qv, pos, dims, pairing, wn[0], 1e-6)
         d = np.abs(out.double().cpu().numpy() - qr)
         assert (d <= qerr * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(qr) + 1e-37).all()
+
+
+def set_code(cache, page, h, token, d, side, code):
+    """The byte of one channel of one token."""
+    t, ch = okv.layout(cache.data.shape[5])[side]
+    at = np.argwhere((t == token % 16) & (ch == d))[0]
+    cache.data[page, h, token // 64, side, token % 64 // 16, int(at[0]), int(at[1])] = code
+
+
+@pytest.mark.parametrize("T,before", [(1, 200), (3, 200), (20, 200), (150, 100)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_values_that_are_not_finite(T, before, D):
+    """A NaN among the keys or values reaches the queries that see it (keys:
+    whole outputs, values: their channel) and no others, wherever the order, the
+    window or the sequence's end hides it; what lies past the end may be
+    anything."""
+    note(f"kv attend NaN {T} {before} {D}")
+    rng = np.random.default_rng(T + D)
+    H, hq, page, window = 2, 4, 128, 150
+    n = T + before
+    pages, table = paged(rng, [n], page, spare=0)
+    state = random_state(rng, pages, page, H, D)
+    q, _ = bf16(rng, (T, hq, D))
+    q = q.cuda()
+    lengths = dev(np.asarray([n], np.int32))
+    for causal, win in ((True, 0), (True, window), (False, 0)):
+        cache = cache_of(state, H, D, page)
+        clean = cache.attend(q, dev(table), lengths, causal=causal, window=win)
+        # past the end: every byte a NaN
+        for t in range(n, -(-n // page) * page):
+            p = int(table[0, t // page])
+            for d in range(0, D, 7):
+                set_code(cache, p, 0, t % page, d, 0, 0x7F)
+                set_code(cache, p, 1, t % page, d, 1, 0xFF)
+        assert torch.equal(cache.attend(q, dev(table), lengths, causal=causal, window=win), clean)
+        # a NaN value and a NaN key among the tokens
+        vt, kt = n - 1 - T // 2, n - 1 - T // 3
+        set_code(cache, int(table[0, vt // page]), 0, vt % page, 5, 1, 0x7F)
+        set_code(cache, int(table[0, kt // page]), 1, kt % page, 3, 0, 0xFF)
+        got = cache.attend(q, dev(table), lengths, causal=causal, window=win)
+        want = clean.clone()
+        for i in range(T):
+            pos = before + i
+            sees = lambda t: (not causal or t <= pos) and (not win or t > pos - win)
+            if sees(vt):
+                want[i, :2, 5] = float("nan")
+            if sees(kt):
+                want[i, 2:] = float("nan")
+        assert torch.equal(got.isnan(), want.isnan())
+        assert torch.equal(got.nan_to_num(nan=7.0), want.nan_to_num(nan=7.0))
+    # a query that is not finite gives NaN, alone
+    bad = q.clone()
+    bad[T // 2, 1, 3], bad[0, 3, 0] = float("inf"), float("nan")
+    cache = cache_of(state, H, D, page)
+    clean, got = (cache.attend(x, dev(table), lengths) for x in (q, bad))
+    assert got[T // 2, 1].isnan().all() and got[0, 3].isnan().all()
+    got[T // 2, 1], got[0, 3] = clean[T // 2, 1], clean[0, 3]
+    assert torch.equal(got, clean)
