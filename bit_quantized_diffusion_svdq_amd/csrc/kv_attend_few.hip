@@ -60,7 +60,7 @@ struct Line {
         }
         const int room = (int)kv_room(a.s, a.c);
         len = len < 0 ? 0 : len;
-        const int hi = len < room ? len : room, from = a.window && len - n - a.window + 1 > 0 ? len - n - a.window + 1 : 0;
+        const int hi = len < room ? len : room, from = a.window && len - n >= a.window ? len - n - a.window + 1 : 0;
         ta = from / 64;
         nt = (hi + 63) / 64 - ta;
         nt = nt < 0 ? 0 : nt;
@@ -155,6 +155,7 @@ DEV void piece(const KvAttendArgs& a, const Work& w, int h, int64_t slot, float 
         load_k(at);                                      // in flight while this tile is worked on
         __builtin_amdgcn_sched_barrier(0);
         if (masked) {
+            sc.y &= ok ? kept_blocks(k0, first.lo, last.hi) : 0u;
             f.mask(s, ok ? k0 : kNowhere);
 #pragma unroll
             for (int b = 0; b < 4; ++b)

@@ -156,7 +156,8 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
         fetch(kfree, at2, 0, ok2);
         fetch(rfree, at2, 1, ok2);
         const uint2 sc2 = *(const uint2*)(a.c.scales + at2 * 8);
-        const uint32_t ve = uni(sc1.y);
+        uint32_t ve = uni(sc1.y);
+        if (!ok1 || partly(k1)) ve &= ok1 ? kept_blocks(k1, wfirst.lo, wlast.hi) : 0u;
         auto meanwhile = [&](int x) __attribute__((always_inline)) {
             constexpr int PER = (8 * SHARES + 4 * C - 1) / (4 * C);
 #pragma unroll
@@ -198,8 +199,10 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
         if (ok0 && partly(k0)) clean(raw0, k0);
         fetch(key1, at1, 0, ok1);
         fetch(raw1, at1, 1, ok1);
+        uint32_t ve = uni(sc0.y);
+        if (!ok0 || partly(k0)) ve &= ok0 ? kept_blocks(k0, wfirst.lo, wlast.hi) : 0u;
 #pragma unroll
-        for (int x = 0; x < 8 * SHARES; ++x) widen(raw0, value0, uni(sc0.y), x);
+        for (int x = 0; x < 8 * SHARES; ++x) widen(raw0, value0, ve, x);
         if (wr < w.rows) {
             f.score_tile(s, sc0.x, codes(key0));
             hide(0, ok0);

@@ -65,7 +65,7 @@ DEV Span span_of(const KvAttendArgs& a, const Work& w, int r) {
     Span s;
     s.hi = a.causal ? (pos + 1 < 0 ? 0 : pos + 1) : w.len;
     if (s.hi > w.room) s.hi = w.room;
-    s.lo = a.window && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
+    s.lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
     return s;
 }
 
@@ -451,6 +451,15 @@ DEV uint32_t kept_bytes(int k0, int b, int lo, int hi) {
     hi = hi < 0 ? 0 : hi > 4 ? 4 : hi;
     const uint32_t below_hi = hi > 3 ? ~0u : (1u << (8 * hi)) - 1u, below_lo = lo > 3 ? ~0u : (1u << (8 * lo)) - 1u;
     return below_hi & ~below_lo;
+}
+
+// The bytes of a tile's exponents whose blocks have a key in [lo, hi): those of the others may be any
+// (255 is a NaN, and times the zeros that stand for their values one again)
+DEV uint32_t kept_blocks(int k0, int lo, int hi) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) w |= k0 + b * 16 < hi && k0 + b * 16 + 16 > lo ? 0xffu << (8 * b) : 0u;
+    return w;
 }
 
 DEV uint4 and4(const uint4& v, uint32_t m) { return make_uint4(v.x & m, v.y & m, v.z & m, v.w & m); }
