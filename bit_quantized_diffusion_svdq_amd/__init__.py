@@ -26,7 +26,7 @@ from .fused import column_offsets, column_slice, projection_weights, split_colum
 from .graph import CapturedSequence
 from .kv import KVCache
 from .rope import RopePlan, rope_axes
-from .block import FusedQKV, SvdqLinear, SvdqMLP, awq_linear
+from .block import CachedAttention, FusedQKV, SvdqLinear, SvdqMLP, awq_linear
 from .package import (load_awq_layer, load_fp8_layer, load_layer, read_metadata, save_awq_layer, save_fp8_layer,
                       save_layer)
 
@@ -46,6 +46,6 @@ __all__ = ["SvdqError", "awq_gemv_w4a16", "check_device", "library_path", "load_
            "svdq_quantize_act_fp8", "svdq_quantize_weight_fp8", "svdq_gemm_fp8", "svdq_gemm_fp8_grouped",
            "svdq_linear_fp8", "svdq_linear_fp8_grouped", "svdq_linear_fp8_workspace_size", "svdq_gemm_fp8_variant", "svdq_rope_axes",
            "svdq_rope_axes_grouped", "Fp8GroupedLinear", "Fp8Linear", "fp8_grouped_linear", "fp8_linear",
-           "quantize_act_fp8", "quantize_fp8", "RopePlan", "rope_axes", "FusedQKV", "save_fp8_layer", "load_fp8_layer",
+           "quantize_act_fp8", "quantize_fp8", "RopePlan", "rope_axes", "FusedQKV", "CachedAttention", "save_fp8_layer", "load_fp8_layer",
            "svdq_gemm_fp8_residual", "svdq_linear_fp8_residual", "Fp8Residual", "KvBatchDesc", "KvCacheDesc", "svdq_kv_append", "svdq_kv_attend", "svdq_kv_attend_workspace_size",
            "svdq_kv_cache_sizes", "KVCache"]

@@ -21,8 +21,9 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from .fp8 import Fp8GroupedLinear, _on
+from .fp8 import Fp8GroupedLinear, Fp8Linear, _on, _residual
 from .graph import CapturedSequence
+from .kv import KVCache
 from .rope import RopePlan, rope_axes
 
 
@@ -201,3 +202,44 @@ class FusedQKV:
             rope_axes(q, k, pos, self.plan, self.q_norm, self.k_norm, self.eps, q_out=q, k_out=k,
                       offsets=offsets)
         return q, k, v
+
+
+class CachedAttention:
+    """An attention block over a KVCache: a FusedQKV's projection, its norms and
+    rotation with the keys and values on their way into the cache
+    (KVCache.append, the queries in place), attention over the cached tokens
+    (KVCache.attend) and the output projection ``out`` (an ``Fp8Linear``, which
+    can add its outputs to a residual, or an ``SvdqLinear``)."""
+
+    def __init__(self, qkv: FusedQKV, out, cache: KVCache, causal: bool = True, window: int = 0,
+                 scale: float | None = None):
+        D, heads = qkv.plan.head_dim, qkv.heads
+        _lib._require(not isinstance(qkv.layer, Fp8GroupedLinear) and not isinstance(out, Fp8GroupedLinear),
+                      "the projections must have one weight each")
+        _lib._require(cache.head_dim == D and cache.kv_heads == qkv.kv_heads,
+                      f"the cache holds {cache.kv_heads} heads of {cache.head_dim}, the projection gives {qkv.kv_heads} of {D}")
+        _lib._require(heads % qkv.kv_heads == 0, f"{heads} query heads are not a multiple of {qkv.kv_heads} key heads")
+        _lib._require(out.K == heads * D, f"out takes K = {out.K}, {heads} heads of {D} give {heads * D}")
+        self.qkv, self.out, self.cache, self.causal, self.window, self.scale = qkv, out, cache, causal, window, scale
+
+    def __call__(self, x: torch.Tensor, pos: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor, offsets=None,
+                 residual=None, gate=None, y=None, stream=None) -> torch.Tensor:
+        """x bf16 [M, K] and pos [M, axes], the call's tokens sorted by sequence;
+        table, lengths and offsets as the cache's -> y bf16 [M, out.N]. residual
+        and gate: y = residual + gate * out(...), y may be residual. Rows of no
+        sequence are unspecified in y."""
+        qkv, cache = self.qkv, self.cache
+        qkv._check(x, pos, None)
+        M, N = x.shape[0], self.out.N
+        fp8 = isinstance(self.out, Fp8Linear)
+        _lib._require(fp8 or (residual is None and gate is None), "a residual needs an Fp8Linear as out")
+        _residual(residual, gate, M, N, torch.bfloat16, (), x.device)      # (before the cache is written)
+        _lib._require(y is None or (tuple(y.shape) == (M, N) and y.dtype is torch.bfloat16 and y.device == x.device
+                                    and (N == 1 or y.stride(1) == 1) and (M <= 1 or y.stride(0) >= N)),
+                      f"y must be bf16 [{M}, {N}] on {x.device} with contiguous columns")
+        with _on(x, stream):
+            flat = qkv.layer(x).unflatten(1, (qkv.heads + 2 * qkv.kv_heads, cache.head_dim))
+            q, k, v = flat.split((qkv.heads, qkv.kv_heads, qkv.kv_heads), dim=1)
+            cache.append(k, v, table, lengths, offsets, pos, qkv.plan, qkv.k_norm, q, qkv.q_norm, q, qkv.eps)
+            o = cache.attend(q, table, lengths, offsets, self.causal, self.window, self.scale).flatten(1)
+            return self.out(o, y=y, residual=residual, gate=gate) if fp8 else self.out(o, y=y)
