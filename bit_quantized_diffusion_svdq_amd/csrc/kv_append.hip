@@ -68,6 +68,19 @@ DEV uint32_t codes4(float a, float b, float c, float d, float r) {
 
 DEV float bf16_at(const uint32_t* w, int e) { return (e & 1) ? bf16_hi_to_f32(w[e >> 1]) : bf16_lo_to_f32(w[e >> 1]); }
 
+// turn_of() (rope_body.h) to a quarter of its error: an angle is rounded to fp32 within an eighth of a
+// turn of a multiple of a quarter, where a last place is 2^-27 of a turn at the most and not 2^-25. A
+// code is a key's nearest of few, so it is the same as that of the key in 64 bits but for some ten in a million.
+DEV float2 near_turn_of(double pos, double turns) {
+    const double turn = pos * turns, quarters = rint(4.0 * turn);
+    const float part = (float)__builtin_fma(-0.25, quarters, turn);
+    float s, c;
+    sincospif(2.0f * part, &s, &c);
+    const int q = (int)(quarters - 4.0 * rint(0.25 * quarters));         // -2 .. 2
+    const float x = q & 1 ? s : c, y = q & 1 ? c : s;                    // a quarter: (-s, c), half: (-c, -s)
+    return make_float2((q + 1) & 2 ? -x : x, q & 2 ? -y : y);
+}
+
 // Cosines and sines of the block's tokens, slots [s0, s1): a wave takes every fourth slot, a lane a
 // pair; the positions of its four slots are read at once.
 DEV void block_angles(const KvAppendArgs& a, float2* cs, int pitch, int s0, int s1, int64_t t_at0, int wave) {
@@ -86,7 +99,7 @@ DEV void block_angles(const KvAppendArgs& a, float2* cs, int pitch, int s0, int 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int s = s0 + wave + 4 * i;
-            if (s < s1) cs[s * pitch + p] = turn_of(a.pos_f32 ? (double)__int_as_float(bits[i]) : (double)bits[i], turns);
+            if (s < s1) cs[s * pitch + p] = near_turn_of(a.pos_f32 ? (double)__int_as_float(bits[i]) : (double)bits[i], turns);
         }
     }
 }
@@ -279,15 +292,16 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
     for (int h = hn; h < hend; h += 2) {
         float r = 1.0f;
         if (a.norm) {
-            float ss = 0.0f;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};     // (short chains: in time and in rounding)
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const uint32_t w[4] = {kw[c][e].x, kw[c][e].y, kw[c][e].z, kw[c][e].w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(bf16_at(w, i), bf16_at(w, i), ss);
+                    for (int i = 0; i < 8; ++i) sum[i % 4] = __builtin_fmaf(bf16_at(w, i), bf16_at(w, i), sum[i % 4]);
                 }
+            float ss = (sum[0] + sum[1]) + (sum[2] + sum[3]);
             ss += lane16_other<0>(ss);
             ss += lane16_other<1>(ss);
             r = knew ? __builtin_amdgcn_rsqf(__builtin_fmaf(ss, 1.0f / (float)D, a.eps)) : 0.0f;
