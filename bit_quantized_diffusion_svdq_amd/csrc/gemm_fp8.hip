@@ -15,7 +15,11 @@
 //    pipe's E8M0 scales: the FMAs (4 of 64 lanes, 16 cycles of a SIMD) run
 //    beside the MFMAs (32 cycles).
 //  - With a residual (kernels of their own: RES), outputs are residual + gate *
-//    act(...), joined in fp32 before the one rounding.
+//    act(...), joined in fp32 before the one rounding. 4608 x 4096 x 4096 takes 89 us
+//    with it and 77 without, 5120 x 12288 x 4096 in two groups 243 and 233: the tiles of a round
+//    end together, and the residual comes at the memory's rate. Read a tile at once it
+//    takes as long; asked for earlier, 91 to 93, as the operands' next
+//    loads are waited for in order, behind it.
 #include "fp8.h"
 
 namespace {
