@@ -41,11 +41,11 @@ def _heads_of(x, name, T, D):
     return H, (ts if T > 1 else H * hs), hs
 
 
-def _norm_at(name, w, D, dev):
+def _norm_at(name, w, D, gpu):
     if not (w.dtype is _BF16 and w.shape == (D,) and w.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous bf16 vector of {D} values")
-    if w.device != dev:
-        raise ValueError(f"{name} is on {w.device}, the cache on {dev}")
+    if w.get_device() != gpu:
+        raise ValueError(f"{name} is on {w.device}, the cache on cuda:{gpu}")
     return w.data_ptr()
 
 
@@ -85,8 +85,9 @@ class KVCache:
         self._desc = KvCacheDesc(self.data.data_ptr(), self.scales.data_ptr(), self.pages, self.kv_heads, self.head_dim,
                                  self.page_size)
         self._at = ctypes.addressof(self._desc)
+        self._gpu = self.data.get_device()           # (numbers compare in half the time of devices)
 
-    def _batch(self, T, table, lengths, offsets, dev):
+    def _batch(self, T, table, lengths, offsets):
         if not (table.dtype is _I32 and table.dim() == 2 and table.shape[0] >= 1 and table.is_contiguous()):
             raise ValueError(f"table must be contiguous int32 [sequences, width], got {tuple(table.shape)} {table.dtype}")
         B, width = table.shape
@@ -97,10 +98,11 @@ class KVCache:
                 raise ValueError(f"{T} tokens are not a multiple of {B} sequences: offsets are needed")
         elif not (offsets.dtype is _I32 and offsets.shape == (B + 1,) and offsets.is_contiguous()):
             raise ValueError(f"offsets must be a contiguous int32 vector of {B + 1} values, got {tuple(offsets.shape)} {offsets.dtype}")
-        if dev.type != "cuda":
-            raise ValueError(f"the cache must be on a GPU device, got {dev}")
-        if table.device != dev or lengths.device != dev or (offsets is not None and offsets.device != dev):
-            raise ValueError(f"table, lengths or offsets is not on {dev}")
+        gpu = self._gpu
+        if gpu < 0:
+            raise ValueError(f"the cache must be on a GPU device, got {self.data.device}")
+        if table.get_device() != gpu or lengths.get_device() != gpu or (offsets is not None and offsets.get_device() != gpu):
+            raise ValueError(f"table, lengths or offsets is not on cuda:{gpu}")
         return KvBatchDesc(table.data_ptr(), lengths.data_ptr(), None if offsets is None else offsets.data_ptr(), T, B, width)
 
     def append(self, k, v, table, lengths, offsets=None, pos=None, plan: RopePlan | None = None, k_norm=None, q=None,
@@ -114,7 +116,7 @@ class KVCache:
         new one), which is returned. Tokens of no sequence are neither stored nor
         turned. Nothing is recorded for autograd: k, v and q that require a
         gradient are refused while it is on."""
-        D, dev = self.head_dim, self.data.device
+        D, gpu = self.head_dim, self._gpu
         if k.dim() != 3:
             raise ValueError(f"k must be [T, {self.kv_heads}, {D}], got {tuple(k.shape)}")
         T = k.shape[0]
@@ -137,14 +139,14 @@ class KVCache:
             f32_pos = pos.dtype is torch.float32
             if not ((f32_pos or pos.dtype is _I32) and pos.shape == (T, plan.axes) and pos.is_contiguous()):
                 raise ValueError(f"pos must be contiguous int32 or fp32 [{T}, {plan.axes}], got {tuple(pos.shape)} {pos.dtype}")
-            if pos.device != dev or plan.turns.device != dev:
-                raise ValueError(f"pos is on {pos.device}, the plan on {plan.turns.device}, the cache on {dev}")
+            if pos.get_device() != gpu or plan.turns.get_device() != gpu:
+                raise ValueError(f"pos is on {pos.device}, the plan on {plan.turns.device}, the cache on {self.data.device}")
             turn = (pos.data_ptr(), f32_pos, plan.axes, plan.turns.data_ptr(), plan.axis.data_ptr(), plan.pairs,
                     PAIRING[plan.pairing])
-        batch = self._batch(T, table, lengths, offsets, dev)
-        if k.device != dev or v.device != dev:
-            raise ValueError(f"k is on {k.device}, v on {v.device}, the cache on {dev}")
-        k_norm = None if k_norm is None else _norm_at("k_norm", k_norm, D, dev)
+        batch = self._batch(T, table, lengths, offsets)
+        if k.get_device() != gpu or v.get_device() != gpu:
+            raise ValueError(f"k is on {k.device}, v on {v.device}, the cache on cuda:{gpu}")
+        k_norm = None if k_norm is None else _norm_at("k_norm", k_norm, D, gpu)
         qs = q_at = None
         if q is not None:
             qh, qts, qhs = _heads_of(q, "q", T, D)
@@ -155,9 +157,9 @@ class KVCache:
                 yh, yts, yhs = _heads_of(q_out, "q_out", T, D)
                 if yh != qh:
                     raise ValueError(f"q_out must have {qh} heads, got {yh}")
-            if q.device != dev or (q_out is not None and q_out.device != dev):
-                raise ValueError(f"q or q_out is not on {dev}")
-            q_norm = None if q_norm is None else _norm_at("q_norm", q_norm, D, dev)
+            if q.get_device() != gpu or (q_out is not None and q_out.get_device() != gpu):
+                raise ValueError(f"q or q_out is not on cuda:{gpu}")
+            q_norm = None if q_norm is None else _norm_at("q_norm", q_norm, D, gpu)
         elif q_norm is not None or q_out is not None:
             raise ValueError("q_norm and q_out need q")
         with _on(k, stream):
@@ -183,7 +185,7 @@ class KVCache:
         scale: 1 / sqrt(head_dim) by default. out: q itself or a buffer of any
         such layout; rows of no sequence are left as they are in it and are
         unspecified in a new one. Nothing is recorded for autograd."""
-        D, dev = self.head_dim, self.data.device
+        D, gpu = self.head_dim, self._gpu
         if q.dim() != 3:
             raise ValueError(f"q must be [T, heads, {D}], got {tuple(q.shape)}")
         if q.requires_grad and torch.is_grad_enabled():
@@ -199,14 +201,14 @@ class KVCache:
             raise ValueError(f"scale must be positive and finite, got {scale}")
         if not 0 <= window < 1 << 31:
             raise ValueError(f"window must be in [0, 2^31), got {window}")
-        batch = self._batch(T, table, lengths, offsets, dev)
+        batch = self._batch(T, table, lengths, offsets)
         yts, yhs = H * D, D
         if out is not None:
             yh, yts, yhs = _heads_of(out, "out", T, D)
             if yh != H:
                 raise ValueError(f"out must have {H} heads, got {yh}")
-        if q.device != dev or (out is not None and out.device != dev):
-            raise ValueError(f"q or out is not on {dev}")
+        if q.get_device() != gpu or (out is not None and out.get_device() != gpu):
+            raise ValueError(f"q or out is not on cuda:{gpu}")
         lib, at = load_library(), ctypes.addressof(batch)
         with _on(q, stream):
             if out is None:
