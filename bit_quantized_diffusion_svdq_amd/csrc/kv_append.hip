@@ -14,7 +14,9 @@
 // wave the keys or the values of one head at a time. The keys' two waves work the
 // block's cosines and sines out once, in LDS, while their first head is on its
 // way. Keys: a lane holds 16 channels of one token in each 64, which is 16
-// bytes of the cache. Values: a lane holds 4 channels of 4 tokens, which is four
+// bytes of the cache; their norm and rotation are in 64 bits (a code is one of few, so a
+// key's own rounding shows where it lies next to a border: of 14 million codes 8 are
+// not the 64-bit key's, 23 with 32 bits, for 1 us of 34). Values: a lane holds 4 channels of 4 tokens, which is four
 // words of it; the words meet in LDS and leave 16 bytes a lane. A block is
 // written by its two waves, so nothing is atomic.
 #include "fp8.h"
@@ -68,22 +70,23 @@ DEV uint32_t codes4(float a, float b, float c, float d, float r) {
 
 DEV float bf16_at(const uint32_t* w, int e) { return (e & 1) ? bf16_hi_to_f32(w[e >> 1]) : bf16_lo_to_f32(w[e >> 1]); }
 
-// turn_of() (rope_body.h) to a quarter of its error: an angle is rounded to fp32 within an eighth of a
-// turn of a multiple of a quarter, where a last place is 2^-27 of a turn at the most and not 2^-25. A
-// code is a key's nearest of few, so it is the same as that of the key in 64 bits but for some ten in a million.
-DEV float2 near_turn_of(double pos, double turns) {
+// Cosine and sine of pos * turns turns, 2^-29 off at the most: within an eighth of a turn of a multiple
+// of a quarter by their series.
+DEV double2 near_turn_of(double pos, double turns) {
     const double turn = pos * turns, quarters = rint(4.0 * turn);
-    const float part = (float)__builtin_fma(-0.25, quarters, turn);
-    float s, c;
-    sincospif(2.0f * part, &s, &c);
+    const double z = 6.283185307179586477 * __builtin_fma(-0.25, quarters, turn), z2 = z * z;
+    const double c = __builtin_fma(z2, __builtin_fma(z2, __builtin_fma(z2, __builtin_fma(z2, __builtin_fma(z2, -1.0 / 3628800,
+                     1.0 / 40320), -1.0 / 720), 1.0 / 24), -0.5), 1.0);
+    const double s = z * __builtin_fma(z2, __builtin_fma(z2, __builtin_fma(z2, __builtin_fma(z2, 1.0 / 362880, -1.0 / 5040),
+                         1.0 / 120), -1.0 / 6), 1.0);
     const int q = (int)(quarters - 4.0 * rint(0.25 * quarters));         // -2 .. 2
-    const float x = q & 1 ? s : c, y = q & 1 ? c : s;                    // a quarter: (-s, c), half: (-c, -s)
-    return make_float2((q + 1) & 2 ? -x : x, q & 2 ? -y : y);
+    const double x = q & 1 ? s : c, y = q & 1 ? c : s;                   // a quarter: (-s, c), half: (-c, -s)
+    return make_double2((q + 1) & 2 ? -x : x, q & 2 ? -y : y);
 }
 
 // Cosines and sines of the block's tokens, slots [s0, s1): a wave takes every fourth slot, a lane a
 // pair; the positions of its four slots are read at once.
-DEV void block_angles(const KvAppendArgs& a, float2* cs, int pitch, int s0, int s1, int64_t t_at0, int wave) {
+DEV void block_angles(const KvAppendArgs& a, double2* cs, int pitch, int s0, int s1, int64_t t_at0, int wave) {
     const int lane = threadIdx.x & 63;
     for (int p = lane; p < a.pairs; p += 64) {
         int ax = a.axis[p];
@@ -203,7 +206,7 @@ DEV void append_values(const KvAppendArgs& a, int page, int tile, int blk, int s
 
 template <int C, int HALF, int U>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs q) {
-    __shared__ float2 cs[16 * (kPairs + 2)];             // a token's pairs, rows apart by two more
+    __shared__ double2 cs[16 * (kPairs + 2)];            // a token's pairs, rows apart by two more
     __shared__ __attribute__((aligned(16))) uint8_t turn[2][C][4 * 272];
     static_assert(sizeof cs >= sizeof(float2) * 4 * kMaxPairs, "the queries' angles fit");
     const int blocks = a.items * a.groups;
@@ -288,9 +291,20 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
                 mw[c][e] = make_uint4(x.x, x.y, y.x, y.y);
             }
         }
+    const double inv_d = 1.0 / D;
     __syncthreads();
+    auto keep = [](uint4& w) __attribute__((always_inline)) { asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w)); };
     for (int h = hn; h < hend; h += 2) {
-        float r = 1.0f;
+        if (a.norm) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {            // (or they are widened before the loop, in twice the registers)
+                    keep(nw[c][e]);
+                    if constexpr (HALF) keep(mw[c][e]);
+                }
+        }
+        double r = 1.0;
         if (a.norm) {
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};     // (short chains: in time and in rounding)
 #pragma unroll
@@ -304,7 +318,10 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
             float ss = (sum[0] + sum[1]) + (sum[2] + sum[3]);
             ss += lane16_other<0>(ss);
             ss += lane16_other<1>(ss);
-            r = knew ? __builtin_amdgcn_rsqf(__builtin_fmaf(ss, 1.0f / (float)D, a.eps)) : 0.0f;
+            const double var = __builtin_fma((double)ss, inv_d, (double)a.eps);
+            r = (double)__builtin_amdgcn_rsqf((float)var);
+            r = __builtin_fma(0.5 * r, __builtin_fma(-var * r, r, 1.0), r);
+            r = knew ? r : 0.0;
         }
         float x[C][16];
         uint32_t m = 0;                                  // magnitudes, ordered as integers
@@ -316,47 +333,51 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
                 const uint4 ow = kw[c][f >> 1], tw = pw[HALF ? c : 0][HALF ? f >> 1 : 0];
                 const uint32_t o[2] = {f & 1 ? ow.z : ow.x, f & 1 ? ow.w : ow.y};
                 const uint32_t p[2] = {f & 1 ? tw.z : tw.x, f & 1 ? tw.w : tw.y};
-                float own[4], other[4];
+                float x32[4], y32[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    own[i] = bf16_at(o, i);
-                    other[i] = HALF ? bf16_at(p, i) : 0.0f;
+                    x32[i] = bf16_at(o, i);
+                    y32[i] = HALF ? bf16_at(p, i) : 0.0f;
                 }
                 const bool first_half = d < P, turned = d < 2 * P;
-                if (a.norm) {                            // (zeros where there is no token or channel)
+                if (a.norm) {                            // (the products with the weights are exact)
                     const uint4 ww = nw[c][f >> 1], vw = mw[HALF ? c : 0][HALF ? f >> 1 : 0];
                     const uint32_t n[2] = {f & 1 ? ww.z : ww.x, f & 1 ? ww.w : ww.y};
                     const uint32_t o2[2] = {f & 1 ? vw.z : vw.x, f & 1 ? vw.w : vw.y};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        own[i] *= r * bf16_at(n, i);
-                        if (HALF) other[i] *= r * bf16_at(o2, i);
+                        x32[i] *= bf16_at(n, i);
+                        if (HALF) y32[i] *= bf16_at(o2, i);
                     }
                 }
+                double own[4], other[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) own[i] = x32[i], other[i] = y32[i];
                 if (turned && knew) {
                     if constexpr (HALF) {
                         const int p0 = first_half ? d : d - P;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 t = cs[key * pitch + p0 + i];
-                            own[i] = __builtin_fmaf(own[i], t.x, first_half ? -(other[i] * t.y) : other[i] * t.y);
+                            const double2 t = cs[key * pitch + p0 + i];
+                            own[i] = __builtin_fma(own[i], t.x, first_half ? -(other[i] * t.y) : other[i] * t.y);
                         }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float2 t = cs[key * pitch + d / 2 + i];
-                            const float u = own[2 * i], v = own[2 * i + 1];
-                            own[2 * i] = __builtin_fmaf(u, t.x, -(v * t.y));
-                            own[2 * i + 1] = __builtin_fmaf(u, t.y, v * t.x);
+                            const double2 t = cs[key * pitch + d / 2 + i];
+                            const double u = own[2 * i], v = own[2 * i + 1];
+                            own[2 * i] = __builtin_fma(u, t.x, -(v * t.y));
+                            own[2 * i + 1] = __builtin_fma(u, t.y, v * t.x);
                         }
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[c][f * 4 + i] = own[i];
-                    const uint32_t b = __float_as_uint(own[i]) & 0x7fffffffu;
+                    x[c][f * 4 + i] = (float)(own[i] * r);
+                    const uint32_t b = __float_as_uint(x[c][f * 4 + i]) & 0x7fffffffu;
                     m = m > b ? m : b;
                 }
+                __builtin_amdgcn_sched_barrier(0);       // (four channels' 64-bit values at a time: registers)
             }
         const bool finite = all_finite(m);
         float amax = __uint_as_float(m);
@@ -411,8 +432,8 @@ hipError_t launch(KvAppendArgs a, RopeArgs q, int half, int cus, hipStream_t str
 hipError_t launch_kv_append(KvAppendArgs a, RopeArgs q, int half, int cus, hipStream_t stream) {
     a.items = (int)(a.s.offs ? a.s.T / 16 + 2 * (int64_t)a.s.B : a.s.n > 0 ? (int64_t)a.s.B * ((a.s.n + 14) / 16 + 1) : 0);
     // Two heads a workgroup; more, which share the angles, while that leaves two workgroups a CU (8003
-    // tokens of 4 heads of 64: 14.1 us with four heads a workgroup, 16.3 with two; 4608 of 24 of 128:
-    // 31.8 with four, 32.6 with sixteen, 38.8 with two).
+    // tokens of 4 heads of 64: 14.9 us with four heads a workgroup, 17.1 with two; 4608 of 24 of 128:
+    // 34.1 with four, 38.9 with all of them, 46.0 with two).
     a.per = 2;
     while (a.per < a.c.H && (int64_t)a.items * ((a.c.H + 2 * a.per - 1) / (2 * a.per)) >= 2 * (int64_t)cus) a.per *= 2;
     a.groups = (a.c.H + a.per - 1) / a.per;
