@@ -1303,7 +1303,8 @@ svdq_status svdq_kv_attend(const svdq_kv_cache* cache, const svdq_kv_batch* batc
     if ((s = check_kv_heads(cache, batch, q->heads, &G)) != SVDQ_OK) return s;
     if (q->norm) return fail(SVDQ_ERR_UNSUPPORTED, "q takes no norm here");
     if ((s = check_rope_heads(q, "q", 1, batch->T, cache->D)) != SVDQ_OK) return s;
-    if (!(scale > 0.0f && scale < __builtin_inff())) return fail(SVDQ_ERR_UNSUPPORTED, "scale must be positive and finite");
+    const float scale2 = scale * 1.4426950408889634f;
+    if (!(scale > 0.0f && scale2 < __builtin_inff())) return fail(SVDQ_ERR_UNSUPPORTED, "scale must be positive and below 2^127");
     if (causal != 0 && causal != 1) return fail(SVDQ_ERR_UNSUPPORTED, "causal must be 0 or 1");
     if (window < 0) return fail(SVDQ_ERR_SHAPE, "window = %d must not be negative", window);
     const KvBatch b = kv_batch_of(batch);
@@ -1331,7 +1332,7 @@ svdq_status svdq_kv_attend(const svdq_kv_cache* cache, const svdq_kv_batch* batc
     a.G = G;
     a.causal = causal;
     a.window = window;
-    a.scale2 = scale * 1.4426950408889634f;
+    a.scale2 = scale2;
     a.part = (float*)workspace;
     const int rows = kv_attend_rows(b, c.D, G);
     return launched(rows ? launch_kv_attend_few(a, rows, kChipCus, (hipStream_t)stream)

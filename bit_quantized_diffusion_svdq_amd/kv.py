@@ -80,12 +80,22 @@ class KVCache:
                      f"{name} must be contiguous uint8 {list(want)}")
         _require(data is None or scales is None or data.device == scales.device, "data and scales must be on one device")
         device = device if data is None and scales is None else (data if data is not None else scales).device
-        self.data = torch.zeros(shape, dtype=torch.uint8, device=device) if data is None else data
-        self.scales = torch.full(lead, 7, dtype=torch.uint8, device=device) if scales is None else scales
-        self._desc = KvCacheDesc(self.data.data_ptr(), self.scales.data_ptr(), self.pages, self.kv_heads, self.head_dim,
+        self._data = torch.zeros(shape, dtype=torch.uint8, device=device) if data is None else data
+        self._scales = torch.full(lead, 7, dtype=torch.uint8, device=device) if scales is None else scales
+        _require(self._data.data_ptr() % 16 == 0 and self._scales.data_ptr() % 8 == 0,
+                 "data needs an address of 16 bytes, scales of 8")
+        self._desc = KvCacheDesc(self._data.data_ptr(), self._scales.data_ptr(), self.pages, self.kv_heads, self.head_dim,
                                  self.page_size)
         self._at = ctypes.addressof(self._desc)
-        self._gpu = self.data.get_device()           # (numbers compare in half the time of devices)
+        self._gpu = self._data.get_device()          # (numbers compare in half the time of devices)
+
+    @property
+    def data(self) -> torch.Tensor:                  # (not to be bound anew: the calls have its address)
+        return self._data
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._scales
 
     def _batch(self, T, table, lengths, offsets):
         if not (table.dtype is _I32 and table.dim() == 2 and table.shape[0] >= 1 and table.is_contiguous()):

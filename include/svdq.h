@@ -733,9 +733,9 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
  *   sees none gives zeros. Statistics and sums are fp32; probabilities are
  *   rounded to bf16 for the second product; one rounding of the output. Keys and
  *   values that a query does not see never reach it, whatever they hold. A query
- *   with an infinity or a NaN gives NaN. q->y may be q->x with its strides.
+ *   with an infinity or a NaN gives NaN (scores that pass fp32 may). q->y may be q->x with its strides.
  *   workspace: svdq_kv_attend_workspace_size bytes (may be 0), 16-byte aligned,
- *   not shared by calls that overlap. scale > 0 and finite.
+ *   not shared by calls that overlap. scale in (0, 2^127).
  *
  * D a multiple of 8 in [8, 256]; page in [64, 65536]; width * page < 2^31 - 64; T <
  * 2^24; sequences in [1, 65536]; window in [0, 2^31); for svdq_kv_attend T * heads <

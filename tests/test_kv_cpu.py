@@ -104,7 +104,7 @@ def test_append_rejects(lib, kw, status):
 
 @pytest.mark.parametrize("kw,status", BOTH + [
     (dict(q=dict(heads=6, yts=6 * 72)), SHAPE), (dict(q=dict(norm=A)), UNSUP), (dict(scale=0.0), UNSUP), (dict(scale=-1.0), UNSUP),
-    (dict(scale=float("inf")), UNSUP), (dict(scale=float("nan")), UNSUP), (dict(causal=2), UNSUP), (dict(window=-1), SHAPE),
+    (dict(scale=float("inf")), UNSUP), (dict(scale=3e38), UNSUP), (dict(scale=float("nan")), UNSUP), (dict(causal=2), UNSUP), (dict(window=-1), SHAPE),
     (dict(bytes=0), SHAPE), (dict(ws=None), NULL), (dict(ws=I + 8), ALIGN), (dict(ws=F), SHAPE), (dict(ws=G), SHAPE),
     (dict(ws=A), SHAPE), (dict(T=(1 << 24) - 1, q=dict(heads=64, yts=64 * 72)), SHAPE),
     (dict(sequences=65536, T=65536, width=1 << 23, offsets=None, page=128), SHAPE),
@@ -184,7 +184,13 @@ def test_cache_refuses():
                dict(data=t(2, 3, 1, 2, 4, 1, 1024, dtype=torch.uint8)), dict(scales=t(2, 3, 1, 2, 4))):
         with pytest.raises(ValueError):
             svdq.KVCache(**{**dict(pages=3, kv_heads=3, head_dim=64, page_size=64, device="cpu"), **kw})
+    with pytest.raises(ValueError):                       # data off its alignment
+        svdq.KVCache(1, 1, 64, data=t(8193, dtype=torch.uint8)[1:].view(1, 1, 1, 2, 4, 1, 1024))
     c = svdq.KVCache(3, 2, 136, page_size=128, device="cpu")
+    with pytest.raises(AttributeError):                   # the calls have the arrays' addresses
+        c.data = c.data.clone()
+    with pytest.raises(AttributeError):
+        c.scales = c.scales.clone()
     assert tuple(c.data.shape) == (3, 2, 2, 2, 4, 3, 1024) and tuple(c.scales.shape) == (3, 2, 2, 2, 4)
 
 
