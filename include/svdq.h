@@ -710,8 +710,8 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
  * outside [0, pages) is one that is not there (its tokens are neither stored nor
  * seen; a window's spent pages may be given back like this), and so is what lies
  * past the table or before token 0. Tokens of no sequence are left as they are.
- * Sequences may share pages that no call writes; a page written by two
- * sequences of a call is the caller's mistake.
+ * Sequences may share pages that the call does not write, and a row may name one
+ * more than once; a page that a call writes twice is the caller's mistake.
  *
  * svdq_kv_cache_sizes -- bytes of data and scales. New pages need no values.
  *

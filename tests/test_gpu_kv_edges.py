@@ -414,6 +414,46 @@ def test_graphs(hq, T):
         assert not (eager.out == 9.0).all(dim=2).any()
 
 
+@pytest.mark.parametrize("T,hq", [(2, 6), (50, 6)])
+def test_two_streams_at_once(T, hq):
+    """Calls that overlap on one cache: each has a workspace of its own."""
+    note(f"kv two streams {T} {hq}")
+    H, D, n = 2, 128, 20000
+    cache = svdq.KVCache(n // 64 + 1, H, D)
+    table = torch.arange(n // 64 + 1, dtype=torch.int32, device="cuda").reshape(1, -1)
+    kv = torch.randn(n, 2 * H, D, device="cuda").bfloat16()
+    cache.append(kv[:, :H], kv[:, H:], table, i32(n))
+    qs = [torch.randn(T, hq, D, device="cuda").bfloat16() for _ in range(4)]
+    want = [cache.attend(q, table, i32(n)) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    lengths = i32(n)
+    torch.cuda.synchronize()
+    got = [[] for _ in qs]
+    for _ in range(5):
+        for out, q, s in zip(got, qs, streams):
+            out.append(cache.attend(q, table, lengths, stream=s))
+    torch.cuda.synchronize()
+    for out, w in zip(got, want):
+        assert all(torch.equal(y, w) for y in out)
+
+
+def test_rewound():
+    """Lengths may go back: tokens that were given up are written over, in place and at once as the oracle has it."""
+    note("kv rewound")
+    rng = np.random.default_rng(13)
+    H, D, page = 2, 64, 64
+    state = random_state(rng, 2, page, H, D)
+    cache = cache_of(state, H, D, page)
+    table = np.asarray([[1, 0]], np.int32)
+    for n, length in ((40, 40), (3, 20), (30, 35), (60, 95), (1, 1)):
+        k, kv = bf16(rng, (n, H, D), float(2.0 ** rng.integers(-3, 4)))
+        v, vv = bf16(rng, (n, H, D))
+        cache.append(k.cuda(), v.cuda(), dev(table), i32(length))
+        okv.append(state, kv, vv, table, [length], [0, n])
+        for a, b in zip(state_of(cache), state):
+            np.testing.assert_array_equal(a, b)
+
+
 def test_scales_and_heads():
     """A scale of one's own, loud scores (one key takes all), equal scores, and a group of many heads."""
     note("kv scales")
