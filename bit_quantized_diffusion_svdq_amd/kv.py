@@ -194,7 +194,9 @@ class KVCache:
         sequence's length; window 0: from 0. One that sees none gives zeros.
         scale: 1 / sqrt(head_dim) by default. out: q itself or a buffer of any
         such layout; rows of no sequence are left as they are in it and are
-        unspecified in a new one. Nothing is recorded for autograd."""
+        unspecified in a new one. Nothing is recorded for autograd. The sequences
+        of a call run in one kernel, which the mean of their tokens chooses: single tokens
+        and prompts take less time in a call each."""
         D, gpu = self.head_dim, self._gpu
         if q.dim() != 3:
             raise ValueError(f"q must be [T, heads, {D}], got {tuple(q.shape)}")
