@@ -19,6 +19,9 @@
 // not the 64-bit key's, 23 with 32 bits, for 1 us of 34). Values: a lane holds 4 channels of 4 tokens, which is four
 // words of it; the words meet in LDS and leave 16 bytes a lane. A block is
 // written by its two waves, so nothing is atomic.
+//
+// Bound by memory and, as a block of work is short, its latency: 4608 tokens of 24 + 2 x 24 heads of 128 with
+// norms and three axes take 34 us in a graph (4.2 TB/s), 8003 of 16 + 2 x 4 of 64 15 (3.1).
 #include "fp8.h"
 #include "kv.h"
 #include "rope_body.h"
