@@ -11,7 +11,7 @@
 // of the block past the last token become zeros.
 //
 // A workgroup takes one block of one sequence and some of its key heads, a
-// wave the keys or the values of one head at a time. The keys' two waves work the
+// wave the keys or the values of one head at a time. The waves work the
 // block's cosines and sines out once, in LDS, while their first head is on its
 // way. Keys: a lane holds 16 channels of one token in each 64, which is 16
 // bytes of the cache; their norm and rotation are in 64 bits (a code is one of few, so a
@@ -323,7 +323,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
             ss += lane16_other<1>(ss);
             const double var = __builtin_fma((double)ss, inv_d, (double)a.eps);
             r = (double)__builtin_amdgcn_rsqf((float)var);
-            r = __builtin_fma(0.5 * r, __builtin_fma(-var * r, r, 1.0), r);
+            if (r > 0.0) r = __builtin_fma(0.5 * r, __builtin_fma(-var * r, r, 1.0), r);     // (0: an infinite sum)
             r = knew ? r : 0.0;
         }
         float x[C][16];
