@@ -81,7 +81,7 @@ struct Line {
 };
 
 // A workgroup's tiles: a multiple of four
-DEV int share_of(const KvAttendArgs& a, int total) {
+DEV int tiles_of(const KvAttendArgs& a, int total) {
     const uint32_t per = ((uint32_t)(total * a.c.H) + a.S - 1) / (uint32_t)a.S;
     return uni(per <= 4 ? 4 : (int)((per + 3) & ~3u));
 }
@@ -215,7 +215,7 @@ DEV void piece(const KvAttendArgs& a, const Work& w, int h, int64_t slot, float 
             v4f y = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float s = __builtin_amdgcn_exp2f((stat[k][r][0] - m) * a.scale2);
+                const float s = share_of(stat[k][r][0], m, a.scale2);
                 sum = __builtin_fmaf(s, stat[k][r][1], sum);
                 const v4f v = *(const v4f*)&red[k][r][c4];
 #pragma unroll
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
     Line<R> line;
     const int total = line.total(a);
     if (total == 0) return;
-    const int share = share_of(a, total), all = total * a.c.H;
+    const int share = tiles_of(a, total), all = total * a.c.H;
     if ((int64_t)blockIdx.x * share >= all) return;
     int x = blockIdx.x * share;
     const int end = all - x < share ? all : x + share;
@@ -297,7 +297,7 @@ __global__ __launch_bounds__(256) void attend_few_join_kernel(KvAttendArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = blockIdx.x, h = blockIdx.y, kh = uni(h / a.G);
     Line<R> line;
-    const int total = line.total(a), share = share_of(a, total);
+    const int total = line.total(a), share = tiles_of(a, total);
     unsigned long long hit = 0;
     if (a.s.B > 64) line.restart();
     else hit = __ballot(t >= line.lo && t < line.lo + line.n);
@@ -325,7 +325,7 @@ __global__ __launch_bounds__(256) void attend_few_join_kernel(KvAttendArgs a) {
 #pragma unroll 4
     for (int j = wave; j < pieces; j += 4) {
         const float2 st = *(const float2*)part_stats<R>(a, slot(j), i, W);
-        const float wgt = __builtin_amdgcn_exp2f((st.x - m) * a.scale2);
+        const float wgt = share_of(st.x, m, a.scale2);
         const float* p = part_sums<R>(a, slot(j), i, W);
         sum = __builtin_fmaf(wgt, st.y, sum);
 #pragma unroll

@@ -277,7 +277,7 @@ __global__ __launch_bounds__(256) void attend_many_join_kernel(KvAttendArgs a) {
         float m = st.x;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-        wgt[j] = lane < a.S ? __builtin_amdgcn_exp2f((st.x - m) * a.scale2) : 0.0f;
+        wgt[j] = lane < a.S ? share_of(st.x, m, a.scale2) : 0.0f;
         sum[j] = st.y * wgt[j];
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) sum[j] += __shfl_xor(sum[j], d);

@@ -30,7 +30,7 @@ namespace {
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
-constexpr float kNone = -1e30f;      // a maximum of nothing
+constexpr float kNone = -__builtin_inff();       // a maximum of nothing
 constexpr int kNowhere = -(1 << 30); // the first key of a tile that is not there
 
 template <int BLK>
@@ -41,6 +41,12 @@ DEV v4f mfma_scores(const uint4& k0, const uint4& k1, const v8i& q, const v4f& c
 
 // the bytes of w that hold a NaN code (0x7f, 0xff), 0x80 each
 DEV uint32_t nan_codes(uint32_t w) { return ~(((w & 0x7f7f7f7fu) ^ 0x7f7f7f7fu) + 0x7f7f7f7fu) & 0x80808080u; }
+
+// What sums taken from `ref` count among those taken from `top` >= ref. (Alike: all, also where both are of
+// nothing, whose difference is none.)
+DEV float share_of(float ref, float top, float scale2) {
+    return ref == top ? 1.0f : __builtin_amdgcn_exp2f((ref - top) * scale2);
+}
 
 // a range of keys, [lo, hi)
 struct Span {
@@ -205,7 +211,7 @@ struct Flash {
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             const float mx = fmaxf(rows4_max(top[t]), m[t]);
-            const float alpha = __builtin_amdgcn_exp2f((m[t] - mx) * a.scale2);
+            const float alpha = share_of(m[t], mx, a.scale2);
             m[t] = mx;
 #pragma unroll
             for (int e = 0; e < 4; ++e) l[t][e] *= alpha;
@@ -268,7 +274,7 @@ struct Flash {
     // weights of two of the lane's four keys of block b, t / 2-th query
     DEV void weight2(const KvAttendArgs& a, const v4f (&s)[QT][4], uint32_t (&p)[QT][8], int b, int i) const {
         const int t = i >> 1, r = 2 * (i & 1);
-        const float off = -m[t] * a.scale2;
+        const float off = m[t] == kNone ? 0.0f : -m[t] * a.scale2;       // (nothing seen so far: the scores are -inf)
         const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][b][r], a.scale2, off));
         const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][b][r + 1], a.scale2, off));
         p[t][2 * b + (i & 1)] = bf16x2(e0, e1);

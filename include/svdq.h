@@ -733,7 +733,8 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
  *   sees none gives zeros. Statistics and sums are fp32; probabilities are
  *   rounded to bf16 for the second product; one rounding of the output. Keys and
  *   values that a query does not see never reach it, whatever they hold. A query
- *   with an infinity or a NaN gives NaN (scores that pass fp32 may). q->y may be q->x with its strides.
+ *   with an infinity or a NaN gives NaN, and one whose scores pass fp32, as q . k or as its product with scale
+ *   log2(e), zeros, infinities or NaN. q->y may be q->x with its strides.
  *   workspace: svdq_kv_attend_workspace_size bytes (may be 0), 16-byte aligned,
  *   not shared by calls that overlap. scale in (0, 2^127).
  *
