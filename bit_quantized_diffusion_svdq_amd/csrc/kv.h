@@ -21,6 +21,7 @@
 #include "rope.h"
 
 constexpr int kKvExpMin = -120;      // least exponent of a block (a block of zeros has it)
+constexpr int kKvExpMax = 120;       // the largest: fp32's largest number is code 256 there
 
 struct KvCache {
     uint8_t* data;                   // [pages][H][tiles][2][4][C][1024]
@@ -123,6 +124,9 @@ DEV int kv_exponent(float amax) {
     const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
     return e < kKvExpMin ? kKvExpMin : e;
 }
+
+// the exponent of a block that is there already (a byte past the largest that an append writes counts as it)
+DEV int kv_old_exponent(uint8_t e) { return (e > kKvExpMax + 127 ? kKvExpMax + 127 : (int)e) - 127; }
 
 // 2^e, e in [-126, 127]
 DEV float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }

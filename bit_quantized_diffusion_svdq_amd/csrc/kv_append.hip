@@ -142,7 +142,7 @@ DEV void append_values(const KvAppendArgs& a, int page, int tile, int blk, int s
             old[c] = make_uint4(0u, 0u, 0u, 0u);
             if (isold) old[c] = *(const uint4*)(vd + c * 1024);
         }
-        if (s0 > 0) e0 = (int)sc[0] - 127;
+        if (s0 > 0) e0 = kv_old_exponent(sc[0]);
     };
     if (hn < hend) fetch(hn);
     meanwhile();
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
                     pw[c][e] = make_uint4(x.x, x.y, y.x, y.y);
                 }
             }
-        if (s0 > 0) e0 = (int)sc[0] - 127;
+        if (s0 > 0) e0 = kv_old_exponent(sc[0]);
     };
     if (hn < hend) fetch(hn);                            // on its way while the angles are worked out
     block_angles(a, cs, pitch, s0, s1, t_at0, wave);

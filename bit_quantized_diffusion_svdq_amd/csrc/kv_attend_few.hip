@@ -228,7 +228,7 @@ DEV void piece(const KvAttendArgs& a, const Work& w, int h, int64_t slot, float 
                     *(v4f*)(part_sums<R>(a, slot, r, W) + d) = y;
                     if (c == 0 && c4 == 0) *(float2*)part_stats<R>(a, slot, r, W) = make_float2(m, sum);
                 } else if (d < a.c.D) {
-                    const float n = sum != 0.0f ? 1.0f / sum : 0.0f;
+                    const float n = sum != 0.0f ? kValueUnit / sum : 0.0f;
                     *(uint2*)(a.y + x.t * a.yts + x.h * a.yhs + d) =
                         make_uint2(bf16x2(y[0] * n, y[1] * n), bf16x2(y[2] * n, y[3] * n));
                 }
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(256) void attend_few_join_kernel(KvAttendArgs a) {
     for (int c = 0; c < C; ++c) red[wave][c * 64 + lane] = y[c];
     if (lane == 0) stat[wave][0] = sum;
     __syncthreads();
-    const float all = stat[0][0] + stat[1][0] + stat[2][0] + stat[3][0], n = all != 0.0f ? 1.0f / all : 0.0f;
+    const float all = stat[0][0] + stat[1][0] + stat[2][0] + stat[3][0], n = all != 0.0f ? kValueUnit / all : 0.0f;
     uint16_t* out = a.y + t * a.yts + h * a.yhs;
     for (int d = threadIdx.x; d < a.c.D; d += 256) out[d] = f32_to_bf16_bits((red[0][d] + red[1][d] + red[2][d] + red[3][d]) * n);
 }

@@ -143,7 +143,7 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
             rw[0] = *(const uint4*)(raw + (2 * hh * C + c) * 1024 + lane * 16);
             rw[1] = *(const uint4*)(raw + ((2 * hh + 1) * C + c) * 1024 + lane * 16);
         }
-        const float vs = __uint_as_float(((ve >> (16 * hh + 8 * b)) & 0xffu) << 23);
+        const float vs = value_scale((ve >> (16 * hh + 8 * b)) & 0xffu);
         const uint4 r = rw[b];
         const uint32_t word = u == 0 ? r.x : u == 1 ? r.y : u == 2 ? r.z : r.w;
         half[2 * b] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)word, vs, false));
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(256, C <= 2 ? 2 : 1) void attend_many_kernel(KvAtte
                 for (int k = 0; k < 4 * C; ++k) *(v4f*)(p + k * 16 + g * 4) = f.o[t][k];
                 if (g == 0) *(float2*)part_stats(a, rest - a.whole, i, split, W) = make_float2(f.m[t], l);
             } else {
-                const float n = l != 0.0f ? 1.0f / l : 0.0f;
+                const float n = l != 0.0f ? kValueUnit / l : 0.0f;
                 uint16_t* p = a.y + x.t * a.yts + x.h * a.yhs;
 #pragma unroll
                 for (int k = 0; k < 4 * C; ++k) {
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(256) void attend_many_join_kernel(KvAttendArgs a) {
     for (int j = 0; j < kJoin; ++j) {
         if (i0 + j >= w.rows) break;
         const Row x = row_of(a, w, h, w.row0 + i0 + j);
-        const float k = sum[j] != 0.0f ? 1.0f / sum[j] : 0.0f;
+        const float k = sum[j] != 0.0f ? kValueUnit / sum[j] : 0.0f;
         uint16_t* out = a.y + x.t * a.yts + x.h * a.yhs;
 #pragma unroll
         for (int c = 0; c < C; ++c)

@@ -42,6 +42,19 @@ DEV v4f mfma_scores(const uint4& k0, const uint4& k1, const v8i& q, const v4f& c
 // the bytes of w that hold a NaN code (0x7f, 0xff), 0x80 each
 DEV uint32_t nan_codes(uint32_t w) { return ~(((w & 0x7f7f7f7fu) ^ 0x7f7f7f7fu) + 0x7f7f7f7fu) & 0x80808080u; }
 
+// Values are taken over 64 and the outputs times 64: the largest (bf16's own go to code 256 at exponent
+// 120, 2^128) stay finite in bf16, where a hidden key's weight of 0 times an infinity would be a NaN, and
+// a weight of up to 2^8 times a value below 2^126 stays finite in fp32. Powers of two, so nothing changes but
+// the finest steps: bf16 has none below 2^-133, so values have none below 2^-127 (blocks of exponents
+// -119 and -120 go down to 2^-129).
+constexpr int kValueShift = 6;
+constexpr float kValueUnit = 1 << kValueShift;
+// the scale of a block with the exponent byte e. (Bytes that no append writes count as the nearest one.)
+DEV float value_scale(uint32_t e) {
+    e = e < kKvExpMin + 127 ? kKvExpMin + 127 : e > kKvExpMax + 127 ? kKvExpMax + 127 : e;
+    return __uint_as_float((e - kValueShift) << 23);
+}
+
 // What sums taken from `ref` count among those taken from `top` >= ref. (Alike: all, also where both are of
 // nothing, whose difference is none.)
 DEV float share_of(float ref, float top, float scale2) {
@@ -347,7 +360,7 @@ struct Flash {
         float vs[4];
         const uint32_t e4 = __builtin_amdgcn_readfirstlane(ve);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) vs[b] = __uint_as_float(((e4 >> (8 * b)) & 0xffu) << 23);
+        for (int b = 0; b < 4; ++b) vs[b] = value_scale((e4 >> (8 * b)) & 0xffu);
         // two values of the operand of rows u: 8 make it (blocks 0 and 1, then 2 and 3)
         auto widen2 = [&](uint32_t (&f)[8], int u, int j) __attribute__((always_inline)) {
             const int b = j / 2;

@@ -698,7 +698,9 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
  * token j / 16 % 16; of the values, channel 64 c + 16 (j / 4 % 4) + j / 16 % 16 of
  * token 4 (j / 256) + j % 4 (a wave's lanes read either as matrix operands, 16
  * bytes each). Channels past D are zeros. scales [pages][heads][page / 64][2][4]
- * bytes: a code stands for code * 2^(byte - 127) (E8M0), one byte a block.
+ * bytes: a code stands for code * 2^(byte - 127) (E8M0), one byte a block. svdq_kv_append
+ * writes bytes from 7 to 247; of a block that it goes on with a byte past 247 counts as 247, of
+ * the values that svdq_kv_attend reads one out of that range as its nearest end.
  *
  * A batch: `sequences` sequences, sequence b on pages table[b][0 .. width - 1], in
  * order; lengths[b] tokens of it are in the cache, those of the call among them
@@ -732,7 +734,9 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
  *   [max(0, p - window + 1), causal ? p + 1 : length), window 0: from 0. One that
  *   sees none gives zeros. Statistics and sums are fp32; probabilities are
  *   rounded to bf16 for the second product; one rounding of the output. Keys and
- *   values that a query does not see never reach it, whatever they hold. A query
+ *   values that a query does not see never reach it, whatever they hold. Weights are at most
+ *   2^8 before their sum is divided out, and weighted values that add up past 2^134 are
+ *   infinite; steps of values below 2^-127 are rounded to it. A query
  *   with an infinity or a NaN gives NaN, and one whose scores pass fp32, as q . k or as its product with scale
  *   log2(e), zeros, infinities or NaN. q->y may be q->x with its strides.
  *   workspace: svdq_kv_attend_workspace_size bytes (may be 0), 16-byte aligned,

@@ -6,8 +6,9 @@ import pytest
 import torch
 
 from gpu_util import note
-from kv_util import bf16, cum, paged, random_state
-from test_gpu_kv import cache_of, dev, run_attend
+from kv_util import attend_bound, bf16, cum, paged, random_state
+from oracle import kv as okv
+from test_gpu_kv import cache_of, dev, run_attend, state_of
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +77,89 @@ def test_scores_far_below_zero(i, up):
     got = cache_of(state, H, 64, 64).attend(q.cuda(), dev(table), dev(np.asarray(lengths, np.int32)), dev(offs), causal=causal,
                                             window=window, scale=2.0 ** (-57 - up))
     assert torch.equal(got, want.expand_as(got))
+
+
+@pytest.mark.parametrize("i", range(len(SHAPES)))
+def test_values_near_the_largest(i):
+    """bf16's largest values go into the cache as 2^128. Queries that do not see them do not change; those
+    that do have them by their weight."""
+    note(f"kv largest values {SHAPES[i]}")
+    counts, before, hq, H, causal, window = SHAPES[i]
+    state, table, lengths, offs, q, qv, *_ = case(i, 64)
+    rng = np.random.default_rng(i)
+    caches = [cache_of(state, H, 64, 64) for _ in range(2)]
+    kv = [bf16(rng, (sum(lengths), H, 64))[0].cuda() for _ in range(2)]
+    big = kv[1].clone()
+    at = []
+    for b, n in enumerate(lengths):                       # (the last ones: early queries do not see them)
+        first = int(cum(lengths)[b])
+        for t in (n - 1, n - counts[b] // 2 - 1):
+            big[first + t, 0, 5], big[first + t, 0, 6] = 3.38e38, -3.38e38
+            at.append((b, t))
+    for cache, v in zip(caches, (kv[1], big)):
+        cache.append(kv[0], v, dev(table), dev(np.asarray(lengths, np.int32)), dev(cum(lengths)))
+    args = (dev(table), dev(np.asarray(lengths, np.int32)), dev(offs))
+    q, qv = (0.1 * q).bfloat16(), (0.1 * q).bfloat16().double().numpy()
+    clean, got = (c.attend(q.cuda(), *args, causal=causal, window=window) for c in caches)
+    y = okv.attend(state_of(caches[1]), qv, table, lengths, offs, causal, window)[0]
+    fits = np.abs(y) < 2.0 ** 126                         # (a row of a few keys: past bf16)
+    assert torch.equal(got.isfinite() | ~torch.from_numpy(fits).cuda(), torch.ones_like(got, dtype=torch.bool))
+    g, bound = got.double().cpu().numpy(), attend_bound(*okv.attend(state_of(caches[1]), qv, table, lengths, offs, causal, window))
+    assert (np.abs(g - y)[fits] <= bound[fits]).all()
+    # what sees none of them, and the channels beside them but for their block's coarser steps, is as it was
+    other = torch.ones(hq, dtype=torch.bool)
+    other[:hq // H] = False
+    assert torch.equal(got[:, other], clean[:, other])
+    hidden = 0
+    for b in range(len(counts)):
+        for r in range(counts[b]):
+            pos = lengths[b] - counts[b] + r
+            sees = [t for bb, t in at if bb == b and (t <= pos if causal else True) and not (window and t <= pos - window)]
+            same = not sees and not [t for bb, t in at if bb == b and t // 16 <= pos // 16]   # (nor their blocks' steps)
+            hidden += same
+            if same:
+                assert torch.equal(got[int(offs[b]) + r], clean[int(offs[b]) + r])
+    assert hidden or max(counts) < 32 or not causal
+
+
+@pytest.mark.parametrize("i", range(len(SHAPES)))
+def test_large_values_under_large_weights(i):
+    """Weights are taken from a reference up to 2^8 below the largest, and values of 2^120 are read under them."""
+    note(f"kv large values {SHAPES[i]}")
+    state, table, lengths, offs, q, qv, H, causal, window = case(i, 64)
+    state[3] = state[3] + 121
+    run_attend(cache_of(state, H, 64, 64), state, q.cuda(), qv, table, lengths, offs, causal, window)
+    # the least exponents: bf16's own step is 2^-133, that of a 64th of the values
+    state[3] = np.maximum(state[3] - 121 - 113, okv.EXP_MIN)
+    y, mag, rss, peak = okv.attend(state, qv, table, lengths, offs, causal, window)
+    got = cache_of(state, H, 64, 64).attend(q.cuda(), dev(table), dev(np.asarray(lengths, np.int32)), dev(offs), causal=causal,
+                                            window=window).double().cpu().numpy()
+    assert (np.abs(got - y) <= attend_bound(y, mag, rss, peak) - 1e-30 + 2.0 ** -127).all()
+
+
+@pytest.mark.parametrize("T,hq", [(2, 2), (40, 2)])
+def test_exponents_that_no_append_writes(T, hq):
+    """A values' byte above 247 counts as 247, under attention and where a block is gone on with."""
+    note(f"kv exponents {T} {hq}")
+    rng = np.random.default_rng(T)
+    n, D = 150, 64
+    pages, table = paged(rng, [n], 64)
+    state = random_state(rng, pages, 64, 1, D)
+    state[1] = np.where(state[1] >= 0, 2.0 ** -6, -2.0 ** -6)
+    state[3][:] = 120
+    caches = [cache_of(state, 1, D, 64) for _ in range(2)]
+    caches[1].scales[:, :, :, 1, ::2] = 255
+    caches[1].scales[:, :, :, 1, 1::2] = 248
+    q, qv = bf16(rng, (T, hq, D))
+    args = (dev(table), dev(np.asarray([n], np.int32)))
+    a, b = (c.attend(q.cuda(), *args) for c in caches)
+    assert torch.equal(a, b) and a.isfinite().all()
+    run_attend(caches[0], state, q.cuda(), qv, table, [n], cum([T]), True, 0)
+    k, v = (bf16(rng, (7, 1, D), 2.0 ** 118)[0].cuda() for _ in range(2))
+    for c, byte in zip(caches, (247, 255)):
+        c.scales[:] = byte
+        c.append(k, v, *args)
+    p, at = int(table[0, (n - 7) // 64]), (n - 7) % 64
+    assert torch.equal(caches[0].data, caches[1].data)
+    for c in caches:
+        assert (c.scales[p, 0, 0, :, at // 16] == 247).all()
