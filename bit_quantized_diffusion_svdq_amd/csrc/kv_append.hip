@@ -215,7 +215,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
     const int blocks = a.items * a.groups;
     if ((int)blockIdx.x >= blocks) {
         const int64_t b = (int)blockIdx.x - blocks;
-        rope_axes_body<0, HALF, U, true>(q, b % a.qx, (int)(b / a.qx), (float2(*)[kMaxPairs])cs);
+        rope_axes_body<0, HALF, U, true, true>(q, b % a.qx, (int)(b / a.qx), (float2(*)[kMaxPairs])cs);
         return;
     }
     const int tid = threadIdx.x, lane = tid & 63;

@@ -69,13 +69,22 @@ DEV float2 turn_of(double pos, double turns) {
 
 constexpr int kMaxPairs = 256;
 
+// Whether some offset is past token t (the same for all lanes). Where offsets fall, each counts as the
+// largest before it, so the last token of a group is before the largest of them all, not before the last.
+DEV bool some_past(const int* offs, int groups, int64_t t) {
+    for (int i = threadIdx.x & 63; __ballot(i <= groups); i += 64)
+        if (__ballot(i <= groups && offs[i < groups ? i : groups] > t)) return true;
+    return false;
+}
+
 // HALF 0: pairs are neighbours (2i, 2i + 1); 1: pair i is (i, i + pairs). U:
 // loads of a wave in flight (16 bytes a lane each, bf16). EDGES: heads may have
 // channels past their pairs and tokens may be of no group (kept apart: the
 // selects and the look at the offsets take 0.1 of 2.9 us for one token and 0.5
 // of 21.0 for 4608 of 24 + 24 heads of 128)
-// A workgroup of 256: tokens 4 bx .. 4 bx + 3, the by-th run of their loads.
-template <int F32, int HALF, int U, bool EDGES>
+// A workgroup of 256: tokens 4 bx .. 4 bx + 3, the by-th run of their loads. RISING: offsets may fall and
+// are made to rise, as the cache's are; else a token from the last one on is of no group.
+template <int F32, int HALF, int U, bool EDGES, bool RISING = false>
 DEV void rope_axes_body(const RopeArgs& a, int64_t bx, int by, float2 (*cs)[kMaxPairs]) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -108,7 +117,8 @@ DEV void rope_axes_body(const RopeArgs& a, int64_t bx, int by, float2 (*cs)[kMax
         }
     };
     if (first < last) fetch(first);                              // on its way while the angles are worked out
-    if (EDGES && a.offs && (t < a.offs[0] || t >= a.offs[a.groups])) return;   // of no group: left as it is
+    if (EDGES && a.offs && (t < a.offs[0] || (t >= a.offs[a.groups] && !(RISING && some_past(a.offs, a.groups, t)))))
+        return;                                                  // of no group: left as it is
 
     // the token's positions, one a lane (no pairs: there may be none)
     const int pv = a.pairs > 0 && lane < a.axes ? ((const int*)a.pos)[t * a.axes + lane] : 0;
