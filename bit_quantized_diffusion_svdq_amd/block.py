@@ -227,8 +227,12 @@ class CachedAttention:
         """x bf16 [M, K] and pos [M, axes], the call's tokens sorted by sequence;
         table, lengths and offsets as the cache's -> y bf16 [M, out.N]. residual
         and gate: y = residual + gate * out(...), y may be residual. Rows of no
-        sequence are unspecified in y."""
+        sequence are unspecified in y. Nothing is recorded for autograd: x, residual
+        and gate that require a gradient are refused while it is on."""
         qkv, cache = self.qkv, self.cache
+        if x.requires_grad and torch.is_grad_enabled():
+            raise ValueError("x requires a gradient, which this call does not record: call it under torch.no_grad() or on a "
+                             "detached tensor")
         qkv._check(x, pos, None)
         M, N = x.shape[0], self.out.N
         fp8 = isinstance(self.out, Fp8Linear)

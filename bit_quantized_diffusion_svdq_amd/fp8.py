@@ -149,6 +149,10 @@ def _output(y, M, N, out_dtype, like):
 
 def _residual(residual, gate, M, N, dtype, lead, dev):
     """What the outputs join, or None: checked (``dtype``: the outputs')."""
+    if torch.is_grad_enabled() and ((residual is not None and residual.requires_grad)
+                                    or (gate is not None and gate.requires_grad)):
+        raise ValueError("residual or gate requires a gradient, which this call does not record: call it under torch.no_grad() "
+                         "or on detached tensors, or add the layer's outputs outside")
     if residual is None:
         if gate is not None:
             raise ValueError("gate needs a residual")
@@ -172,7 +176,8 @@ def fp8_linear(qx, sx, qw, sw, bias=None, act: str = "none", out_dtype=torch.bfl
     or fp32; rows of a given y may be strided; y must not overlap the inputs).
     residual [M, N] of the outputs' type (rows may be strided; y itself: in
     place): the outputs are residual + gate * act(...), gate bf16 [N] or None
-    (ones), joined in fp32 before the one rounding.
+    (ones), joined in fp32 before the one rounding. Nothing is recorded for
+    autograd: a residual or gate that requires a gradient is refused while it is on.
 
     The output type also chooses the sums. bf16: the E4M3 matrix instructions,
     which drop what falls 13 bits below the largest of each 8 products, 1.4e-5
