@@ -403,6 +403,11 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
                 for (int i = 0; i < 4; ++i)
                     w[i] = finite ? codes4<true>(x[c][4 * i], x[c][4 * i + 1], x[c][4 * i + 2], x[c][4 * i + 3], rk)
                                   : codes4<false>(x[c][4 * i], x[c][4 * i + 1], x[c][4 * i + 2], x[c][4 * i + 3], rk);
+                if (c == C - 1 && !finite) {             // past the head: 0 times a root that is a NaN
+                    const int past = c * 64 + part * 16 + 16 - D;
+                    if (past > 0) w[2] = w[3] = 0u;      // (a multiple of 8)
+                    if (past > 8) w[0] = w[1] = 0u;
+                }
                 *(uint4*)(kd + c * 1024) = make_uint4(w[0], w[1], w[2], w[3]);
             } else if (e != e0) {
                 *(uint4*)(kd + c * 1024) = rescale16(*(const uint4*)(kd + c * 1024), exp2i(e0 - e < -126 ? -126 : e0 - e));

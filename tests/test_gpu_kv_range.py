@@ -7,10 +7,12 @@ import torch
 
 from gpu_util import note
 from kv_util import attend_bound, bf16, cum, paged, random_state
-from oracle import kv as okv
 from test_gpu_kv import cache_of, dev, run_attend, state_of
 
 pytestmark = pytest.mark.gpu
+
+import bit_quantized_diffusion_svdq_amd as svdq
+from oracle import kv as okv
 
 # counts, tokens before, heads, key heads, causal, window: few rows, with pieces; more, with and without splits
 SHAPES = [
@@ -163,3 +165,24 @@ def test_exponents_that_no_append_writes(T, hq):
     assert torch.equal(caches[0].data, caches[1].data)
     for c in caches:
         assert (c.scales[p, 0, 0, :, at // 16] == 247).all()
+
+
+@pytest.mark.parametrize("D", [8, 40, 72, 136, 200])
+@pytest.mark.parametrize("turns", [False, True])
+def test_channels_past_the_head(D, turns):
+    """They stay zeros where a key's norm is a NaN as well (a NaN or, with eps 0, a key of zeros)."""
+    note(f"kv channels past {D}")
+    T, H = 40, 2
+    cache = svdq.KVCache(1, H, D)
+    k = torch.randn(T, H, D, generator=torch.Generator().manual_seed(D)).bfloat16()
+    k[3, 0, 1], k[20, 1, D - 1], k[7, 1], k[33] = float("nan"), float("inf"), 0.0, float("nan")
+    k = k.cuda()
+    more = dict(pos=torch.ones(T, 1, dtype=torch.int32, device="cuda"), plan=svdq.RopePlan((8,), head_dim=D)) if turns else {}
+    for eps in (1e-6, 0.0):
+        cache.data.zero_()
+        cache.append(k, k, dev(np.zeros((1, 1), np.int32)), dev(np.asarray([T], np.int32)), eps=eps,
+                     k_norm=torch.ones(D, dtype=torch.bfloat16, device="cuda"), **more)
+        keys, values, *_ = state_of(cache)
+        assert (keys[..., D:] == 0).all() and (values[..., D:] == 0).all() and (keys[0, T:] == 0).all()
+        assert np.isnan(keys[0, 3, 0, :D]).all() and np.isnan(keys[0, 7, 1, :D]).all() == (eps == 0.0)
+        assert np.isnan(keys[0, 20, 1, D - 1]) and np.isnan(values[0, 33, 0, :D]).all()
