@@ -259,7 +259,10 @@ __global__ __launch_bounds__(256, C <= 2 && QT == 1 ? 2 : 1) void attend_few_ker
             ++h;
             if (a.s.B > 64) line.restart();
         }
-        while (at >= line.before + line.sum) line.next(a);
+        while (at >= line.before + line.sum) {
+            if (line.b0 + 64 >= a.s.B) return;           // lengths that fell since they were added up: no more tiles
+            line.next(a);
+        }
         const unsigned long long hit = __ballot(at >= line.start && at < line.start + line.units);
         const int src = __builtin_ctzll(hit);
         const int pad = __builtin_amdgcn_readlane(line.pad, src);
@@ -310,8 +313,10 @@ __global__ __launch_bounds__(256) void attend_few_join_kernel(KvAttendArgs a) {
     const int r = (t - __builtin_amdgcn_readlane(line.lo, src)) * a.G + h - kh * a.G, i = r % R;
     const int pad = __builtin_amdgcn_readlane(line.pad, src);
     const uint32_t from = kh * total + __builtin_amdgcn_readlane(line.start, src) + r / R * pad;
-    const int w0 = uni(from / (uint32_t)share), w1 = uni((from + pad - 1) / (uint32_t)share);
+    int w0 = uni(from / (uint32_t)share), w1 = uni((from + pad - 1) / (uint32_t)share);
     if (w0 == w1) return;                                // one piece: written already
+    if (w1 >= a.S) w1 = a.S - 1;                         // (lengths that have changed since: in bounds all the same)
+    if (w0 > w1) w0 = w1;
     // piece 0 is the last of workgroup w0, piece j > 0 the first of w0 + j
     const int pieces = w1 - w0 + 1;
     auto slot = [&](int j) __attribute__((always_inline)) { return (int64_t)(j ? 2 * (w0 + j) : 2 * w0 + 1); };

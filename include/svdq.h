@@ -711,7 +711,9 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
  * clamped into [0, T], one that falls counts as the largest before it; a page
  * outside [0, pages) is one that is not there (its tokens are neither stored nor
  * seen; a window's spent pages may be given back like this), and so is what lies
- * past the table or before token 0. Tokens of no sequence are left as they are.
+ * past the table or before token 0. Where the arrays change before a call's work is done its
+ * results are any; nothing outside the buffers is touched, and every kernel ends.
+ * Tokens of no sequence are left as they are.
  * Sequences may share pages that the call does not write, and a row may name one
  * more than once; a page that a call writes twice is the caller's mistake.
  *
