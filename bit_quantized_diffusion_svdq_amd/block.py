@@ -220,6 +220,9 @@ class CachedAttention:
                       f"the cache holds {cache.kv_heads} heads of {cache.head_dim}, the projection gives {qkv.kv_heads} of {D}")
         _lib._require(heads % qkv.kv_heads == 0, f"{heads} query heads are not a multiple of {qkv.kv_heads} key heads")
         _lib._require(out.K == heads * D, f"out takes K = {out.K}, {heads} heads of {D} give {heads * D}")
+        # (what attention would refuse, before the first call has written the cache)
+        _lib._require(scale is None or 0.0 < scale < 2.0 ** 127, f"scale must be in (0, 2^127), got {scale}")
+        _lib._require(0 <= window < 1 << 31, f"window must be in [0, 2^31), got {window}")
         self.qkv, self.out, self.cache, self.causal, self.window, self.scale = qkv, out, cache, causal, window, scale
 
     def __call__(self, x: torch.Tensor, pos: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor, offsets=None,

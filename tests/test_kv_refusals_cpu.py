@@ -46,3 +46,12 @@ def test_block_refuses_a_gradient(name):
     a[name] = a[name].clone().requires_grad_()
     with pytest.raises(ValueError, match="gradient"):
         block()(**a)
+
+
+@pytest.mark.parametrize("kw", [dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
+                                dict(scale=3e38), dict(window=-1), dict(window=1 << 31)], ids=str)
+def test_block_refuses_what_attention_would(kw):
+    """At once, not after a call has written its keys and values."""
+    with pytest.raises(ValueError, match="scale|window"):
+        block(**kw)
+    assert block(scale=2.0 ** 126, window=(1 << 31) - 1).scale == 2.0 ** 126
