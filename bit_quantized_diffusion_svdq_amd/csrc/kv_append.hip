@@ -14,9 +14,10 @@
 // wave the keys or the values of one head at a time. The waves work the
 // block's cosines and sines out once, in LDS, while their first head is on its
 // way. Keys: a lane holds 16 channels of one token in each 64, which is 16
-// bytes of the cache; their norm and rotation are in 64 bits (a code is one of few, so a
-// key's own rounding shows where it lies next to a border: of 14 million codes 8 are
-// not the 64-bit key's, 23 with 32 bits, for 1 us of 34). Values: a lane holds 4 channels of 4 tokens, which is four
+// bytes of the cache; their norm and rotation are in 64 bits and their only rounding is that to
+// the code (a code is one of few, so a rounding on the way shows where a key lies next to a
+// border: of 14 million codes 27 are not the 64-bit key's in 32 bits, 7 with the rotation in 64, 3 with one
+// rounding, none with the squares' sum in 64 as well; the last two take 1.3 us of 36). Values: a lane holds 4 channels of 4 tokens, which is four
 // words of it; the words meet in LDS and leave 16 bytes a lane. A block is
 // written by its two waves, so nothing is atomic.
 //
@@ -69,6 +70,22 @@ template <bool FINITE>
 DEV uint32_t codes4(float a, float b, float c, float d, float r) {
     if constexpr (FINITE) return e4m3_x4(a * r, b * r, c * r, d * r);
     else return e4m3_x4(fit(a, r), fit(b, r), fit(c, r), fit(d, r));
+}
+
+template <int STEP>
+DEV double lane16_other64(double v) {
+    const uint2 u = __builtin_bit_cast(uint2, v);
+    return __builtin_bit_cast(double, make_uint2(__float_as_uint(lane16_other<STEP>(__uint_as_float(u.x))),
+                                                 __float_as_uint(lane16_other<STEP>(__uint_as_float(u.y)))));
+}
+
+// A number in 64 bits to one in 32 that rounds to the code that the first one rounds to: 20 bits of its
+// fraction and, in the last place, whether there was more (so what lies beside a border does not come to
+// lie on it).
+DEV float to_odd(double v) {
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, v);
+    const uint32_t lo = (uint32_t)u;
+    return (float)__builtin_bit_cast(double, (u & 0xffffffff00000000ull) | ((unsigned long long)((lo < 1u ? lo : 1u) << 29)));
 }
 
 DEV float bf16_at(const uint32_t* w, int e) { return (e & 1) ? bf16_hi_to_f32(w[e >> 1]) : bf16_lo_to_f32(w[e >> 1]); }
@@ -309,19 +326,23 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
         }
         double r = 1.0;
         if (a.norm) {
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};     // (short chains: in time and in rounding)
+            double sum[2] = {0.0, 0.0};
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const uint32_t w[4] = {kw[c][e].x, kw[c][e].y, kw[c][e].z, kw[c][e].w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sum[i % 4] = __builtin_fmaf(bf16_at(w, i), bf16_at(w, i), sum[i % 4]);
+                    for (int i = 0; i < 8; i += 4) {     // (four squares, each exact, in 32 bits: 2^-28 of the root)
+                        const float s0 = __builtin_fmaf(bf16_at(w, i), bf16_at(w, i), bf16_at(w, i + 1) * bf16_at(w, i + 1));
+                        const float s1 = __builtin_fmaf(bf16_at(w, i + 2), bf16_at(w, i + 2), bf16_at(w, i + 3) * bf16_at(w, i + 3));
+                        sum[i / 4] += (double)(s0 + s1);
+                    }
                 }
-            float ss = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            ss += lane16_other<0>(ss);
-            ss += lane16_other<1>(ss);
-            const double var = __builtin_fma((double)ss, inv_d, (double)a.eps);
+            double ss = sum[0] + sum[1];
+            ss += lane16_other64<0>(ss);
+            ss += lane16_other64<1>(ss);
+            const double var = __builtin_fma(ss, inv_d, (double)a.eps);
             r = (double)__builtin_amdgcn_rsqf((float)var);
             if (r > 0.0) r = __builtin_fma(0.5 * r, __builtin_fma(-var * r, r, 1.0), r);     // (0: an infinite sum)
             r = knew ? r : 0.0;
@@ -376,7 +397,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[c][f * 4 + i] = (float)(own[i] * r);
+                    x[c][f * 4 + i] = to_odd(own[i] * r);
                     const uint32_t b = __float_as_uint(x[c][f * 4 + i]) & 0x7fffffffu;
                     m = m > b ? m : b;
                 }

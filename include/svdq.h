@@ -720,8 +720,9 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
  * svdq_kv_cache_sizes -- bytes of data and scales. New pages need no values.
  *
  * svdq_kv_append -- k and v [T][heads][D] into the cache. Keys are normed (RMS,
- *   norm [D] or NULL) and rotated as svdq_rope_axes does (pairs 0: not), in fp32,
- *   and rounded once, to their codes. Per block of 16 tokens, head and side: e the
+ *   norm [D] or NULL) and rotated as svdq_rope_axes does (pairs 0: not), in fp64
+ *   (four squares at a time in fp32), and rounded once, to their codes; a key whose mean square
+ *   passes fp32 becomes zeros, as there. Per block of 16 tokens, head and side: e the
  *   least exponent with amax <= 448 * 2^e over the call's finite values, at least
  *   -120, and not below the block's own where the call does not begin it; code =
  *   e4m3(x * 2^-e), nearest even, infinities saturate, NaN stays. Tokens from

@@ -13,6 +13,7 @@ pytestmark = pytest.mark.gpu
 
 import bit_quantized_diffusion_svdq_amd as svdq
 from oracle import kv as okv
+from oracle.fp8 import e4m3_round
 
 
 def both(rng, counts_or_offsets, lengths, hq, H, D, dims, pairing, norm, pos, T):
@@ -89,3 +90,44 @@ def test_positions_in_fp32(counts, before, dims, pairing, norm, D):
     T = sum(counts)
     pos = (rng.standard_normal((T, len(dims))) * np.where(rng.random((T, 1)) < 0.3, 3e5, 40.0)).astype(np.float32)
     both(rng, cum(counts), [a + b for a, b in zip(counts, before)], 4, 2, D, dims, pairing, norm, pos, T)
+
+
+@pytest.mark.parametrize("pairing,norm", [("interleaved", True), ("half", False)])
+def test_keys_are_rounded_once(pairing, norm):
+    """14 million codes against the 64-bit keys'. Angles are 2^-29 off at the most and the root 2^-28, so a
+    key is off by some 2^-28 of itself; a power of two has 8 borders between codes, so a code in 2^24 / 2 may be
+    another: about one of 14 million. (Rounded to 32 bits first, a key within 2^-24 of a border comes to lie on it: 7.)"""
+    note(f"kv codes {pairing} {norm}")
+    rng = np.random.default_rng(77)
+    T, H, D, dims = 4608, 24, 128, (16, 56, 56)
+    cache = svdq.KVCache(T // 64, H, D)
+    k, kv = bf16(rng, (T, H, D))
+    w = torch.from_numpy(1 + 0.2 * rng.standard_normal(D)).bfloat16()
+    pos = rng.integers(0, 4096, (T, 3)).astype(np.int32)
+    cache.append(k.cuda(), k.cuda(), dev(np.arange(T // 64, dtype=np.int32)[None]), dev(np.asarray([T], np.int32)), pos=dev(pos),
+                 plan=svdq.RopePlan(dims, head_dim=D, pairing=pairing), k_norm=w.cuda() if norm else None)
+    keys, _, exps, _ = state_of(cache)
+    x = turned(kv, pos, dims, pairing, w.double().numpy() if norm else None, 1e-6)[0].reshape(T // 64, 64, H, D)
+    e = okv.exponent(np.abs(x).reshape(T // 64, 4, 16, H, D).max(axis=(2, 4)))
+    np.testing.assert_array_equal(exps, e)
+    other = int((keys != e4m3_round(np.ldexp(x, -np.repeat(e, 16, axis=1)[..., None]))).sum())
+    print(f"{other} codes of {keys.size} are others")
+    assert other <= 3
+
+
+@pytest.mark.parametrize("D", [64, 72, 256])
+def test_ties_go_to_even(D):
+    """Keys that lie on a border between codes, with no norm and a rotation by no angle, and beside one."""
+    note(f"kv ties {D}")
+    T, H = 64, 2
+    rng = np.random.default_rng(D)
+    k = torch.from_numpy(np.ldexp(rng.integers(-31, 32, (T, H, D)).astype(np.float64), rng.integers(-12, 3, (T, 1, D)))).bfloat16()
+    k[::16, :, 0] = 448.0                                 # (exponent 0: borders at odd numbers of 2^-4 of a power of two)
+    cache = svdq.KVCache(1, H, D)
+    for more in ({}, dict(pos=torch.zeros(T, 1, dtype=torch.int32, device="cuda"), plan=svdq.RopePlan((D,), head_dim=D))):
+        cache.append(k.cuda(), k.cuda(), dev(np.zeros((1, 1), np.int32)), dev(np.asarray([T], np.int32)), **more)
+        keys, values, ke, ve = state_of(cache)
+        assert (ke == 0).all() and (ve == 0).all()
+        want = e4m3_round(k.double().numpy())
+        np.testing.assert_array_equal(keys[0, :, :, :D], want)
+        np.testing.assert_array_equal(values[0, :, :, :D], want)
