@@ -22,7 +22,7 @@
 // written by its two waves, so nothing is atomic.
 //
 // Bound by memory and, as a block of work is short, its latency: 4608 tokens of 24 + 2 x 24 heads of 128 with
-// norms and three axes take 34 us in a graph (4.2 TB/s), 8003 of 16 + 2 x 4 of 64 15 (3.1).
+// norms and three axes take 32.5 us in a graph (4.4 TB/s), 8003 of 16 + 2 x 4 of 64 15 (3.1).
 #include "fp8.h"
 #include "kv.h"
 #include "rope_body.h"
@@ -460,11 +460,15 @@ hipError_t launch(KvAppendArgs a, RopeArgs q, int half, int cus, hipStream_t str
 
 hipError_t launch_kv_append(KvAppendArgs a, RopeArgs q, int half, int cus, hipStream_t stream) {
     a.items = (int)(a.s.offs ? a.s.T / 16 + 2 * (int64_t)a.s.B : a.s.n > 0 ? (int64_t)a.s.B * ((a.s.n + 14) / 16 + 1) : 0);
-    // Two heads a workgroup; more, which share the angles, while that leaves two workgroups a CU (8003
-    // tokens of 4 heads of 64: 14.9 us with four heads a workgroup, 17.1 with two; 4608 of 24 of 128:
-    // 34.1 with four, 38.9 with all of them, 46.0 with two).
-    a.per = 2;
-    while (a.per < a.c.H && (int64_t)a.items * ((a.c.H + 2 * a.per - 1) / (2 * a.per)) >= 2 * (int64_t)cus) a.per *= 2;
+    // The heads of a block share its angles, and more workgroups share the chip: as few of a block as make
+    // three for each two CUs, with as many heads each, in twos. (Tokens of 24 heads of 128, us with 2 heads a
+    // workgroup, 4, 8, 12, 24, the rule's in brackets: 512 [9.0] 9.7 13.8 18.0 30.3; 1152 14.6 [12.7] 15.6 19.9
+    // 33.2; 2304 26.4 22.5 [20.1] 23.4 35.0; 4608 46.1 39.4 34.3 [32.5] 40.4; 9216 92.3 76.0 66.7 64.8 [62.4]. 2048
+    // of 8 heads 17.9 [16.4] 16.8.)
+    const int64_t blocks = a.s.T / 16 + a.s.B;           // (about: sequences begin and end inside of blocks)
+    int64_t groups = (3 * (int64_t)cus / 2 + blocks - 1) / blocks;
+    if (groups > a.c.H) groups = a.c.H;
+    a.per = (int)((a.c.H + groups - 1) / groups + 1) & ~1;
     a.groups = (a.c.H + a.per - 1) / a.per;
     switch ((a.c.D + 63) / 64) {
         case 1: return launch<1>(a, q, half, cus, stream);
