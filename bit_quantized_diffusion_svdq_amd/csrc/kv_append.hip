@@ -345,7 +345,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a, RopeArgs
             const double var = __builtin_fma(ss, inv_d, (double)a.eps);
             r = (double)__builtin_amdgcn_rsqf((float)var);
             if (r > 0.0) r = __builtin_fma(0.5 * r, __builtin_fma(-var * r, r, 1.0), r);     // (0: an infinite sum)
-            r = knew ? r : 0.0;
+            r = knew && (float)ss != __builtin_inff() ? r : 0.0;         // (past 32 bits: 0, as the queries')
         }
         float x[C][16];
         uint32_t m = 0;                                  // magnitudes, ordered as integers

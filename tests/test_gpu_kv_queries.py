@@ -131,3 +131,24 @@ def test_ties_go_to_even(D):
         want = e4m3_round(k.double().numpy())
         np.testing.assert_array_equal(keys[0, :, :, :D], want)
         np.testing.assert_array_equal(values[0, :, :, :D], want)
+
+
+@pytest.mark.parametrize("D", [64, 200])
+def test_squares_past_fp32(D):
+    """A head whose squares add up past fp32 becomes zeros, of keys as of queries; one just below is normed."""
+    note(f"kv squares past fp32 {D}")
+    T, H = 20, 2
+    x = torch.ones(T, H, D)
+    x[3] = 5e18                                           # (their mean does not pass it)
+    x[7, 1], x[11, 0] = 1e30, 3e38
+    x[5] = (3e38 / D) ** 0.5
+    x = x.bfloat16().cuda()
+    cache = svdq.KVCache(1, H, D)
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    q = cache.append(x, x, dev(np.zeros((1, 1), np.int32)), dev(np.asarray([T], np.int32)), k_norm=w, q=x, q_norm=w)
+    keys, _, e, _ = state_of(cache)
+    keys = np.ldexp(keys[0, :T, :, :D], np.repeat(e[0], 16, axis=0)[:T, :, None])
+    want = np.ones((T, H, D))
+    want[3] = want[7, 1] = want[11, 0] = 0.0
+    np.testing.assert_array_equal(q.double().cpu().numpy(), want)
+    np.testing.assert_array_equal(keys, want)
