@@ -1,5 +1,5 @@
 // svdq_kv_attend for sequences of many query rows (kv_flash.h has the mathematics):
-// the matrix pipe counts. 4608 queries over 23040 keys of 24 heads of 128 take 1100 to 1130 us, 1.15 to
+// the matrix pipe counts. 4608 queries over 23040 keys of 24 heads of 128 take 1100 to 1136 us, 1.15 to
 // 1.19 PFLOP/s where a large bf16 product reaches 1.48; the pipe is 59 % busy, the vector work (an
 // exponential and its share of the rest a score) mostly in its shadow. 32 rows a wave fill the registers, two
 // workgroups of four waves the CU: each key operand read from LDS serves two products, and one

@@ -15,11 +15,14 @@
 //
 // S: one v_mfma_scale_f32_16x16x128_f8f6f4 takes the keys' codes as they lie in
 // memory, their block's exponent as the instruction's scale. The queries' 8
-// significant bits are the sum of two E4M3 numbers of 4 (what the first leaves
-// is exact in the second): two instructions at twice bf16's rate, and no key is
-// ever converted. Q's row exponent is the other scale. (The instruction drops
-// what falls 13 bits below the largest of 8 products: some 1e-4 of a score's
-// larger terms, where P's rounding to bf16 is 2e-3 of a weight.)
+// significant bits are the sum of two E4M3 numbers of 4: two instructions at twice
+// bf16's rate, and no key is ever converted. Q's row exponent is the other scale.
+// What the first number leaves is exact in the second for channels from 1/896 of the
+// row's largest on; E4M3's least step, 2^-9 where that largest is over 224, leaves
+// smaller ones off by up to 2^-10 / 224 of it (2^-17.8; a bf16 product would keep their
+// own 8 bits, in twice the time). The instruction drops what falls 13 bits below the
+// largest of 8 products: at most 9e-4 of a score's larger terms, some 1e-4 as a rule,
+// where P's rounding to bf16 is 2e-3 of a weight.
 // O: bf16 instructions; four values of a lane are two conversions with the
 // block's exponent as scale.
 #pragma once

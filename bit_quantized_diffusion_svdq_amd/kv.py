@@ -121,8 +121,8 @@ class KVCache:
         and head strides multiples of 8, addresses of 16 bytes) into the cache:
         keys through an RMS norm of each head (k_norm [head_dim]) and the
         rotation of ``plan`` at pos [T, axes] (int32 or fp32) where given, then
-        both as E4M3 codes. q [T, heads, head_dim]: its norm and rotation in
-        the same launch, into q_out (q itself, a buffer of any such layout, or a
+        both as E4M3 codes (the keys' norm and rotation in 64 bits, rounded once).
+        q [T, heads, head_dim]: its norm and rotation (as rope_axes') in the same launch, into q_out (q itself, a buffer of any such layout, or a
         new one), which is returned. Tokens of no sequence are neither stored nor
         turned. Nothing is recorded for autograd: k, v and q that require a
         gradient are refused while it is on."""
@@ -194,9 +194,20 @@ class KVCache:
         sequence's length; window 0: from 0. One that sees none gives zeros.
         scale: 1 / sqrt(head_dim) by default. out: q itself or a buffer of any
         such layout; rows of no sequence are left as they are in it and are
-        unspecified in a new one. Nothing is recorded for autograd. The sequences
-        of a call run in one kernel, which the mean of their tokens chooses: single tokens
-        and prompts take less time in a call each."""
+        unspecified in a new one. Nothing is recorded for autograd.
+
+        Scores are summed by the E4M3 matrix instructions, which drop what falls
+        13 bits below the largest of each 8 products (at most 9e-4 of a score's
+        larger terms); query channels below 1/896 of the largest are off by up to
+        2^-17.8 of it; weights are rounded to bf16 before they meet the values,
+        statistics and sums are fp32. Outputs are some 2.1e-3 of their size from
+        the definition's (rms; their own rounding to bf16 is 1.7e-3 of that).
+
+        The sequences of a call run in one kernel, which the mean of their tokens
+        chooses: single tokens and prompts take less time in a call each. Work and
+        workspace are planned for sequences as long as ``table`` is wide: 512
+        queries of 24 heads over 1000 keys take 34 us with a table for 1024
+        tokens, 66 us and 102 MB with one for 131072."""
         D, gpu = self.head_dim, self._gpu
         if q.dim() != 3:
             raise ValueError(f"q must be [T, heads, {D}], got {tuple(q.shape)}")
