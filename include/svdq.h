@@ -739,7 +739,8 @@ svdq_status svdq_rope_axes_grouped(const svdq_rope_heads* q, const svdq_rope_hea
  *   [max(0, p - window + 1), causal ? p + 1 : length), window 0: from 0. One that
  *   sees none gives zeros. Scores are summed by the E4M3 matrix instructions, which
  *   drop what falls 13 bits below the largest of each 8 products; query channels
- *   below 1/896 of the query's largest are off by up to 2^-17.8 of it. Statistics
+ *   below 1/896 of the query's largest are off by up to 2^-17.8 of it (of a query
+ *   below 2^-112, by 2^-130). Statistics
  *   and sums are fp32; weights are rounded to bf16 for the second product; one
  *   rounding of the output. Keys and values that a query does not see never reach
  *   it, whatever they hold. Weights are at most 2^8 before their sum is divided

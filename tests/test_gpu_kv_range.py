@@ -42,18 +42,29 @@ def case(i, D, hidden=False):
 
 
 @pytest.mark.parametrize("i", range(len(SHAPES)))
+@pytest.mark.parametrize("D", [64, 200])
 @pytest.mark.parametrize("up", [27, 28, 60, 105])
-def test_large_scales(i, up):
+def test_large_scales(i, D, up):
     """scale = 2^up over queries as much smaller: the scaled scores are the usual ones, and a query that
     sees nothing gives zeros. (q 2^-105 keeps all bits: a row's exponent is at least -120, its second
     parts' step 2^-129.) The largest scale of all, over queries of zeros, gives the mean."""
-    note(f"kv scale 2^{up} {SHAPES[i]}")
-    state, table, lengths, offs, q, qv, H, causal, window = case(i, 64, hidden=True)
+    note(f"kv scale 2^{up} {SHAPES[i]} {D}")
+    state, table, lengths, offs, q, qv, H, causal, window = case(i, D, hidden=True)
     f = 2.0 ** -up
-    run_attend(cache_of(state, H, 64, 64), state, (q.double() * f).bfloat16().cuda(), qv * f, table, lengths, offs, causal, window,
+    run_attend(cache_of(state, H, D, 64), state, (q.double() * f).bfloat16().cuda(), qv * f, table, lengths, offs, causal, window,
                scale=2.0 ** up / 8)
-    run_attend(cache_of(state, H, 64, 64), state, torch.zeros_like(q).cuda(), 0 * qv, table, lengths, offs, causal, window,
+    run_attend(cache_of(state, H, D, 64), state, torch.zeros_like(q).cuda(), 0 * qv, table, lengths, offs, causal, window,
                scale=2.0 ** 127 / 1.5)
+
+
+@pytest.mark.parametrize("i", range(len(SHAPES)))
+@pytest.mark.parametrize("D", [64, 200])
+@pytest.mark.parametrize("scale", [2.0 ** -149, 2.0 ** -126, 1e-30])
+def test_least_scales(i, D, scale):
+    """Weights are all alike, and what is hidden has none."""
+    note(f"kv scale {scale} {SHAPES[i]} {D}")
+    state, table, lengths, offs, q, qv, H, causal, window = case(i, D, hidden=True)
+    run_attend(cache_of(state, H, D, 64), state, q.cuda(), qv, table, lengths, offs, causal, window, scale=scale)
 
 
 @pytest.mark.parametrize("i", range(len(SHAPES)))
@@ -125,16 +136,17 @@ def test_values_near_the_largest(i):
 
 
 @pytest.mark.parametrize("i", range(len(SHAPES)))
-def test_large_values_under_large_weights(i):
+@pytest.mark.parametrize("D", [64, 200])
+def test_large_values_under_large_weights(i, D):
     """Weights are taken from a reference up to 2^8 below the largest, and values of 2^120 are read under them."""
-    note(f"kv large values {SHAPES[i]}")
-    state, table, lengths, offs, q, qv, H, causal, window = case(i, 64)
+    note(f"kv large values {SHAPES[i]} {D}")
+    state, table, lengths, offs, q, qv, H, causal, window = case(i, D)
     state[3] = state[3] + 121
-    run_attend(cache_of(state, H, 64, 64), state, q.cuda(), qv, table, lengths, offs, causal, window)
+    run_attend(cache_of(state, H, D, 64), state, q.cuda(), qv, table, lengths, offs, causal, window)
     # the least exponents: bf16's own step is 2^-133, that of a 64th of the values
     state[3] = np.maximum(state[3] - 121 - 113, okv.EXP_MIN)
     y, mag, rss, peak = okv.attend(state, qv, table, lengths, offs, causal, window)
-    got = cache_of(state, H, 64, 64).attend(q.cuda(), dev(table), dev(np.asarray(lengths, np.int32)), dev(offs), causal=causal,
+    got = cache_of(state, H, D, 64).attend(q.cuda(), dev(table), dev(np.asarray(lengths, np.int32)), dev(offs), causal=causal,
                                             window=window).double().cpu().numpy()
     assert (np.abs(got - y) <= attend_bound(y, mag, rss, peak) - 1e-30 + 2.0 ** -127).all()
 
